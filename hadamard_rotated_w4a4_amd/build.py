@@ -15,8 +15,9 @@ LIB = os.path.join(PKG, "libw4a4.so")
 CEILINGS_LIB = os.path.join(PKG, "libw4a4_ceilings.so")  # measured ceilings for the benchmark
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
-SOURCES = [os.path.join(CSRC, "w4a4.hip")]
-HEADERS = [os.path.join(CSRC, h) for h in ("common.h", "k_prep.h", "k_rotq.h", "k_route.h", "k_dense.h", "k_smallm.h", "k_grouped.h", "k_w16.h")] + [
+SOURCES = [os.path.join(CSRC, f) for f in ("w4a4.hip", "rows.hip", "mx4.hip")]
+HEADERS = [os.path.join(CSRC, h) for h in ("abi.h", "common.h", "k_prep.h", "k_rotq.h", "k_route.h", "k_dense.h", "k_smallm.h", "k_grouped.h", "k_w16.h",
+                                            "k_rows.h", "k_mx4.h")] + [
     os.path.join(ROOT, "include", "w4a4.h")]
 
 FLAGS = [

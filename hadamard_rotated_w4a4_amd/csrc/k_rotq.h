@@ -116,21 +116,13 @@ __device__ __forceinline__ void fwht32_quad(float v[8], int L) {
     }
 }
 
-// One (row, block) of the quantiser, held by a quad of lanes (lane L of the
-// quad: elements 8L .. 8L + 7 at src): the butterflies (unless ROTATE is
-// false), the absmax, the scale s and this lane's 8 codes.  live: the row
-// and block exist (uniform per quad; a dead quad quantises zeros).  Every
-// lane of the quad must take part (the butterflies and the absmax exchange
-// values through quad permutes).
-template <typename T, int QMAX, bool ROTATE>
-__device__ __forceinline__ void quantise_quad(const T *src, int mode, bool live, int L, int q[8], float &s) {
-    float v[8];
-    if (live) {
-        load8(src, mode, v);
-    } else {
-#pragma unroll
-        for (int t = 0; t < 8; t++) v[t] = 0.0f;
-    }
+// The values of one (row, block), held by a quad of lanes (lane L of the quad:
+// elements 8L .. 8L + 7 in v), quantised: the butterflies (unless ROTATE is
+// false), the absmax, the scale s and this lane's 8 codes.  Every lane of the
+// quad must take part (the butterflies and the absmax exchange values through
+// quad permutes).
+template <int QMAX, bool ROTATE>
+__device__ __forceinline__ void quantise_values(float v[8], int L, int q[8], float &s) {
     if constexpr (ROTATE) fwht32_quad(v, L);
 
     float amax = 0.0f;
@@ -146,6 +138,21 @@ __device__ __forceinline__ void quantise_quad(const T *src, int mode, bool live,
 #pragma unroll
     for (int t = 0; t < 8; t++)
         q[t] = nonzero ? (int)fminf((float)QMAX, fmaxf(-(float)QMAX, round_half_away(__fmul_rn(v[t], id)))) : 0;
+}
+
+// quantise_values of a block in memory (lane L's elements 8L .. 8L + 7 at
+// src).  live: the row and block exist (uniform per quad; a dead quad
+// quantises zeros).
+template <typename T, int QMAX, bool ROTATE>
+__device__ __forceinline__ void quantise_quad(const T *src, int mode, bool live, int L, int q[8], float &s) {
+    float v[8];
+    if (live) {
+        load8(src, mode, v);
+    } else {
+#pragma unroll
+        for (int t = 0; t < 8; t++) v[t] = 0.0f;
+    }
+    quantise_values<QMAX, ROTATE>(v, L, q, s);
 }
 
 // The public int4 codes of a block (byte j = code j | code j + 16 << 4) from
@@ -197,6 +204,60 @@ __device__ __forceinline__ void put_quad_row(const uint32_t f[8], int L, uint8_t
     }
 }
 
+// What the quantiser writes for one (row, block) from its quad: the public
+// codes and scale (rows below m, blocks below k / 32), and the operand records
+// in act or sma (layouts in common.h), padding rows and blocks included.
+template <int QMAX>
+__device__ __forceinline__ void store_quantised(const int q[8], float s, int L, int64_t row, int64_t b, int64_t m,
+                                                int64_t k, uint8_t *__restrict__ codes, float *__restrict__ scales,
+                                                uint8_t *__restrict__ act, uint8_t *__restrict__ sma) {
+    const int64_t nb = k / QK, tile = row >> 5;
+    const int r = (int)(row & 31);  // row within the tile
+    const bool live = row < m && b < nb;  // uniform per quad
+    if constexpr (QMAX == 127) {  // int8 codes: lane L writes elements 8L .. 8L + 7
+        if (live) {
+            uint32_t w0 = 0, w1 = 0;
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                w0 |= (uint32_t)(q[i] & 0xFF) << (8 * i);
+                w1 |= (uint32_t)(q[4 + i] & 0xFF) << (8 * i);
+            }
+            *reinterpret_cast<uint2 *>(codes + row * k + b * QK + 8 * L) = make_uint2(w0, w1);
+            if (L == 0) scales[row * nb + b] = s;
+        }
+        if (act && b < mx_blocks(k)) {
+            uint32_t fh[8], fl[8];
+#pragma unroll
+            for (int t = 0; t < 8; t++) {
+                const int h = (q[t] + 8) >> 4;  // floor: h in [-8, 8], q - 16 h in [-8, 7]
+                fh[t] = fp6_e2m3_of(h);
+                fl[t] = fp6_e2m3_of(q[t] - 16 * h);
+            }
+            uint8_t *rec = act + (tile * 2 * mx_blocks(k) + b) * MX_REC;
+            put_quad_row(fh, L, rec, r, act_scale_operand(s));
+            put_quad_row(fl, L, rec + mx_blocks(k) * MX_REC, r, make_uint2(0, 0));
+        }
+        return;
+    }
+
+    if (codes) store_codes4(q, s, L, live, codes + row * (k / 2) + b * 16, scales + row * nb + b);
+
+    if (sma && row < SMA_ROWS && b < sq_quads(k) * SQ_BLOCKS) {  // uniform per quad
+        const int64_t qd = b / SQ_BLOCKS;
+        const int j = (int)(b % SQ_BLOCKS);
+        store_codes4(q, s, L, true, sma + qd * SMA_CODE_BYTES + row * 64 + j * 16,
+                     reinterpret_cast<float *>(sma + sq_quads(k) * SMA_CODE_BYTES + qd * SMA_SCALE_BYTES +
+                                               row * 16 + j * 4));
+    }
+
+    if (act && b < mx_blocks(k)) {  // the operand record of (row tile, block)
+        uint32_t f[8];
+#pragma unroll
+        for (int t = 0; t < 8; t++) f[t] = fp6_e2m3_of(q[t]);
+        put_quad_row(f, L, act + (tile * mx_blocks(k) + b) * MX_REC, r, act_scale_operand(s));
+    }
+}
+
 // One workgroup = 32 rows (row tile blockIdx.y) x 2 neighbouring blocks
 // (2 blockIdx.x and 2 blockIdx.x + 1), four lanes per (row, block): wave w
 // takes block w / 2 and rows 16 (w % 2) .. + 15, lane 4 i + L row i, elements
@@ -236,48 +297,7 @@ __global__ __launch_bounds__(128 * RQ_BLOCKS) void rotate_quantize_kernel(const 
     float s;
     quantise_quad<T, QMAX, ROTATE>(x + row * ldx + b * QK + 8 * L, mode, live, L, q, s);
 
-    if constexpr (QMAX == 127) {  // int8 codes: lane L writes elements 8L .. 8L + 7
-        if (live) {
-            uint32_t w0 = 0, w1 = 0;
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                w0 |= (uint32_t)(q[i] & 0xFF) << (8 * i);
-                w1 |= (uint32_t)(q[4 + i] & 0xFF) << (8 * i);
-            }
-            *reinterpret_cast<uint2 *>(codes + row * k + b * QK + 8 * L) = make_uint2(w0, w1);
-            if (L == 0) scales[row * nb + b] = s;
-        }
-        if (act && b < mx_blocks(k)) {
-            uint32_t fh[8], fl[8];
-#pragma unroll
-            for (int t = 0; t < 8; t++) {
-                const int h = (q[t] + 8) >> 4;  // floor: h in [-8, 8], q - 16 h in [-8, 7]
-                fh[t] = fp6_e2m3_of(h);
-                fl[t] = fp6_e2m3_of(q[t] - 16 * h);
-            }
-            uint8_t *rec = act + ((int64_t)blockIdx.y * 2 * mx_blocks(k) + b) * MX_REC;
-            put_quad_row(fh, L, rec, r, act_scale_operand(s));
-            put_quad_row(fl, L, rec + mx_blocks(k) * MX_REC, r, make_uint2(0, 0));
-        }
-        return;
-    }
-
-    if (codes) store_codes4(q, s, L, live, codes + row * (k / 2) + b * 16, scales + row * nb + b);
-
-    if (sma && row < SMA_ROWS && b < sq_quads(k) * SQ_BLOCKS) {  // uniform per quad
-        const int64_t qd = b / SQ_BLOCKS;
-        const int j = (int)(b % SQ_BLOCKS);
-        store_codes4(q, s, L, true, sma + qd * SMA_CODE_BYTES + row * 64 + j * 16,
-                     reinterpret_cast<float *>(sma + sq_quads(k) * SMA_CODE_BYTES + qd * SMA_SCALE_BYTES +
-                                               row * 16 + j * 4));
-    }
-
-    if (act && b < mx_blocks(k)) {  // the operand record of (row tile, block)
-        uint32_t f[8];
-#pragma unroll
-        for (int t = 0; t < 8; t++) f[t] = fp6_e2m3_of(q[t]);
-        put_quad_row(f, L, act + ((int64_t)blockIdx.y * mx_blocks(k) + b) * MX_REC, r, act_scale_operand(s));
-    }
+    store_quantised<QMAX>(q, s, L, row, b, m, k, codes, scales, act, sma);
 }
 
 }  // namespace w4a4

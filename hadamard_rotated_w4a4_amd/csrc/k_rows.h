@@ -1,0 +1,466 @@
+// Producers of quantised activation rows, and the rows read back.
+//
+// Every product here reads rows of 32-element blocks in one of these formats
+// (w4a4_act_format): int4 or int8 codes of the rotated block with one fp32
+// scale, or MXFP4 (the OCP Microscaling format: FP4 E2M1 codes with one E8M0
+// power-of-two scale), rotated or not.  The kernels below write them straight
+// from what makes the rows: a residual addition and RMS norm, a gated
+// activation, or a plain matrix (MXFP4; k_rotq.h has the int4 and int8 forms).
+//
+// Codes depend on every rounding before them, so each is defined by a fixed
+// sequence of roundings.  Where an exact value is an unordered sum (the row's
+// sum of squares) or a transcendental function (the gated activation), it is
+// evaluated in fp64, to within 2^-40, and rounded once to fp32: the codes do
+// not depend on the launch shape.  fp64 multiply-adds issue at the fp32 rate on
+// this part, and both kernels are bound by memory.
+//
+// A block is held by a quad of lanes (lane L: elements 8L .. 8L + 7), as in
+// the quantiser.
+#pragma once
+
+#include "common.h"
+#include "k_rotq.h"
+
+namespace w4a4 {
+
+constexpr int ROW_F32 = 0, ROW_F16 = 1, ROW_BF16 = 2;  // w4a4_dtype
+constexpr int FMT_INT4 = 0, FMT_INT4_SMALL = 1, FMT_INT8 = 2, FMT_MX4 = 3, FMT_MX4_H32 = 4;  // w4a4_act_format
+
+// MXFP4 rows: scale bytes per row (whole groups of 8 blocks: 256 elements of
+// K; the bytes past k / 32 are written as 127 and never read as scales).
+constexpr int MX4_GROUP = 8;
+__host__ __device__ inline int64_t mx4_stride(int64_t k) { return (k / QK + MX4_GROUP - 1) / MX4_GROUP * MX4_GROUP; }
+
+struct RowsOut {
+    uint8_t *codes;
+    void *scales;
+    uint8_t *act;  // operand records (int4, int8), the record-ordered operand (int4_small), or null
+    int64_t m, k;
+};
+
+// Eight elements of type dt at byte address p as fp32.  vec: 16-byte aligned.
+__device__ __forceinline__ void load_row8(const uint8_t *p, int dt, bool vec, float v[8]) {
+    if (dt == ROW_F32) {
+        load8(reinterpret_cast<const float *>(p), vec ? 2 : 0, v);
+    } else if (dt == ROW_F16) {
+        load8(reinterpret_cast<const __half *>(p), vec ? 2 : 0, v);
+    } else {
+        uint32_t w[4];
+        if (vec) {
+            const uint4 u = *reinterpret_cast<const uint4 *>(p);
+            w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+        } else {
+            const uint16_t *h = reinterpret_cast<const uint16_t *>(p);
+#pragma unroll
+            for (int i = 0; i < 4; i++) w[i] = (uint32_t)h[2 * i] | (uint32_t)h[2 * i + 1] << 16;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    }
+}
+
+// fp32 -> 16-bit types, to nearest even.
+__device__ __forceinline__ uint16_t f16_bits(float x) { return __half_as_ushort(__float2half_rn(x)); }
+__device__ __forceinline__ uint16_t bf16_bits(float x) { return __builtin_bit_cast(uint16_t, static_cast<__bf16>(x)); }
+
+// v rounded to type dt.
+__device__ __forceinline__ void round_row8(int dt, float v[8]) {
+    if (dt == ROW_F16) {
+#pragma unroll
+        for (int i = 0; i < 8; i++) v[i] = __half2float(__ushort_as_half(f16_bits(v[i])));
+    } else if (dt == ROW_BF16) {
+#pragma unroll
+        for (int i = 0; i < 8; i++) v[i] = __uint_as_float((uint32_t)bf16_bits(v[i]) << 16);
+    }
+}
+
+// Eight values rounded to type dt at byte address p.  vec: 16-byte aligned.
+__device__ __forceinline__ void store_row8(uint8_t *p, int dt, bool vec, const float v[8]) {
+    if (dt == ROW_F32) {
+        float *f = reinterpret_cast<float *>(p);
+        if (vec) {
+            reinterpret_cast<float4 *>(f)[0] = make_float4(v[0], v[1], v[2], v[3]);
+            reinterpret_cast<float4 *>(f)[1] = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; i++) f[i] = v[i];
+        }
+        return;
+    }
+    uint16_t h[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) h[i] = dt == ROW_F16 ? f16_bits(v[i]) : bf16_bits(v[i]);
+    if (vec) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) w[i] = (uint32_t)h[2 * i] | (uint32_t)h[2 * i + 1] << 16;
+        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++) reinterpret_cast<uint16_t *>(p)[i] = h[i];
+    }
+}
+
+// One block as MXFP4: e = floor(log2 max|v|) - 2 (at least -127), the codes
+// E2M1(v 2^-e) to nearest even, magnitudes of 6 and more saturating at 6, the
+// scale byte e + 127.  A block that holds an infinity or NaN gets byte 255
+// (the format's NaN) and zero codes; a zero block byte 0.  Returns this lane's
+// eight codes, element 8L + i in bits 4i .. 4i + 3.
+__device__ __forceinline__ uint32_t mx4_quantise(const float v[8], uint32_t &byte) {
+    uint32_t top = 0;  // |v| as integers: the same order, NaN and infinity on top
+#pragma unroll
+    for (int t = 0; t < 8; t++) top = max(top, __float_as_uint(v[t]) & 0x7FFFFFFFu);
+    top = max(top, quad_u32<QP_XOR1>(top));
+    top = max(top, quad_u32<QP_XOR2>(top));
+    const int E = (int)(top >> 23);  // biased exponent; 0 for subnormals
+    byte = E == 255 ? 255u : (uint32_t)max(E - 2, 0);
+    const int sh = 127 - (int)byte;
+    float u[8];
+#pragma unroll
+    for (int t = 0; t < 8; t++)  // exact (the scale is a power of two); in (-8, 8) before the clamp
+        u[t] = __builtin_amdgcn_fmed3f(ldexpf(v[t], sh), -6.0f, 6.0f);
+    uint32_t c = 0;
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, u[0], u[1], 1.0f, 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, u[2], u[3], 1.0f, 1);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, u[4], u[5], 1.0f, 2);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, u[6], u[7], 1.0f, 3);
+    return E == 255 ? 0u : c;
+}
+
+// The values v of one (row, block), held by a quad, quantised and written in
+// format FMT: public codes and scales for rows below m and blocks below k / 32,
+// padding scale bytes (MXFP4) and operand records as the format has them.
+// Every lane of the quad must take part.
+template <int FMT>
+__device__ __forceinline__ void emit_block(float v[8], int L, int64_t row, int64_t b, const RowsOut &o) {
+    if constexpr (FMT == FMT_MX4 || FMT == FMT_MX4_H32) {
+        if constexpr (FMT == FMT_MX4_H32) {
+            fwht32_quad(v, L);
+#pragma unroll
+            for (int t = 0; t < 8; t++) v[t] = __fmul_rn(v[t], kInvSqrt32f);
+        }
+        uint32_t byte;
+        const uint32_t c = mx4_quantise(v, byte);
+        if (row < o.m) {
+            const bool live = b < o.k / QK;
+            if (live) reinterpret_cast<uint32_t *>(o.codes + row * (o.k / 2) + b * 16)[L] = c;
+            if (L == 0 && b < mx4_stride(o.k))
+                static_cast<uint8_t *>(o.scales)[row * mx4_stride(o.k) + b] = (uint8_t)(live ? byte : 127u);
+        }
+    } else {
+        constexpr int QMAX = FMT == FMT_INT8 ? 127 : 7;
+        int q[8];
+        float s;
+        quantise_values<QMAX, true>(v, L, q, s);
+        store_quantised<QMAX>(q, s, L, row, b, o.m, o.k, o.codes, static_cast<float *>(o.scales),
+                              FMT == FMT_INT4_SMALL ? nullptr : o.act, FMT == FMT_INT4_SMALL ? o.act : nullptr);
+    }
+}
+
+// Rows and blocks that a format's outputs cover, padding included.
+__host__ __device__ inline int64_t rows_covered(int fmt, bool act, int64_t m) {
+    return !act ? m : fmt == FMT_INT4_SMALL ? SMA_ROWS : (m + 31) / 32 * 32;
+}
+__host__ __device__ inline int64_t blocks_covered(int fmt, bool act, int64_t k) {
+    if (fmt == FMT_MX4 || fmt == FMT_MX4_H32) return mx4_stride(k);
+    return !act ? k / QK : fmt == FMT_INT4_SMALL ? sq_quads(k) * SQ_BLOCKS : mx_blocks(k);
+}
+
+// Which (row, block) a quad of the element-wise kernels takes.  TILED (outputs
+// with operand records): as the quantiser, a workgroup covers 32 rows x 2
+// blocks, so that the records are written in runs.  Otherwise consecutive
+// quads take consecutive blocks of a row: every load and store is contiguous.
+constexpr int ROWS_THREADS = 256;
+template <bool TILED>
+__device__ __forceinline__ void block_of_quad(int64_t blocks, int64_t &row, int64_t &b) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    if constexpr (TILED) {
+        b = (int64_t)blockIdx.x * RQ_BLOCKS + (wave >> 1);
+        row = (int64_t)blockIdx.y * 32 + (wave & 1) * 16 + (lane >> 2);
+    } else {
+        const uint32_t i = blockIdx.x * (ROWS_THREADS / 4) + (tid >> 2);  // below 2^30 (the launch is below 2^32 threads)
+        row = i / (uint32_t)blocks;
+        b = i - (uint32_t)row * (uint32_t)blocks;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Plain rows to MXFP4.
+// ---------------------------------------------------------------------------
+struct PlainArgs {
+    const uint8_t *x;
+    int64_t ld;  // elements
+    int dt;
+    bool vec;
+    RowsOut out;
+};
+template <int FMT>
+__global__ __launch_bounds__(ROWS_THREADS) void quantise_rows_kernel(PlainArgs a) {
+    int64_t row, b;
+    block_of_quad<false>(mx4_stride(a.out.k), row, b);
+    const int L = threadIdx.x & 3;
+    float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    if (row < a.out.m && b < a.out.k / QK)
+        load_row8(a.x + (row * a.ld + b * QK + 8 * L) * (a.dt == ROW_F32 ? 4 : 2), a.dt, a.vec, v);
+    emit_block<FMT>(v, L, row, b, a.out);
+}
+
+// ---------------------------------------------------------------------------
+// Gated activation: v = fl32(act(g) u), act in fp64.
+// ---------------------------------------------------------------------------
+constexpr int GLU_SILU = 0, GLU_GELU_TANH = 1;  // w4a4_glu_act
+
+// 1 / (1 + e^-z) to within 2^-40 relative: z is reduced to n ln 2 + r with
+// |r| <= ln 2 / 2 (ln 2 in two parts), e^r is its Taylor sum to r^11 / 11!
+// (the next term is below 2^-47), the quotient two Newton steps from the
+// hardware reciprocal.  Arguments past +-700 are clamped: e^700 is finite in
+// fp64 and the result rounds to 0 or 1 in fp32 either way.
+__device__ __forceinline__ double sigmoid64(double z) {
+    const double t = fmin(fmax(-z, -700.0), 700.0);
+    const double n = rint(t * 1.4426950408889634);
+    double r = fma(n, -0x1.62e42fefa38p-1, t);         // ln 2, leading 42 bits: n times it is exact
+    r = fma(n, -0x1.ef35793c7673p-45, r);              // ln 2 minus those
+    double p = 1.0 / 39916800.0;
+    p = fma(p, r, 1.0 / 3628800.0);
+    p = fma(p, r, 1.0 / 362880.0);
+    p = fma(p, r, 1.0 / 40320.0);
+    p = fma(p, r, 1.0 / 5040.0);
+    p = fma(p, r, 1.0 / 720.0);
+    p = fma(p, r, 1.0 / 120.0);
+    p = fma(p, r, 1.0 / 24.0);
+    p = fma(p, r, 1.0 / 6.0);
+    p = fma(p, r, 0.5);
+    p = fma(p, r, 1.0);
+    p = fma(p, r, 1.0);
+    const double d = 1.0 + ldexp(p, (int)n);
+    double q = __builtin_amdgcn_rcp(d);
+    q = fma(fma(-d, q, 1.0), q, q);
+    return fma(fma(-d, q, 1.0), q, q);
+}
+// act(g) u: silu(g) = g s(g); the tanh form of gelu, g (1 + tanh w) / 2 with
+// w = sqrt(2 / pi) (g + 0.044715 g^3), is g s(2 w).  One rounding, to fp32.
+__device__ __forceinline__ float gated(float gate, float up, int act) {
+    const double g = gate;
+    double z = g;
+    if (act == GLU_GELU_TANH) z = 1.5957691216057308 * (g + 0.044715 * g * g * g);
+    return (float)(g * sigmoid64(z) * (double)up);
+}
+
+struct GluArgs {
+    const uint8_t *gate, *up;
+    int64_t ldg, ldu;  // elements
+    int dt, act;
+    bool vecg, vecu;
+    RowsOut out;
+};
+template <int FMT, bool TILED>
+__global__ __launch_bounds__(ROWS_THREADS) void glu_rows_kernel(GluArgs a) {
+    int64_t row, b;
+    block_of_quad<TILED>(blocks_covered(FMT, TILED, a.out.k), row, b);
+    const int L = threadIdx.x & 3, esz = a.dt == ROW_F32 ? 4 : 2;
+    float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    if (row < a.out.m && b < a.out.k / QK) {
+        float g[8], u[8];
+        load_row8(a.gate + (row * a.ldg + b * QK + 8 * L) * esz, a.dt, a.vecg, g);
+        load_row8(a.up + (row * a.ldu + b * QK + 8 * L) * esz, a.dt, a.vecu, u);
+#pragma unroll
+        for (int t = 0; t < 8; t++) v[t] = gated(g[t], u[t], a.act);
+    }
+    emit_block<FMT>(v, L, row, b, a.out);
+}
+
+// ---------------------------------------------------------------------------
+// Residual addition + RMS norm: h = r(x + residual), the sum of h^2 in fp64
+// (each square exact), rstd = fl32((sum / k + eps)^(-1/2)), v = fl32(fl32(h
+// rstd) weight).
+//
+// One workgroup per row: its threads hold the row in registers, CHUNKS pieces
+// of 8 elements each, between the sum and the quantising; CHUNKS = 0 walks a
+// longer row twice, reading h (or the inputs, when h is not written) again.
+// With operand records, the 32 rows of a tile go to workgroups of one XCD
+// (they are dealt round-robin), whose L2 joins their 8-byte pieces of a record
+// to whole lines.
+// ---------------------------------------------------------------------------
+struct NormArgs {
+    const uint8_t *x, *residual;  // residual may be null
+    const float *weight;          // may be null: ones
+    uint8_t *h;                   // may be null, or x or residual itself
+    int64_t ldx, ldr, ldh;        // elements
+    double eps;
+    int xdt, rdt;
+    bool vecx, vecr, vech, vecw;
+    RowsOut out;
+};
+
+// Sum over the wave, in a fixed order, in every lane: DPP shifts within rows
+// of 16 lanes and two row broadcasts bring it to lane 63.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_f64(double x) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xF, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROWS, 0xF, false);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double wave_sum(double x) {
+    x += dpp_f64<0x111, 0xF>(x);  // row_shr:1
+    x += dpp_f64<0x112, 0xF>(x);  // row_shr:2
+    x += dpp_f64<0x114, 0xF>(x);  // row_shr:4
+    x += dpp_f64<0x118, 0xF>(x);  // row_shr:8: lane 15 of each row holds the row's sum
+    x += dpp_f64<0x142, 0xA>(x);  // row_bcast:15 into rows 1 and 3
+    x += dpp_f64<0x143, 0xC>(x);  // row_bcast:31 into rows 2 and 3
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, 63);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), 63);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// This lane's 8 elements of h at column c of the row.
+__device__ __forceinline__ void norm_h8(const NormArgs &a, int64_t row, int64_t c, float v[8]) {
+    load_row8(a.x + (row * a.ldx + c) * (a.xdt == ROW_F32 ? 4 : 2), a.xdt, a.vecx, v);
+    if (a.residual) {
+        float r[8];
+        load_row8(a.residual + (row * a.ldr + c) * (a.rdt == ROW_F32 ? 4 : 2), a.rdt, a.vecr, r);
+#pragma unroll
+        for (int t = 0; t < 8; t++) v[t] = __fadd_rn(v[t], r[t]);
+    }
+    round_row8(a.rdt, v);
+}
+__device__ __forceinline__ void norm_scale8(const NormArgs &a, int64_t c, float rstd, float v[8]) {
+    float w[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
+    if (a.weight) load8(a.weight + c, a.vecw ? 2 : 0, w);
+#pragma unroll
+    for (int t = 0; t < 8; t++) v[t] = __fmul_rn(__fmul_rn(v[t], rstd), w[t]);
+}
+
+template <int FMT, int CHUNKS>
+__global__ __launch_bounds__(1024) void norm_rows_kernel(NormArgs a, bool act) {
+    __shared__ double part[16];
+    const int tid = threadIdx.x, L = tid & 3, quads = blockDim.x / 4, waves = blockDim.x / 64;
+    const int64_t k = a.out.k, nb = k / QK, blocks = blocks_covered(FMT, act, k);
+    int64_t row = blockIdx.x;
+    if (act && FMT != FMT_INT4_SMALL) {
+        const int64_t tiles = gridDim.x / 32, group = row / 256, in = row % 256;
+        const int64_t width = min((int64_t)8, tiles - group * 8);
+        row = (group * 8 + in % width) * 32 + in / width;
+    }
+    const bool live = row < a.out.m;
+
+    float v[CHUNKS ? CHUNKS : 1][8];
+    double sum = 0.0;
+    if (live) {
+        if constexpr (CHUNKS > 0) {
+#pragma unroll
+            for (int i = 0; i < CHUNKS; i++) {
+                const int64_t b = i * quads + (tid >> 2);
+                if (b < nb) norm_h8(a, row, b * QK + 8 * L, v[i]);
+                else
+#pragma unroll
+                    for (int t = 0; t < 8; t++) v[i][t] = 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < CHUNKS; i++) {
+                const int64_t b = i * quads + (tid >> 2);
+                if (a.h && b < nb)
+                    store_row8(a.h + (row * a.ldh + b * QK + 8 * L) * (a.rdt == ROW_F32 ? 4 : 2), a.rdt, a.vech, v[i]);
+#pragma unroll
+                for (int t = 0; t < 8; t++) sum = fma((double)v[i][t], (double)v[i][t], sum);
+            }
+        } else {
+            for (int64_t b = tid >> 2; b < nb; b += quads) {
+                norm_h8(a, row, b * QK + 8 * L, v[0]);
+                if (a.h) store_row8(a.h + (row * a.ldh + b * QK + 8 * L) * (a.rdt == ROW_F32 ? 4 : 2), a.rdt, a.vech, v[0]);
+#pragma unroll
+                for (int t = 0; t < 8; t++) sum = fma((double)v[0][t], (double)v[0][t], sum);
+            }
+        }
+    }
+    sum = wave_sum(sum);
+    if ((tid & 63) == 0) part[tid >> 6] = sum;
+    __syncthreads();
+    sum = part[0];
+    for (int w = 1; w < waves; w++) sum += part[w];
+    const float rstd = (float)(1.0 / sqrt(sum / (double)k + a.eps));
+
+    if constexpr (CHUNKS > 0) {
+#pragma unroll
+        for (int i = 0; i < CHUNKS; i++) {
+            const int64_t b = i * quads + (tid >> 2);
+            if (b >= blocks) continue;  // uniform per quad
+            if (live && b < nb) {
+                norm_scale8(a, b * QK + 8 * L, rstd, v[i]);
+            } else {
+#pragma unroll
+                for (int t = 0; t < 8; t++) v[i][t] = 0.0f;
+            }
+            emit_block<FMT>(v[i], L, row, b, a.out);
+        }
+    } else {
+        for (int64_t b = tid >> 2; b < blocks; b += quads) {
+            if (live && b < nb) {
+                const int64_t c = b * QK + 8 * L;
+                // this thread's own stores above, when h is written (it may be x or residual itself)
+                if (a.h) load_row8(a.h + (row * a.ldh + c) * (a.rdt == ROW_F32 ? 4 : 2), a.rdt, a.vech, v[0]);
+                else norm_h8(a, row, c, v[0]);
+                norm_scale8(a, c, rstd, v[0]);
+            } else {
+#pragma unroll
+                for (int t = 0; t < 8; t++) v[0][t] = 0.0f;
+            }
+            emit_block<FMT>(v[0], L, row, b, a.out);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Quantised rows read back: y = fl(q s) in type dt (MXFP4 values are exact in
+// fp32 and bf16; a block whose scale byte is 255 reads as NaN).
+// ---------------------------------------------------------------------------
+struct ReadArgs {
+    const uint8_t *codes;
+    const void *scales;
+    uint8_t *y;
+    int64_t m, k, ld;  // ld: elements
+    int dt;
+    bool vec;
+};
+template <int FMT>
+__global__ __launch_bounds__(ROWS_THREADS) void read_rows_kernel(ReadArgs a) {
+    const int64_t nb = a.k / QK;
+    int64_t row, b;
+    block_of_quad<false>(nb, row, b);
+    if (row >= a.m) return;
+    const int L = threadIdx.x & 3;
+    float v[8];
+    if constexpr (FMT == FMT_MX4 || FMT == FMT_MX4_H32) {
+        const uint32_t c = reinterpret_cast<const uint32_t *>(a.codes + row * (a.k / 2) + b * 16)[L];
+        const int byte = static_cast<const uint8_t *>(a.scales)[row * mx4_stride(a.k) + b];
+#pragma unroll
+        for (int t = 0; t < 8; t++) {
+            const uint32_t q = c >> (4 * t) & 15u;
+            const float twice = (float)(0xC8643210u >> (4 * (q & 7u)) & 15u);  // 2 |E2M1|: 0 1 2 3 4 6 8 12
+            const float x = ldexpf(q & 8u ? -twice : twice, byte - 128);
+            v[t] = byte == 255 ? __uint_as_float(0x7FC00000u) : x;
+        }
+    } else {
+        const float s = static_cast<const float *>(a.scales)[row * nb + b];
+        if constexpr (FMT == FMT_INT8) {
+            const uint2 w = *reinterpret_cast<const uint2 *>(a.codes + row * a.k + b * QK + 8 * L);
+#pragma unroll
+            for (int t = 0; t < 8; t++) v[t] = __fmul_rn((float)(int8_t)((t < 4 ? w.x : w.y) >> (8 * (t & 3))), s);
+        } else {  // byte j: element j low, element j + 16 high
+            const uint2 w = *reinterpret_cast<const uint2 *>(a.codes + row * (a.k / 2) + b * 16 + 8 * (L & 1));
+            const int up = L < 2 ? 4 : 0;  // bring the nibble to the top of its byte
+#pragma unroll
+            for (int t = 0; t < 8; t++) {
+                const uint32_t byte = (t < 4 ? w.x : w.y) >> (8 * (t & 3)) & 255u;
+                v[t] = __fmul_rn((float)((int8_t)(byte << up) >> 4), s);
+            }
+        }
+    }
+    store_row8(a.y + (row * a.ld + b * QK + 8 * L) * (a.dt == ROW_F32 ? 4 : 2), a.dt, a.vec, v);
+}
+
+}  // namespace w4a4

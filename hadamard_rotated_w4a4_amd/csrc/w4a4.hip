@@ -12,6 +12,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "abi.h"
 #include "common.h"
 #include "k_dense.h"
 #include "k_grouped.h"
@@ -25,19 +26,6 @@ using namespace w4a4;
 
 namespace {
 
-thread_local char g_last_hip_error[256] = "";
-
-w4a4_status hip_status(const char *what) {
-    const hipError_t err = hipGetLastError();
-    if (err == hipSuccess) return W4A4_OK;
-    std::snprintf(g_last_hip_error, sizeof g_last_hip_error, "%s: %s", what, hipGetErrorString(err));
-    return W4A4_ERR_HIP;
-}
-
-inline bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-inline hipStream_t as_stream(void *s) { return reinterpret_cast<hipStream_t>(s); }
-inline unsigned blocks_for(int64_t work, int per) { return (unsigned)((work + per - 1) / per); }
-inline size_t up256_bytes(int64_t b) { return (size_t)((b + 255) / 256 * 256); }
 // An odd 48-bit ticket per m <= 16 launch that splits K, for its tiles'
 // arrival words: the top 48 bits of the call count times an odd 64-bit
 // constant (a Weyl sequence), made odd, so that a word of the ticket's form
@@ -189,18 +177,6 @@ void launch_mx_a8(const MxArgs &a, hipStream_t s) {
     else launch_mx_cfg<Mx64x128A8>(a, p2, s);
 }
 
-// Size bounds, so that every launch fits the hardware's grid limits and the
-// kernels' 32-bit offsets: rows (m, or routed rows) within 65535 row tiles of
-// 32 (the quantisers' grid.y); K and N well past any model's.  A 1-D launch
-// must stay below 2^32 threads in all.
-constexpr int64_t kMaxGridY = 65535;
-constexpr int64_t kMaxRows = kMaxGridY * 32;
-constexpr int64_t kMaxK = int64_t{1} << 24;
-constexpr int64_t kMaxN = int64_t{1} << 26;
-constexpr int64_t kMaxThreads = (int64_t{1} << 32) - 1;
-inline bool grid_fits(int64_t threads) { return threads <= kMaxThreads; }
-// m rows, n columns, k: inside the bounds above (sizes already known >= 0)
-inline bool within_bounds(int64_t m, int64_t n, int64_t k) { return m <= kMaxRows && n <= kMaxN && k <= kMaxK; }
 // 128 x 128 output tiles of a dense product: each is at most one 256-thread
 // workgroup, plus at most 16 pieces per leftover tile of one round
 constexpr int64_t kMaxDenseTiles = int64_t{1} << 20;

@@ -54,7 +54,10 @@ typedef enum {
     W4A4_ERR_HIP = 6                   /* a HIP runtime call failed */
 } w4a4_status;
 
-typedef enum { W4A4_DTYPE_F32 = 0, W4A4_DTYPE_F16 = 1 } w4a4_dtype;
+/* W4A4_DTYPE_BF16 is taken by the calls from w4a4_quantize_mx4 on (the
+ * quantised-row producers, the read-back and the MXFP4 product); the others
+ * return W4A4_ERR_UNSUPPORTED_DTYPE for it. */
+typedef enum { W4A4_DTYPE_F32 = 0, W4A4_DTYPE_F16 = 1, W4A4_DTYPE_BF16 = 2 } w4a4_dtype;
 
 /* Human-readable name of a status.  Host only; never NULL. */
 const char *w4a4_status_string(w4a4_status s);
@@ -484,6 +487,143 @@ w4a4_status w4a4_gemm_id_routed(const void *packed_w, int64_t n_expert, const ui
                                 const float *scales, int64_t act_rows_per_token, int64_t n_tokens, int64_t top_k,
                                 float *y, int64_t n, int64_t k, const void *workspace, size_t workspace_bytes,
                                 void *stream);
+
+/*
+ * Formats of quantised activation rows, for the calls below that write or
+ * read them.  int4 and int8 are the formats of w4a4_rotate_quantize_act and
+ * w4a4_rotate_quantize_act8 (rotated, fp32 scales [m][k/32]); an operand
+ * buffer, where one is given, is written as by the call named:
+ *   W4A4_ACT_INT4        codes [m][k/2]; operand (may be NULL) as
+ *                        w4a4_rotate_quantize_prepare.
+ *   W4A4_ACT_INT4_SMALL  the same codes and scales, m <= 16; operand
+ *                        (required by the producers) as
+ *                        w4a4_rotate_quantize_prepare_small.
+ *   W4A4_ACT_INT8        codes [m][k] int8; operand (may be NULL) as
+ *                        w4a4_rotate_quantize_prepare8.
+ *   W4A4_ACT_MX4         MXFP4 rows (w4a4_quantize_mx4), not rotated; no
+ *                        operand (NULL).
+ *   W4A4_ACT_MX4_H32     MXFP4 rows of the rotated blocks.
+ * The three size queries return the bytes of each buffer (0 for invalid
+ * sizes, and where a format has no operand).  Host only, pure.
+ */
+typedef enum {
+    W4A4_ACT_INT4 = 0,
+    W4A4_ACT_INT4_SMALL = 1,
+    W4A4_ACT_INT8 = 2,
+    W4A4_ACT_MX4 = 3,
+    W4A4_ACT_MX4_H32 = 4
+} w4a4_act_format;
+size_t w4a4_act_format_code_bytes(w4a4_act_format fmt, int64_t m, int64_t k);
+size_t w4a4_act_format_scale_bytes(w4a4_act_format fmt, int64_t m, int64_t k);
+size_t w4a4_act_format_operand_bytes(w4a4_act_format fmt, int64_t m, int64_t k);
+
+/*
+ * MXFP4 rows (the OCP Microscaling format): FP4 E2M1 codes (sign, magnitude 0
+ * 0.5 1 1.5 2 3 4 6) with one E8M0 scale byte (2^(byte - 127); 255 is NaN)
+ * per 32 elements.
+ *   codes   [m][k/2] bytes, 16-byte aligned: element 2j of a row in byte j's
+ *           low half, 2j + 1 in its high half.
+ *   scales  [m][w4a4_mx4_scale_stride(k)] bytes, 8-byte aligned: k / 32 rounded
+ *           up to a multiple of 8, so a row's groups of 8 blocks are aligned.
+ *           Writers set the bytes past k / 32 to 127, readers ignore them.
+ * w4a4_mx4_scale_stride: 0 for invalid k.  Host only, pure.
+ *
+ * w4a4_quantize_mx4: per block, v = x, or (rotate != 0) v = fl(u * fp32(1/
+ * sqrt(32))) with u the block's unnormalised Walsh-Hadamard butterflies in
+ * fp32 as in w4a4_rotate_quantize_act; e = floor(log2 max|v|) - 2, at least
+ * -127; code = v / 2^e to the nearest E2M1 value, ties to the even code,
+ * magnitudes past 6 to 6; scale byte e + 127.  A zero block gets byte 0; a
+ * block that holds an infinity or a NaN (after the rotation) byte 255 and zero
+ * codes.  Weights and activations are quantised alike; a product needs both
+ * sides rotated or neither.
+ *   x   [m][ldx] of type dt (fp32, fp16 or bf16), ldx >= k, element-aligned.
+ * Bounds: m at most 2^26, k at most 2^24, m * (k / 32) * 4 below 2^32 threads.
+ * Errors as w4a4_rotate_quantize_act.
+ */
+size_t w4a4_mx4_scale_stride(int64_t k);
+w4a4_status w4a4_quantize_mx4(const void *x, w4a4_dtype dt, int64_t m, int64_t k, int64_t ldx, int rotate,
+                              uint8_t *codes, uint8_t *scales, void *stream);
+
+/*
+ * Quantised rows read back: y = fl(code * scale) in fp32, rounded to the
+ * nearest dt (MXFP4 values are exact in fp32 and bf16; a block with scale byte
+ * 255 reads as NaN).  Rotated formats give the rotated row.
+ *   y   out, [m][ldy] of type dt, ldy >= k, element-aligned; only the m x k
+ *       block is written.
+ */
+w4a4_status w4a4_dequantize_act(w4a4_act_format fmt, const void *codes, const void *scales, int64_t m, int64_t k,
+                                void *y, w4a4_dtype dt, int64_t ldy, void *stream);
+
+/*
+ * Residual addition and RMS norm, written as quantised rows in one launch
+ * (what a decoder layer computes before its q/k/v and gate/up products):
+ *   h = rdt(x + residual)        (one fp32 addition, one rounding; rdt(x)
+ *                                 without a residual)
+ *   s = fp32(1 / sqrt(sum_i h_i^2 / k + eps))   (the sum and the root in
+ *                                 fp64, one rounding: s does not depend on
+ *                                 the order of the sum)
+ *   v_i = fl(fl(h_i * s) * weight_i)            (fp32)
+ * and v quantised in format fmt as the calls named above quantise x.
+ *   x         [m][ldx] of type xdt.
+ *   residual  [m][ldr] of type rdt, or NULL.
+ *   weight    [k] fp32, or NULL for ones; 4-byte aligned.
+ *   eps       > 0, finite.
+ *   h         out, [m][ldh] of type rdt, or NULL.  May be residual, or x when
+ *             the types are equal (same pointer and stride: in place); no
+ *             other overlap of outputs with inputs.
+ *   codes, scales, operand   out, as fmt has them.
+ * Errors: an unknown type -> W4A4_ERR_UNSUPPORTED_DTYPE; an unknown format,
+ * negative sizes, a stride below k, bad eps, null pointers with work to do, an
+ * operand with MXFP4 -> W4A4_ERR_INVALID_VALUE; k % 32 ->
+ * W4A4_ERR_K_NOT_MULTIPLE_OF_32; misalignment -> W4A4_ERR_MISALIGNED; a short
+ * operand buffer -> W4A4_ERR_WORKSPACE_TOO_SMALL.
+ */
+w4a4_status w4a4_rms_norm_quantize(const void *x, w4a4_dtype xdt, int64_t ldx, const void *residual, w4a4_dtype rdt,
+                                   int64_t ldr, const float *weight, double eps, int64_t m, int64_t k, void *h,
+                                   int64_t ldh, w4a4_act_format fmt, void *codes, void *scales, void *operand,
+                                   size_t operand_bytes, void *stream);
+
+/*
+ * Gated activation, written as quantised rows in one launch (the input of a
+ * down projection, dense or per routed expert row): v = fp32(act(gate) * up),
+ * with act(g) = g / (1 + e^-g) (W4A4_GLU_SILU) or its tanh-form GELU, g / (1 +
+ * e^-2w), w = sqrt(2/pi) (g + 0.044715 g^3) (W4A4_GLU_GELU_TANH), evaluated in
+ * fp64 to within 2^-40 and rounded once; then v quantised in format fmt.
+ *   gate, up  [m][ldg], [m][ldu] of type dt (two column ranges of one packed
+ *             gate|up product, or two matrices).
+ * Other arguments and errors as w4a4_rms_norm_quantize.
+ */
+typedef enum { W4A4_GLU_SILU = 0, W4A4_GLU_GELU_TANH = 1 } w4a4_glu_act;
+w4a4_status w4a4_glu_quantize(const void *gate, const void *up, w4a4_dtype dt, int64_t m, int64_t k, int64_t ldg,
+                              int64_t ldu, w4a4_glu_act act, w4a4_act_format fmt, void *codes, void *scales,
+                              void *operand, size_t operand_bytes, void *stream);
+
+/*
+ * MXFP4 product: y[i][j] = sum over t of a[i][t] * w[j][t], a and w the values
+ * of two MXFP4 matrices, accumulated in fp32 and rounded once to ydt.  A row
+ * of a (or w) with a NaN block gives a NaN row (column) of y.
+ *
+ * w4a4_mx4_packed_bytes(n, k): bytes of the packed weights.
+ * w4a4_repack_mx4: one-time, lossless re-layout of MXFP4 weights [n][k/2],
+ *   [n][stride] (from w4a4_quantize_mx4, or any MXFP4 file's) for the product.
+ *   packed  out, 16-byte aligned; private layout, 17/32 B per weight with n
+ *           padded to 32 and k to 256.
+ * w4a4_gemm_mx4:
+ *   codes, scales  m activation rows (w4a4_quantize_mx4 or a producer above).
+ *   y              out, [m][ldy] of type ydt (fp32, fp16 or bf16), ldy >= n,
+ *                  element-aligned; only the m x n block is written.
+ *   workspace      w4a4_gemm_mx4_workspace_bytes(m, n, k) bytes, 256-byte
+ *                  aligned (may be NULL when that is 0); contents on entry are
+ *                  ignored, calls that share one must not overlap.
+ * k == 0 writes zeros.  Sizes and errors as w4a4_gemm.
+ */
+size_t w4a4_mx4_packed_bytes(int64_t n, int64_t k);
+w4a4_status w4a4_repack_mx4(const uint8_t *codes, const uint8_t *scales, int64_t n, int64_t k, void *packed,
+                            void *stream);
+size_t w4a4_gemm_mx4_workspace_bytes(int64_t m, int64_t n, int64_t k);
+w4a4_status w4a4_gemm_mx4(const void *packed_w, const uint8_t *codes, const uint8_t *scales, void *y, w4a4_dtype ydt,
+                          int64_t m, int64_t n, int64_t k, int64_t ldy, void *workspace, size_t workspace_bytes,
+                          void *stream);
 
 #ifdef __cplusplus
 }
