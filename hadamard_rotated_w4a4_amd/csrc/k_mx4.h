@@ -8,15 +8,20 @@
 // fp32.  So a block needs no work beyond the instruction: no widening, no
 // scale product, no epilogue per block, which is what bounds the Q4_0 product.
 //
-// Weight records (written once by repack_mx4_kernel): [n / 32 tiles][K groups
-// of 256][4352 B], in the instruction's lane order.  Lane l = 32 h + c of
-// instruction p (0..3) of a group takes block 4 h + p of column c:
-//   bytes [0, 4096)     lane l's 16 code bytes for instruction p at 1024 p + 16 l;
-//   bytes [4096, 4352)  lane l's scale bytes of blocks 4 h .. 4 h + 3 at
-//                       4096 + 4 l; instruction p selects byte p.
-// Columns past n and blocks past k / 32 hold zero codes and scale byte 127:
-// FP4 has no NaN or infinity, so they add exact zeros whatever finite value
-// the other side holds there.
+// K is walked in stages of 128 (4 blocks, two instructions): in instruction j
+// of a stage, lane half h = l / 32 takes block 2 j + h.  The four scale bytes
+// of a row's stage are one dword; shifted right by 8 h, its bytes 0 and 2 are
+// the scales of the lane's two blocks.
+//
+// Records (written by repack_mx4_kernel: once for the weights, per call for the
+// rows of a tiled product): [32-row tiles][stages, K padded to 256][2176 B], in
+// the instruction's lane order:
+//   bytes [0, 2048)     lane l's 16 code bytes for instruction j at 1024 j + 16 l;
+//   bytes [2048, 2176)  row (column) c's four scale bytes at 2048 + 4 c.
+// Rows past the matrix and blocks past k / 32 hold zero codes and scale byte
+// 127: FP4 has no NaN or infinity, so they add exact zeros whatever codes the
+// other side holds there (a reader of plain rows replaces the scale bytes past
+// k / 32 by 127).
 #pragma once
 
 #include "common.h"
@@ -25,36 +30,37 @@
 namespace w4a4 {
 
 typedef int mx4_v8i __attribute__((ext_vector_type(8)));
-constexpr int MX4_REC = 4352;
-constexpr int MX4_SCALE_OFF = 4096;
-constexpr int MX4_GROUP_BYTES = MX4_GROUP * QK / 2;  // code bytes of a row per K group
-__host__ __device__ inline int64_t mx4_groups(int64_t k) { return mx4_stride(k) / MX4_GROUP; }
+constexpr int MX4_REC = 2176;
+constexpr int MX4_SCALE_OFF = 2048;
+constexpr int MX4_BLOCKS = 4;                      // blocks per stage
+constexpr int MX4_ROW_BYTES = MX4_BLOCKS * QK / 2;  // code bytes of a row per stage
+__host__ __device__ inline int64_t mx4_rec_stages(int64_t k) { return mx4_stride(k) / MX4_BLOCKS; }  // stored
+__host__ __device__ inline int64_t mx4_stages(int64_t k) { return (k / QK + MX4_BLOCKS - 1) / MX4_BLOCKS; }  // to compute
 __host__ __device__ inline int64_t mx4_packed_bytes(int64_t n, int64_t k) {
-    return padded_n(n) / TILE_N * mx4_groups(k) * MX4_REC;
+    return padded_n(n) / TILE_N * mx4_rec_stages(k) * MX4_REC;
 }
 
-// One thread per (tile, group, lane).
+// One thread per (tile, stage, lane).
 __global__ __launch_bounds__(256) void repack_mx4_kernel(const uint8_t *__restrict__ codes,
                                                          const uint8_t *__restrict__ scales, int64_t n, int64_t k,
                                                          uint8_t *__restrict__ packed) {
-    const int64_t groups = mx4_groups(k), nb = k / QK;
+    const int64_t stages = mx4_rec_stages(k), nb = k / QK;
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= padded_n(n) / TILE_N * groups * 64) return;
+    if (i >= padded_n(n) / TILE_N * stages * 64) return;
     const int lane = (int)(i & 63), h = lane >> 5;
-    const int64_t rec = i >> 6, tile = rec / groups, grp = rec % groups, col = tile * TILE_N + (lane & 31);
-    uint32_t sc = 0;
-    for (int p = 0; p < 4; p++) {
-        const int64_t b = grp * MX4_GROUP + 4 * h + p;
+    const int64_t rec = i >> 6, tile = rec / stages, t = rec % stages, col = tile * TILE_N + (lane & 31);
+    uint8_t *out = packed + rec * MX4_REC;
+    for (int j = 0; j < 2; j++) {
+        const int64_t b = t * MX4_BLOCKS + 2 * j + h;
         uint4 c = make_uint4(0, 0, 0, 0);
-        uint32_t s = 127;
+        uint8_t s = 127;
         if (col < n && b < nb) {
             c = *reinterpret_cast<const uint4 *>(codes + col * (k / 2) + b * 16);
             s = scales[col * mx4_stride(k) + b];
         }
-        *reinterpret_cast<uint4 *>(packed + rec * MX4_REC + 1024 * p + 16 * lane) = c;
-        sc |= s << (8 * p);
+        *reinterpret_cast<uint4 *>(out + 1024 * j + 16 * lane) = c;
+        out[MX4_SCALE_OFF + 4 * (lane & 31) + 2 * j + h] = s;
     }
-    *reinterpret_cast<uint32_t *>(packed + rec * MX4_REC + MX4_SCALE_OFF + 4 * lane) = sc;
 }
 
 // An FP4 operand (four dwords) as the v8i the builtin takes; the instruction
@@ -63,18 +69,29 @@ __device__ __forceinline__ mx4_v8i mx4_operand(v4u c) {
     const v4i v = {(int)c.x, (int)c.y, (int)c.z, (int)c.w};
     return __builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1);
 }
-// acc += instruction P of a group (P picks the scale byte on both sides).
-template <int P>
+// acc += instruction J of a stage; sa, sb: the lanes' scale dwords, shifted.
+template <int J>
 __device__ __forceinline__ v16f mx4_mfma(v4u a, v4u b, v16f acc, uint32_t sa, uint32_t sb) {
-    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mx4_operand(a), mx4_operand(b), acc, 4, 4, P, (int)sa, P,
-                                                           (int)sb);
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mx4_operand(a), mx4_operand(b), acc, 4, 4, 2 * J, (int)sa,
+                                                           2 * J, (int)sb);
+}
+// The scale bytes of stage t with those of blocks past nb replaced by 127.
+__device__ __forceinline__ uint32_t mx4_live_scales(uint32_t s, int64_t t, int64_t nb) {
+    const int live = (int)min(nb - t * MX4_BLOCKS, (int64_t)MX4_BLOCKS);  // 1..4 for a stage that is computed
+    const uint32_t keep = 0xFFFFFFFFu >> (8 * (MX4_BLOCKS - live));
+    return (s & keep) | (0x7F7F7F7Fu & ~keep);
 }
 
 struct Mx4Args {
     const uint8_t *packed, *codes, *scales;
+    const uint8_t *rows;  // the activation rows as records (tiled product)
     uint8_t *y;
     int64_t m, n, k, ldy;  // ldy: elements
     int dt;
+    int64_t first;    // tiled product: first 32-column tile (the columns before it are another launch's)
+    int64_t columns;  // and how many of the kernel's own column tiles
+    int64_t splits;   // K splits of every tile (1: stored to y)
+    float *partial;   // splits > 1: [splits][m][n] partial sums
 };
 
 // One output of type dt.
@@ -83,39 +100,349 @@ __device__ __forceinline__ void mx4_store(uint8_t *y, int dt, int64_t i, float v
     else reinterpret_cast<uint16_t *>(y)[i] = dt == ROW_F16 ? f16_bits(v) : bf16_bits(v);
 }
 
-// A wave per 32 x 32 outputs over the whole of K, operands straight from
-// global memory.
-constexpr int MX4_WAVES = 4;
-__global__ __launch_bounds__(64 * MX4_WAVES) void gemm_mx4_kernel(Mx4Args a) {
-    const int lane = threadIdx.x & 63, h = lane >> 5, r = lane & 31;
-    const int64_t tile = (int64_t)blockIdx.x * MX4_WAVES + (threadIdx.x >> 6);
-    if (tile >= padded_n(a.n) / TILE_N) return;
-    const int64_t groups = mx4_groups(a.k), nb = a.k / QK;
-    const int64_t row0 = (int64_t)blockIdx.y * 32, row = min(row0 + r, a.m - 1);
-    const uint8_t *arow = a.codes + row * (a.k / 2), *srow = a.scales + row * mx4_stride(a.k);
-    v16f acc = {};
-    for (int64_t g = 0; g < groups; g++) {
-        const uint8_t *rec = a.packed + (tile * groups + g) * MX4_REC;
-        v4u av[4], bv[4];
-        uint32_t sa = 0;
-#pragma unroll
-        for (int p = 0; p < 4; p++) {
-            const int64_t b = g * MX4_GROUP + 4 * h + p;
-            bv[p] = *reinterpret_cast<const v4u *>(rec + 1024 * p + 16 * lane);
-            av[p] = *reinterpret_cast<const v4u *>(arow + min(b, nb - 1) * 16);
-            sa |= (b < nb ? (uint32_t)srow[b] : 127u) << (8 * p);
-        }
-        const uint32_t sb = *reinterpret_cast<const uint32_t *>(rec + MX4_SCALE_OFF + 4 * lane);
-        acc = mx4_mfma<0>(av[0], bv[0], acc, sa, sb);
-        acc = mx4_mfma<1>(av[1], bv[1], acc, sa, sb);
-        acc = mx4_mfma<2>(av[2], bv[2], acc, sa, sb);
-        acc = mx4_mfma<3>(av[3], bv[3], acc, sa, sb);
+// ---------------------------------------------------------------------------
+// Tiled product (both sides as records): WM x WN waves, each owning TM x TN
+// tiles of 32 x 32.  The records go through a ring of NS stages in LDS, filled
+// by direct global-to-LDS loads of contiguous memory, NS - 1 stages ahead of
+// the one computed; one barrier per stage.
+//
+// In LDS a stage holds the row tiles' codes, the column tiles' (2 KB each),
+// then their scale bytes.
+// ---------------------------------------------------------------------------
+template <int WM_, int WN_, int TM_, int TN_, int NS_>
+struct Mx4Cfg {
+    static constexpr int WM = WM_, WN = WN_, TM = TM_, TN = TN_, NS = NS_;
+    static constexpr int WAVES = WM * WN, NT = 64 * WAVES;
+    static constexpr int RT = WM * TM, CT = WN * TN, BM = 32 * RT, BN = 32 * CT;
+    static constexpr int SCALES = (RT + CT) * 2048;         // offset of the scales in a stage
+    static constexpr int PAIRS = (RT + CT + 1) / 2;         // of tiles: one scale load each
+    static constexpr int STAGE = SCALES + PAIRS * 256;      // bytes
+    static constexpr int CODE_LOADS = (2 * (RT + CT) + WAVES - 1) / WAVES;   // 1 KB each, per wave
+    static constexpr int SCALE_LOADS = (PAIRS + WAVES - 1) / WAVES;          // 256 B each, per wave
+    static constexpr int LOADS = CODE_LOADS + SCALE_LOADS;
+    static_assert(RT % 2 == 0, "a pair of tiles is of one side");
+    static_assert(NS >= 3 && NS * STAGE <= 160 * 1024, "the ring fits the LDS");
+    static_assert(32 * TN * 32 * 2 * WAVES <= NS * STAGE, "so does a row of output tiles per wave");
+};
+
+__device__ __forceinline__ int mx4_swizzle(int row) { return ((row >> 1) ^ (row >> 2)) & 3; }
+
+// One global-to-LDS load of 16 (4) bytes per lane: lane l's bytes at base +
+// off land at LDS byte address lds + 16 l (4 l); base and lds are uniform.
+__device__ __forceinline__ void mx4_load16(const uint8_t *base, uint32_t off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds) : "memory");
+}
+__device__ __forceinline__ void mx4_load4(const uint8_t *base, uint32_t off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dword %0, %1" ::"v"(off), "s"(base), "s"(lds) : "memory");
+}
+template <class T>
+__device__ __forceinline__ T mx4_lds(const uint8_t *p) {
+    return *reinterpret_cast<const volatile __attribute__((address_space(3))) T *>(
+        (const __attribute__((address_space(3))) uint8_t *)p);
+}
+// A wave-uniform pointer, placed in SGPRs.
+__device__ __forceinline__ const uint8_t *mx4_uniform(const uint8_t *p) {
+    const uint64_t v = (uint64_t)(uintptr_t)p;
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)v);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+    return (const uint8_t *)(uintptr_t)((uint64_t)hi << 32 | (uint64_t)lo);
+}
+
+// Tile of workgroup id, XCD-aware: workgroups are dealt to the 8 XCDs
+// round-robin, so ids x, x + 8, ... share an L2; the row tiles of a column
+// tile take ids x + 8 y and read its weights from HBM about once.
+__device__ __forceinline__ void mx4_tile_of(int64_t id, int64_t nx, int64_t ny, int64_t &bx, int64_t &by) {
+    const int64_t group = id / (8 * ny), in = id % (8 * ny);
+    const int64_t width = min((int64_t)8, nx - group * 8);
+    bx = group * 8 + in % width;
+    by = in / width;
+}
+
+template <class C>
+__global__ __launch_bounds__(C::NT) void gemm_mx4_tile_kernel(Mx4Args a) {
+    __shared__ __align__(1024) uint8_t smem[C::NS * C::STAGE];
+    constexpr int RT = C::RT, CT = C::CT, TM = C::TM, TN = C::TN, NS = C::NS;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / C::WN, wn = wave % C::WN, h = lane >> 5, r = lane & 31;
+    const int64_t rec_stages = mx4_rec_stages(a.k), stages = mx4_stages(a.k);
+    const int64_t rtiles = padded_n(a.m) / TILE_N, ctiles = padded_n(a.n) / TILE_N;
+
+    int64_t id = blockIdx.x, z = 0;
+    if (a.splits > 1) {
+        z = id % a.splits;
+        id /= a.splits;
     }
-    const int64_t col = tile * TILE_N + r;
+    int64_t bx, by;
+    mx4_tile_of(id, a.columns, (a.m + C::BM - 1) / C::BM, bx, by);
+    const int64_t rt0 = by * RT, ct0 = a.first + bx * CT;
+    const int64_t t_lo = z * stages / a.splits;
+    const int nst = (int)((z + 1) * stages / a.splits - t_lo);
+
+    // ---- this wave's loads: code load i (of 2 (RT + CT)) is half i % 2 of
+    // tile i / 2, row tiles first; scale load i (of PAIRS) tiles 2 i and 2 i + 1,
+    // lanes 32..63 the second.  Tiles past the matrix are clamped (their outputs are not stored).
+    const uint32_t smem_base = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)smem;
+    auto record = [&](int t) {  // of tile t at stage t_lo
+        return t < RT ? a.rows + (min(rt0 + t, rtiles - 1) * rec_stages + t_lo) * MX4_REC
+                      : a.packed + (min(ct0 + t - RT, ctiles - 1) * rec_stages + t_lo) * MX4_REC;
+    };
+    const uint8_t *cbase[C::CODE_LOADS], *sbase[C::SCALE_LOADS];
+    uint32_t cdst[C::CODE_LOADS], sdst[C::SCALE_LOADS], soff[C::SCALE_LOADS];
 #pragma unroll
-    for (int v = 0; v < 16; v++) {
-        const int64_t i = row0 + mfma32_row(v, lane);
-        if (i < a.m && col < a.n) mx4_store(a.y, a.dt, i * a.ldy + col, acc[v]);
+    for (int d = 0; d < C::CODE_LOADS; d++) {
+        const int i = min(wave + C::WAVES * d, 2 * (RT + CT) - 1);
+        cdst[d] = (uint32_t)(i * 1024);
+        cbase[d] = mx4_uniform(record(i >> 1) + (i & 1) * 1024);
+    }
+#pragma unroll
+    for (int d = 0; d < C::SCALE_LOADS; d++) {
+        const int i = min(wave + C::WAVES * d, C::PAIRS - 1);
+        const uint8_t *p0 = record(2 * i), *p1 = record(min(2 * i + 1, RT + CT - 1));
+        sdst[d] = (uint32_t)(C::SCALES + i * 256);
+        sbase[d] = mx4_uniform(p0 + MX4_SCALE_OFF);
+        soff[d] = (h ? (uint32_t)(p1 - p0) : 0u) + 4 * r;
+    }
+    const uint32_t voff = lane * 16;
+    auto issue = [&](int s) {
+        const uint32_t lds = __builtin_amdgcn_readfirstlane(smem_base + (s % NS) * C::STAGE);
+#pragma unroll
+        for (int d = 0; d < C::CODE_LOADS; d++) mx4_load16(cbase[d] + (int64_t)s * MX4_REC, voff, lds + cdst[d]);
+#pragma unroll
+        for (int d = 0; d < C::SCALE_LOADS; d++) mx4_load4(sbase[d] + (int64_t)s * MX4_REC, soff[d], lds + sdst[d]);
+    };
+
+    v16f acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; i++)
+#pragma unroll
+        for (int j = 0; j < TN; j++)
+#pragma unroll
+            for (int v = 0; v < 16; v++) acc[i][j][v] = 0.0f;
+
+    // Fragments are read one instruction ahead: while the MFMAs of instruction
+    // j of stage s run, those of the next one (j = 1, or j = 0 of stage s + 1)
+    // arrive.  The wait and barrier between the two instructions of stage s
+    // publish stage s + 1, and free the slot of stage s, whose last reads have
+    // returned by then, for stage s + NS.
+    v4u af[2][TM], bf[2][TN];
+    uint32_t sa[TM], sb[TN];
+    auto fragments = [&](int s, int j) {
+        const uint8_t *st = smem + (s % NS) * C::STAGE + j * 1024 + lane * 16;
+        const uint8_t *ap = st + wm * TM * 2048, *bp = st + (RT + wn * TN) * 2048;
+#pragma unroll
+        for (int i = 0; i < TN; i++) bf[j][i] = mx4_lds<v4u>(bp + i * 2048);
+#pragma unroll
+        for (int i = 0; i < TM; i++) af[j][i] = mx4_lds<v4u>(ap + i * 2048);
+    };
+    auto scales = [&](int s, uint32_t (&xa)[TM], uint32_t (&xb)[TN]) {
+        const uint8_t *sc = smem + (s % NS) * C::STAGE + C::SCALES + 4 * r;
+#pragma unroll
+        for (int i = 0; i < TN; i++) xb[i] = mx4_lds<uint32_t>(sc + (RT + wn * TN + i) * 128);
+#pragma unroll
+        for (int i = 0; i < TM; i++) xa[i] = mx4_lds<uint32_t>(sc + (wm * TM + i) * 128);
+    };
+#pragma unroll
+    for (int s = 0; s < NS; s++)
+        if (s < nst) issue(s);
+    if (nst >= NS) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(C::LOADS * (NS - 1)) : "memory");
+    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    scales(0, sa, sb);
+    fragments(0, 0);
+    for (int s = 0; s < nst; s++) {
+        uint32_t na[TM], nb[TN];
+#pragma unroll
+        for (int i = 0; i < TM; i++) sa[i] >>= 8 * h;
+#pragma unroll
+        for (int i = 0; i < TN; i++) sb[i] >>= 8 * h;
+        fragments(s, 1);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < TM; i++)
+#pragma unroll
+            for (int j = 0; j < TN; j++) acc[i][j] = mx4_mfma<0>(af[0][i], bf[0][j], acc[i][j], sa[i], sb[j]);
+        __builtin_amdgcn_sched_barrier(0);
+        if (s + NS - 1 < nst) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(C::LOADS * (NS - 2)) : "memory");
+        else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        const int next = min(s + 1, nst - 1);
+        scales(next, na, nb);
+        fragments(next, 0);
+        if (s + NS < nst) issue(s + NS);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < TM; i++)
+#pragma unroll
+            for (int j = 0; j < TN; j++) acc[i][j] = mx4_mfma<1>(af[1][i], bf[1][j], acc[i][j], sa[i], sb[j]);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < TM; i++) sa[i] = na[i];
+#pragma unroll
+        for (int i = 0; i < TN; i++) sb[i] = nb[i];
+    }
+    __syncthreads();
+
+    // ---- outputs.  A 32 x 32 tile's registers hold 32 columns of two rows per
+    // register: 128 contiguous bytes a row in fp32, stored as they are.  16-bit
+    // outputs go through the wave's own part of the LDS, a row of tiles at a
+    // time, and leave as 16 bytes per lane, 64 TN contiguous bytes a row.
+    const int64_t col0 = (ct0 + wn * TN) * TILE_N;
+    if (a.dt == ROW_F32 || a.splits > 1) {
+        float *out = a.splits > 1 ? a.partial + z * a.m * a.n : reinterpret_cast<float *>(a.y);
+        const int64_t ld = a.splits > 1 ? a.n : a.ldy;
+#pragma unroll
+        for (int i = 0; i < TM; i++)
+#pragma unroll
+            for (int j = 0; j < TN; j++) {
+                const int64_t row = (rt0 + wm * TM + i) * 32, col = col0 + j * 32 + r;
+                if (col >= a.n) continue;
+#pragma unroll
+                for (int v = 0; v < 16; v++) {
+                    const int64_t o = row + mfma32_row(v, lane);
+                    if (o < a.m) out[o * ld + col] = acc[i][j][v];
+                }
+            }
+        return;
+    }
+    constexpr int PIECES = TN * 4;  // of 16 bytes in a row
+    uint16_t *mine = reinterpret_cast<uint16_t *>(smem) + wave * 32 * TN * 32;
+    uint16_t *y = reinterpret_cast<uint16_t *>(a.y);
+    const bool vec = (reinterpret_cast<uintptr_t>(a.y) & 15) == 0 && a.ldy % 8 == 0;
+#pragma unroll
+    for (int i = 0; i < TM; i++) {
+#pragma unroll
+        for (int j = 0; j < TN; j++)
+#pragma unroll
+            for (int v = 0; v < 16; v++)
+                mine[mfma32_row(v, lane) * (TN * 32) + j * 32 + r] =
+                    a.dt == ROW_F16 ? f16_bits(acc[i][j][v]) : bf16_bits(acc[i][j][v]);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the wave's own writes, read below by other lanes of it
+#pragma unroll
+        for (int q = 0; q < 32 * PIECES / 64; q++) {
+            const int lr = (q * 64 + lane) / PIECES, lc = (q * 64 + lane) % PIECES * 8;
+            const int64_t row = (rt0 + wm * TM + i) * 32 + lr, col = col0 + lc;
+            const uint4 u = *reinterpret_cast<const uint4 *>(mine + lr * (TN * 32) + lc);
+            if (row >= a.m) continue;
+            if (vec && col + 8 <= a.n) {
+                *reinterpret_cast<uint4 *>(y + row * a.ldy + col) = u;
+            } else {
+                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int e = 0; e < 8; e++)
+                    if (col + e < a.n) y[row * a.ldy + col + e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+            }
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    }
+}
+
+// y = the splits' partial sums added in ascending order.
+__global__ __launch_bounds__(256) void mx4_reduce_kernel(Mx4Args a) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= a.m * a.n) return;
+    float s = a.partial[i];
+    for (int64_t z = 1; z < a.splits; z++) s += a.partial[z * a.m * a.n + i];
+    mx4_store(a.y, a.dt, (i / a.n) * a.ldy + i % a.n, s);
+}
+
+// ---------------------------------------------------------------------------
+// m <= 32: the weights are streamed once, straight into registers.
+//
+// A workgroup takes one 32-column tile over the whole of K; its waves take the
+// stages round-robin, each with its next DEPTH records in flight, and their
+// sums meet in LDS, added in wave order.  The rows' codes and scales are
+// staged in LDS by direct loads (the tiled kernel's row layout, rows past
+// ROWS left out: with 16 rows the matrix instruction's other 16 read the same
+// ones), CHUNK stages at a time; the first weight loads are issued before them.
+// ---------------------------------------------------------------------------
+template <int ROWS_, int WAVES_, int DEPTH_>
+struct Mx4Stream {
+    static constexpr int ROWS = ROWS_, WAVES = WAVES_, DEPTH = DEPTH_, NT = 64 * WAVES;
+    static constexpr int STAGE = ROWS * (MX4_ROW_BYTES + 4);  // LDS bytes of a stage: codes, then scales
+};
+// Stages staged at once: what fits in 144 KB, in whole turns of the rings.
+template <class C>
+__host__ __device__ constexpr int mx4_stream_chunk() {
+    return 144 * 1024 / C::STAGE / (C::WAVES * C::DEPTH) * (C::WAVES * C::DEPTH);
+}
+template <class C>
+__host__ inline size_t mx4_stream_lds(int64_t k) {
+    const int64_t st = mx4_stages(k), chunk = mx4_stream_chunk<C>();
+    const size_t staged = (size_t)((st < chunk ? st : chunk) * C::STAGE), red = (size_t)C::WAVES * C::ROWS * 32 * 4;
+    return staged > red ? staged : red;
+}
+
+template <class C>
+__global__ __launch_bounds__(C::NT) void gemm_mx4_stream_kernel(Mx4Args a) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    constexpr int ROWS = C::ROWS, WAVES = C::WAVES, DEPTH = C::DEPTH, CHUNK = mx4_stream_chunk<C>();
+    const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, r = lane & 31, ar = r % ROWS;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t nb = a.k / QK, tile = blockIdx.x, stride = mx4_stride(a.k);
+    const int stages = (int)mx4_stages(a.k);
+    const uint8_t *rec = a.packed + tile * mx4_rec_stages(a.k) * MX4_REC;
+
+    // this wave's stages: wave, wave + WAVES, ...; past the end the last one
+    // again (not computed), so that every wave has the same loads in flight
+    struct Rec { v4u c0, c1; uint32_t s; } ring[DEPTH];
+    auto load = [&](int t, Rec &R) {
+        const uint8_t *p = rec + (int64_t)min(t, stages - 1) * MX4_REC;
+        R.c0 = *reinterpret_cast<const v4u *>(p + 16 * lane);
+        R.c1 = *reinterpret_cast<const v4u *>(p + 1024 + 16 * lane);
+        R.s = *reinterpret_cast<const uint32_t *>(p + MX4_SCALE_OFF + 4 * r);
+    };
+#pragma unroll
+    for (int d = 0; d < DEPTH; d++) load(wave + WAVES * d, ring[d]);
+
+    v16f acc = {};
+    const int sw = mx4_swizzle(ar);
+    for (int t0 = 0; t0 < stages; t0 += CHUNK) {
+        const int cnt = min(CHUNK, stages - t0);
+        uint8_t *scl = smem + cnt * ROWS * MX4_ROW_BYTES;
+        if (t0) __syncthreads();
+        // rows' chunks: thread i takes 16 bytes of stage i / (4 ROWS), row i / 4 % ROWS
+        for (int i = tid; i < cnt * ROWS * 4; i += C::NT) {
+            const int t = i / (4 * ROWS), row = i / 4 % ROWS, pos = i & 3;
+            const int64_t b = min((int64_t)(t0 + t) * MX4_BLOCKS + (pos ^ mx4_swizzle(row)), nb - 1);
+            *reinterpret_cast<uint4 *>(smem + i * 16) =
+                *reinterpret_cast<const uint4 *>(a.codes + min((int64_t)row, a.m - 1) * (a.k / 2) + b * 16);
+        }
+        for (int i = tid; i < cnt * ROWS; i += C::NT) {
+            const int t = i / ROWS, row = i % ROWS;
+            const uint32_t s = *reinterpret_cast<const uint32_t *>(a.scales + min((int64_t)row, a.m - 1) * stride +
+                                                                   (int64_t)(t0 + t) * MX4_BLOCKS);
+            reinterpret_cast<uint32_t *>(scl)[i] = mx4_live_scales(s, t0 + t, nb);
+        }
+        __syncthreads();
+        for (int t = t0 + wave; t < t0 + cnt; t += WAVES * DEPTH) {
+#pragma unroll
+            for (int d = 0; d < DEPTH; d++) {
+                const int u = t + WAVES * d;
+                if (u < t0 + cnt) {
+                    const uint8_t *p = smem + (u - t0) * ROWS * MX4_ROW_BYTES + ar * MX4_ROW_BYTES;
+                    const v4u x0 = mx4_lds<v4u>(p + (h ^ sw) * 16), x1 = mx4_lds<v4u>(p + ((2 + h) ^ sw) * 16);
+                    const uint32_t sa = mx4_lds<uint32_t>(scl + ((u - t0) * ROWS + ar) * 4) >> (8 * h);
+                    const uint32_t sb = ring[d].s >> (8 * h);
+                    acc = mx4_mfma<0>(x0, ring[d].c0, acc, sa, sb);
+                    acc = mx4_mfma<1>(x1, ring[d].c1, acc, sa, sb);
+                    load(u + WAVES * DEPTH, ring[d]);
+                }
+            }
+        }
+    }
+    __syncthreads();
+    // sums of the waves: [wave][row][column]
+    float *red = reinterpret_cast<float *>(smem);
+#pragma unroll
+    for (int v = 0; v < ROWS / 2; v++) red[(wave * ROWS + mfma32_row(v, lane)) * 32 + r] = acc[v];
+    __syncthreads();
+    for (int i = tid; i < ROWS * 32; i += C::NT) {
+        const int64_t row = i / 32, col = tile * TILE_N + i % 32;
+        float s = red[i];
+#pragma unroll
+        for (int w = 1; w < WAVES; w++) s += red[w * ROWS * 32 + i];
+        if (row < a.m && col < a.n) mx4_store(a.y, a.dt, row * a.ldy + col, s);
     }
 }
 

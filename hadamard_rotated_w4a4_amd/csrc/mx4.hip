@@ -23,7 +23,7 @@ w4a4_status w4a4_repack_mx4(const uint8_t *codes, const uint8_t *scales, int64_t
     if (k % QK) return W4A4_ERR_K_NOT_MULTIPLE_OF_32;
     if (n == 0 || k == 0) return W4A4_OK;
     if (!codes || !scales || !packed) return W4A4_ERR_INVALID_VALUE;
-    const int64_t threads = padded_n(n) / TILE_N * mx4_groups(k) * 64;
+    const int64_t threads = padded_n(n) / TILE_N * mx4_rec_stages(k) * 64;
     if (!grid_fits(threads + 256)) return W4A4_ERR_INVALID_VALUE;
     if (!aligned(codes, 16) || !aligned(scales, 8) || !aligned(packed, 16)) return W4A4_ERR_MISALIGNED;
     repack_mx4_kernel<<<blocks_for(threads, 256), 256, 0, as_stream(stream)>>>(codes, scales, n, k,
@@ -31,9 +31,100 @@ w4a4_status w4a4_repack_mx4(const uint8_t *codes, const uint8_t *scales, int64_t
     return hip_status("repack_mx4_kernel");
 }
 
+}  // extern "C"
+
+namespace {
+
+using Stream16 = Mx4Stream<16, 8, 3>;
+using Stream32 = Mx4Stream<32, 8, 3>;
+constexpr int64_t kStreamRows = 32;  // m up to this takes the streaming kernels
+
+template <class C>
+void launch_stream(const Mx4Args &a, hipStream_t s) {
+    gemm_mx4_stream_kernel<C><<<(unsigned)(padded_n(a.n) / TILE_N), C::NT, mx4_stream_lds<C>(a.k), s>>>(a);
+}
+
+// Tile shapes of the tiled product.
+using T64x64 = Mx4Cfg<2, 2, 1, 1, 4>;
+using T64x128 = Mx4Cfg<2, 2, 1, 2, 4>;
+using T128x128 = Mx4Cfg<2, 2, 2, 2, 4>;
+using T256x192 = Mx4Cfg<4, 2, 2, 3, 4>;
+using T256x256 = Mx4Cfg<4, 2, 2, 4, 4>;
+
+template <class C>
+void launch_tile(const Mx4Args &a, hipStream_t s) {
+    const int64_t tiles = (a.m + C::BM - 1) / C::BM * a.columns * a.splits;
+    gemm_mx4_tile_kernel<C><<<(unsigned)tiles, C::NT, 0, s>>>(a);
+}
+
+// What the plan knows of a shape: its size, how many workgroups a CU holds
+// (their LDS rings decide), and the measured time of one stage (128 of K), in
+// us, of a workgroup alone on its CU and per workgroup on a full CU.
+struct TileShape {
+    int64_t bm, bn, per_cu;
+    double alone, full;
+    void (*launch)(const Mx4Args &, hipStream_t);
+};
+template <class C>
+constexpr TileShape shape(int64_t per_cu, double alone, double full) {
+    return TileShape{C::BM, C::BN, per_cu, alone, full, launch_tile<C>};
+}
+const TileShape kShapes[] = {shape<T64x64>(4, 0.19, 0.125), shape<T64x128>(3, 0.27, 0.167), shape<T128x128>(2, 0.38, 0.375),
+                             shape<T256x192>(1, 0.82, 0.82), shape<T256x256>(1, 1.25, 1.25)};
+
+// Modelled time of one launch: rounds of resident workgroups, each as long as
+// the fullest CU takes.  256 CUs: a pure function of the sizes, because the
+// workspace's size depends on the plan.
+constexpr int64_t kPlanCus = 256;
+double tiles_time(const TileShape &t, int64_t tiles, double stages) {
+    const int64_t slots = kPlanCus * t.per_cu, whole = tiles / slots, left = tiles % slots;
+    const double q = (double)((left + kPlanCus - 1) / kPlanCus);
+    const double last = left == 0 ? 0.0 : q * t.full > t.alone ? q * t.full : t.alone;
+    return ((double)whole * t.full * t.per_cu + last) * stages;
+}
+
+// The tiled product's launches: shape `a` over the first `columns` of its
+// column tiles with `splits` K splits, then shape `b` over the rest (none: -1).
+struct TilePlan {
+    int a, b;
+    int64_t columns, splits;
+};
+TilePlan tile_plan(int64_t m, int64_t n, int64_t k) {
+    constexpr double kLaunch = 2.5;  // us: a further launch, its start and its outputs' tail
+    const double stages = (double)mx4_stages(k);
+    TilePlan best{0, -1, 0, 1};
+    double best_time = 1e30;
+    auto take = [&](double time, TilePlan p) {
+        if (time < best_time) best = p, best_time = time;
+    };
+    for (int i = 0; i < (int)(sizeof kShapes / sizeof kShapes[0]); i++) {
+        const TileShape &t = kShapes[i];
+        const int64_t rows = (m + t.bm - 1) / t.bm, cols = (n + t.bn - 1) / t.bn;
+        take(tiles_time(t, rows * cols, stages), TilePlan{i, -1, cols, 1});
+        // K splits: their partial sums (4 bytes, written and read) at 4 TB/s
+        for (int64_t s = 2; s <= 8 && stages >= 8.0 * s; s++)
+            take(tiles_time(t, rows * cols * s, (double)((mx4_stages(k) + s - 1) / s)) + kLaunch + 8e-6 * s * m * n / 4.0,
+                 TilePlan{i, -1, cols, s});
+        // whole rounds of this shape, the rest in another
+        const int64_t slots = kPlanCus * t.per_cu, first = rows * cols / slots * slots / rows;
+        if (first == 0 || first == cols) continue;
+        for (int j = 0; j < i; j++) {
+            const TileShape &u = kShapes[j];
+            const int64_t rest = (m + u.bm - 1) / u.bm * ((n - first * t.bn + u.bn - 1) / u.bn);
+            take(tiles_time(t, rows * first, stages) + tiles_time(u, rest, stages) + kLaunch, TilePlan{i, j, first, 1});
+        }
+    }
+    return best;
+}
+
+}  // namespace
+
+extern "C" {
+
 size_t w4a4_gemm_mx4_workspace_bytes(int64_t m, int64_t n, int64_t k) {
-    (void)m, (void)n, (void)k;
-    return 0;
+    if (m < 0 || n < 0 || k < 0 || k % QK || m <= kStreamRows || n == 0 || k == 0 || !within_bounds(m, n, k)) return 0;
+    const TilePlan p = tile_plan(m, n, k);  // the rows as records, then the splits' partial sums
+    return up256_bytes(mx4_packed_bytes(m, k)) + (p.splits > 1 ? up256_bytes(p.splits * m * n * 4) : 0);
 }
 
 w4a4_status w4a4_gemm_mx4(const void *packed_w, const uint8_t *codes, const uint8_t *scales, void *y, w4a4_dtype ydt,
@@ -46,9 +137,7 @@ w4a4_status w4a4_gemm_mx4(const void *packed_w, const uint8_t *codes, const uint
     if (!y) return W4A4_ERR_INVALID_VALUE;
     if (!aligned(y, ydt == W4A4_DTYPE_F32 ? 4 : 2)) return W4A4_ERR_MISALIGNED;
     hipStream_t s = as_stream(stream);
-    const int64_t tiles = padded_n(n) / TILE_N;
-    const dim3 grid((unsigned)((tiles + MX4_WAVES - 1) / MX4_WAVES), (unsigned)((m + 31) / 32));
-    if (!grid_fits((int64_t)grid.x * grid.y * 64 * MX4_WAVES)) return W4A4_ERR_INVALID_VALUE;
+    if ((m + 127) / 128 * ((n + 127) / 128) >= (int64_t{1} << 20)) return W4A4_ERR_INVALID_VALUE;
     if (k == 0) {  // empty sum
         zero_typed_kernel<<<(unsigned)std::min<int64_t>((m * n + 255) / 256, 1 << 16), 256, 0, s>>>(
             static_cast<uint8_t *>(y), ydt, m, n, ldy);
@@ -56,10 +145,47 @@ w4a4_status w4a4_gemm_mx4(const void *packed_w, const uint8_t *codes, const uint
     }
     if (!packed_w || !codes || !scales) return W4A4_ERR_INVALID_VALUE;
     if (!aligned(packed_w, 16) || !aligned(codes, 16) || !aligned(scales, 8)) return W4A4_ERR_MISALIGNED;
-    (void)workspace, (void)workspace_bytes;
-    gemm_mx4_kernel<<<grid, 64 * MX4_WAVES, 0, s>>>(Mx4Args{static_cast<const uint8_t *>(packed_w), codes, scales,
-                                                           static_cast<uint8_t *>(y), m, n, k, ldy, ydt});
-    return hip_status("gemm_mx4_kernel");
+    const size_t need = w4a4_gemm_mx4_workspace_bytes(m, n, k);
+    if (need) {
+        if (!workspace) return W4A4_ERR_INVALID_VALUE;
+        if (!aligned(workspace, 256)) return W4A4_ERR_MISALIGNED;
+        if (workspace_bytes < need) return W4A4_ERR_WORKSPACE_TOO_SMALL;
+    }
+    Mx4Args a{};
+    a.packed = static_cast<const uint8_t *>(packed_w);
+    a.codes = codes;
+    a.scales = scales;
+    a.rows = static_cast<const uint8_t *>(workspace);
+    a.y = static_cast<uint8_t *>(y);
+    a.m = m;
+    a.n = n;
+    a.k = k;
+    a.ldy = ldy;
+    a.dt = ydt;
+    a.splits = 1;
+    if (m <= SMA_ROWS) {
+        launch_stream<Stream16>(a, s);
+        return hip_status("gemm_mx4_stream_kernel");
+    }
+    if (m <= kStreamRows) {
+        launch_stream<Stream32>(a, s);
+        return hip_status("gemm_mx4_stream_kernel");
+    }
+    const w4a4_status st = w4a4_repack_mx4(codes, scales, m, k, workspace, stream);
+    if (st != W4A4_OK) return st;
+    const TilePlan p = tile_plan(m, n, k);
+    a.columns = p.columns;
+    a.splits = p.splits;
+    a.partial = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + up256_bytes(mx4_packed_bytes(m, k)));
+    kShapes[p.a].launch(a, s);
+    if (p.splits > 1) mx4_reduce_kernel<<<blocks_for(m * n, 256), 256, 0, s>>>(a);
+    if (p.b >= 0) {
+        const TileShape &u = kShapes[p.b];
+        a.first = p.columns * kShapes[p.a].bn / TILE_N;
+        a.columns = (n - a.first * TILE_N + u.bn - 1) / u.bn;
+        u.launch(a, s);
+    }
+    return hip_status("gemm_mx4_tile_kernel");
 }
 
 }  // extern "C"
