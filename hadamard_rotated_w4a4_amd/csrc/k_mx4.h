@@ -102,16 +102,17 @@ __device__ __forceinline__ void mx4_store(uint8_t *y, int dt, int64_t i, float v
 
 // ---------------------------------------------------------------------------
 // Tiled product (both sides as records): WM x WN waves, each owning TM x TN
-// tiles of 32 x 32.  The records go through a ring of NS stages in LDS, filled
-// by direct global-to-LDS loads of contiguous memory, NS - 1 stages ahead of
-// the one computed; one barrier per stage.
+// tiles of 32 x 32.  The records go through a ring of NS slots of KS stages in
+// LDS, filled by direct global-to-LDS loads of contiguous memory, NS - 1 slots
+// ahead of the one computed; one barrier per slot.
 //
 // In LDS a stage holds the row tiles' codes, the column tiles' (2 KB each),
 // then their scale bytes.
 // ---------------------------------------------------------------------------
-template <int WM_, int WN_, int TM_, int TN_, int NS_>
+template <int WM_, int WN_, int TM_, int TN_, int KS_, int NS_>
 struct Mx4Cfg {
-    static constexpr int WM = WM_, WN = WN_, TM = TM_, TN = TN_, NS = NS_;
+    static constexpr int WM = WM_, WN = WN_, TM = TM_, TN = TN_, KS = KS_, NS = NS_;
+    static_assert(KS == 1 || KS == 2, "the records hold whole slots: K padded to 256");
     static constexpr int WAVES = WM * WN, NT = 64 * WAVES;
     static constexpr int RT = WM * TM, CT = WN * TN, BM = 32 * RT, BN = 32 * CT;
     static constexpr int SCALES = (RT + CT) * 2048;         // offset of the scales in a stage
@@ -119,10 +120,10 @@ struct Mx4Cfg {
     static constexpr int STAGE = SCALES + PAIRS * 256;      // bytes
     static constexpr int CODE_LOADS = (2 * (RT + CT) + WAVES - 1) / WAVES;   // 1 KB each, per wave
     static constexpr int SCALE_LOADS = (PAIRS + WAVES - 1) / WAVES;          // 256 B each, per wave
-    static constexpr int LOADS = CODE_LOADS + SCALE_LOADS;
+    static constexpr int SLOT = KS * STAGE, LOADS = KS * (CODE_LOADS + SCALE_LOADS);
     static_assert(RT % 2 == 0, "a pair of tiles is of one side");
-    static_assert(NS >= 3 && NS * STAGE <= 160 * 1024, "the ring fits the LDS");
-    static_assert(32 * TN * 32 * 2 * WAVES <= NS * STAGE, "so does a row of output tiles per wave");
+    static_assert(NS >= 2 && NS * SLOT <= 160 * 1024, "the ring fits the LDS");
+    static_assert(32 * TN * 32 * 2 * WAVES <= NS * SLOT, "so does a row of output tiles per wave");
 };
 
 __device__ __forceinline__ int mx4_swizzle(int row) { return ((row >> 1) ^ (row >> 2)) & 3; }
@@ -160,12 +161,12 @@ __device__ __forceinline__ void mx4_tile_of(int64_t id, int64_t nx, int64_t ny, 
 
 template <class C>
 __global__ __launch_bounds__(C::NT) void gemm_mx4_tile_kernel(Mx4Args a) {
-    __shared__ __align__(1024) uint8_t smem[C::NS * C::STAGE];
-    constexpr int RT = C::RT, CT = C::CT, TM = C::TM, TN = C::TN, NS = C::NS;
+    __shared__ __align__(1024) uint8_t smem[C::NS * C::SLOT];
+    constexpr int RT = C::RT, CT = C::CT, TM = C::TM, TN = C::TN, KS = C::KS, NS = C::NS, STEPS = 2 * KS;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / C::WN, wn = wave % C::WN, h = lane >> 5, r = lane & 31;
-    const int64_t rec_stages = mx4_rec_stages(a.k), stages = mx4_stages(a.k);
+    const int64_t rec_stages = mx4_rec_stages(a.k), slots = (mx4_stages(a.k) + KS - 1) / KS;
     const int64_t rtiles = padded_n(a.m) / TILE_N, ctiles = padded_n(a.n) / TILE_N;
 
     int64_t id = blockIdx.x, z = 0;
@@ -176,8 +177,8 @@ __global__ __launch_bounds__(C::NT) void gemm_mx4_tile_kernel(Mx4Args a) {
     int64_t bx, by;
     mx4_tile_of(id, a.columns, (a.m + C::BM - 1) / C::BM, bx, by);
     const int64_t rt0 = by * RT, ct0 = a.first + bx * CT;
-    const int64_t t_lo = z * stages / a.splits;
-    const int nst = (int)((z + 1) * stages / a.splits - t_lo);
+    const int64_t lo = z * slots / a.splits, t_lo = lo * KS;
+    const int nst = (int)((z + 1) * slots / a.splits - lo);
 
     // ---- this wave's loads: code load i (of 2 (RT + CT)) is half i % 2 of
     // tile i / 2, row tiles first; scale load i (of PAIRS) tiles 2 i and 2 i + 1,
@@ -205,11 +206,15 @@ __global__ __launch_bounds__(C::NT) void gemm_mx4_tile_kernel(Mx4Args a) {
     }
     const uint32_t voff = lane * 16;
     auto issue = [&](int s) {
-        const uint32_t lds = __builtin_amdgcn_readfirstlane(smem_base + (s % NS) * C::STAGE);
+        const uint32_t lds = __builtin_amdgcn_readfirstlane(smem_base + (s % NS) * C::SLOT);
 #pragma unroll
-        for (int d = 0; d < C::CODE_LOADS; d++) mx4_load16(cbase[d] + (int64_t)s * MX4_REC, voff, lds + cdst[d]);
+        for (int u = 0; u < KS; u++) {
+            const int64_t at = (int64_t)(s * KS + u) * MX4_REC;
 #pragma unroll
-        for (int d = 0; d < C::SCALE_LOADS; d++) mx4_load4(sbase[d] + (int64_t)s * MX4_REC, soff[d], lds + sdst[d]);
+            for (int d = 0; d < C::CODE_LOADS; d++) mx4_load16(cbase[d] + at, voff, lds + u * C::STAGE + cdst[d]);
+#pragma unroll
+            for (int d = 0; d < C::SCALE_LOADS; d++) mx4_load4(sbase[d] + at, soff[d], lds + u * C::STAGE + sdst[d]);
+        }
     };
 
     v16f acc[TM][TN];
@@ -220,27 +225,27 @@ __global__ __launch_bounds__(C::NT) void gemm_mx4_tile_kernel(Mx4Args a) {
 #pragma unroll
             for (int v = 0; v < 16; v++) acc[i][j][v] = 0.0f;
 
-    // Fragments are read one instruction ahead: while the MFMAs of instruction
-    // j of stage s run, those of the next one (j = 1, or j = 0 of stage s + 1)
-    // arrive.  The wait and barrier between the two instructions of stage s
-    // publish stage s + 1, and free the slot of stage s, whose last reads have
-    // returned by then, for stage s + NS.
+    // Fragments are read one step (instruction) ahead: while the MFMAs of a
+    // step run, the next step's operands arrive.  The wait and barrier before a
+    // slot's last step publish slot s + 1, and free slot s, whose last reads
+    // have returned by then, for slot s + NS.
     v4u af[2][TM], bf[2][TN];
-    uint32_t sa[TM], sb[TN];
-    auto fragments = [&](int s, int j) {
-        const uint8_t *st = smem + (s % NS) * C::STAGE + j * 1024 + lane * 16;
-        const uint8_t *ap = st + wm * TM * 2048, *bp = st + (RT + wn * TN) * 2048;
+    uint32_t sa[TM], sb[TN], na[TM], nb[TN];
+    auto fragments = [&](int s, int q) {  // step q of slot s; with a stage's first step, its scales
+        const uint8_t *st = smem + (s % NS) * C::SLOT + (q >> 1) * C::STAGE;
+        const uint8_t *ap = st + wm * TM * 2048 + (q & 1) * 1024 + lane * 16;
+        const uint8_t *bp = st + (RT + wn * TN) * 2048 + (q & 1) * 1024 + lane * 16;
+        const uint8_t *sc = st + C::SCALES + 4 * r;
 #pragma unroll
-        for (int i = 0; i < TN; i++) bf[j][i] = mx4_lds<v4u>(bp + i * 2048);
+        for (int i = 0; i < TN; i++) {
+            bf[q & 1][i] = mx4_lds<v4u>(bp + i * 2048);
+            if (!(q & 1)) nb[i] = mx4_lds<uint32_t>(sc + (RT + wn * TN + i) * 128);
+        }
 #pragma unroll
-        for (int i = 0; i < TM; i++) af[j][i] = mx4_lds<v4u>(ap + i * 2048);
-    };
-    auto scales = [&](int s, uint32_t (&xa)[TM], uint32_t (&xb)[TN]) {
-        const uint8_t *sc = smem + (s % NS) * C::STAGE + C::SCALES + 4 * r;
-#pragma unroll
-        for (int i = 0; i < TN; i++) xb[i] = mx4_lds<uint32_t>(sc + (RT + wn * TN + i) * 128);
-#pragma unroll
-        for (int i = 0; i < TM; i++) xa[i] = mx4_lds<uint32_t>(sc + (wm * TM + i) * 128);
+        for (int i = 0; i < TM; i++) {
+            af[q & 1][i] = mx4_lds<v4u>(ap + i * 2048);
+            if (!(q & 1)) na[i] = mx4_lds<uint32_t>(sc + (wm * TM + i) * 128);
+        }
     };
 #pragma unroll
     for (int s = 0; s < NS; s++)
@@ -248,38 +253,34 @@ __global__ __launch_bounds__(C::NT) void gemm_mx4_tile_kernel(Mx4Args a) {
     if (nst >= NS) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(C::LOADS * (NS - 1)) : "memory");
     else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    scales(0, sa, sb);
     fragments(0, 0);
     for (int s = 0; s < nst; s++) {
-        uint32_t na[TM], nb[TN];
 #pragma unroll
-        for (int i = 0; i < TM; i++) sa[i] >>= 8 * h;
+        for (int q = 0; q < STEPS; q++) {
+            if (!(q & 1)) {  // a new stage's scales: bytes 0 and 2 of the shifted dword are the lane's
 #pragma unroll
-        for (int i = 0; i < TN; i++) sb[i] >>= 8 * h;
-        fragments(s, 1);
-        __builtin_amdgcn_sched_barrier(0);
+                for (int i = 0; i < TM; i++) sa[i] = na[i] >> (8 * h);
 #pragma unroll
-        for (int i = 0; i < TM; i++)
+                for (int i = 0; i < TN; i++) sb[i] = nb[i] >> (8 * h);
+            }
+            if (q + 1 < STEPS) {
+                fragments(s, q + 1);
+            } else {
+                if (s + NS - 1 < nst) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(C::LOADS * (NS - 2)) : "memory");
+                else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+                __builtin_amdgcn_s_barrier();
+                fragments(min(s + 1, nst - 1), 0);
+                if (s + NS < nst) issue(s + NS);
+            }
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int j = 0; j < TN; j++) acc[i][j] = mx4_mfma<0>(af[0][i], bf[0][j], acc[i][j], sa[i], sb[j]);
-        __builtin_amdgcn_sched_barrier(0);
-        if (s + NS - 1 < nst) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(C::LOADS * (NS - 2)) : "memory");
-        else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-        __builtin_amdgcn_s_barrier();
-        const int next = min(s + 1, nst - 1);
-        scales(next, na, nb);
-        fragments(next, 0);
-        if (s + NS < nst) issue(s + NS);
-        __builtin_amdgcn_sched_barrier(0);
+            for (int i = 0; i < TM; i++)
 #pragma unroll
-        for (int i = 0; i < TM; i++)
-#pragma unroll
-            for (int j = 0; j < TN; j++) acc[i][j] = mx4_mfma<1>(af[1][i], bf[1][j], acc[i][j], sa[i], sb[j]);
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int i = 0; i < TM; i++) sa[i] = na[i];
-#pragma unroll
-        for (int i = 0; i < TN; i++) sb[i] = nb[i];
+                for (int j = 0; j < TN; j++)
+                    acc[i][j] = (q & 1) ? mx4_mfma<1>(af[1][i], bf[1][j], acc[i][j], sa[i], sb[j])
+                                        : mx4_mfma<0>(af[0][i], bf[0][j], acc[i][j], sa[i], sb[j]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
     }
     __syncthreads();
 

@@ -45,11 +45,11 @@ void launch_stream(const Mx4Args &a, hipStream_t s) {
 }
 
 // Tile shapes of the tiled product.
-using T64x64 = Mx4Cfg<2, 2, 1, 1, 4>;
-using T64x128 = Mx4Cfg<2, 2, 1, 2, 4>;
-using T128x128 = Mx4Cfg<2, 2, 2, 2, 4>;
-using T256x192 = Mx4Cfg<4, 2, 2, 3, 4>;
-using T256x256 = Mx4Cfg<4, 2, 2, 4, 4>;
+using T64x64 = Mx4Cfg<2, 2, 1, 1, 2, 3>;
+using T64x128 = Mx4Cfg<2, 2, 1, 2, 1, 4>;
+using T128x128 = Mx4Cfg<2, 2, 2, 2, 1, 4>;
+using T256x192 = Mx4Cfg<4, 2, 2, 3, 1, 4>;
+using T256x256 = Mx4Cfg<4, 2, 2, 4, 1, 4>;
 
 template <class C>
 void launch_tile(const Mx4Args &a, hipStream_t s) {
@@ -59,7 +59,7 @@ void launch_tile(const Mx4Args &a, hipStream_t s) {
 
 // What the plan knows of a shape: its size, how many workgroups a CU holds
 // (their LDS rings decide), and the measured time of one stage (128 of K), in
-// us, of a workgroup alone on its CU and per workgroup on a full CU.
+// us, of a workgroup on an otherwise idle chip and of a full round.
 struct TileShape {
     int64_t bm, bn, per_cu;
     double alone, full;
@@ -69,18 +69,17 @@ template <class C>
 constexpr TileShape shape(int64_t per_cu, double alone, double full) {
     return TileShape{C::BM, C::BN, per_cu, alone, full, launch_tile<C>};
 }
-const TileShape kShapes[] = {shape<T64x64>(4, 0.19, 0.125), shape<T64x128>(3, 0.27, 0.167), shape<T128x128>(2, 0.38, 0.375),
-                             shape<T256x192>(1, 0.82, 0.82), shape<T256x256>(1, 1.25, 1.25)};
+const TileShape kShapes[] = {shape<T64x64>(3, 0.175, 0.38), shape<T64x128>(3, 0.30, 0.65), shape<T128x128>(2, 0.41, 0.77),
+                             shape<T256x192>(1, 0.79, 1.02), shape<T256x256>(1, 0.89, 1.30)};
 
-// Modelled time of one launch: rounds of resident workgroups, each as long as
-// the fullest CU takes.  256 CUs: a pure function of the sizes, because the
-// workspace's size depends on the plan.
+// Modelled time of one launch: rounds of resident workgroups; a partial round
+// lies between the two times by how much of the chip it fills.  256 CUs: a
+// pure function of the sizes, because the workspace's size depends on the plan.
 constexpr int64_t kPlanCus = 256;
 double tiles_time(const TileShape &t, int64_t tiles, double stages) {
     const int64_t slots = kPlanCus * t.per_cu, whole = tiles / slots, left = tiles % slots;
-    const double q = (double)((left + kPlanCus - 1) / kPlanCus);
-    const double last = left == 0 ? 0.0 : q * t.full > t.alone ? q * t.full : t.alone;
-    return ((double)whole * t.full * t.per_cu + last) * stages;
+    const double last = left == 0 ? 0.0 : t.alone + (t.full - t.alone) * (double)left / (double)slots;
+    return ((double)whole * t.full + last) * stages;
 }
 
 // The tiled product's launches: shape `a` over the first `columns` of its
