@@ -658,44 +658,22 @@ def gemm_w16(w16: torch.Tensor, a16: torch.Tensor, m: int, n: int, k: int,
 # activation), the MXFP4 format, and its product
 # --------------------------------------------------------------------------
 
-_ROW_DTYPES = {torch.float32: DTYPE_F32, torch.float16: DTYPE_F16, torch.bfloat16: DTYPE_BF16}
+_native_module = None
 
 
-def _row_dtype(dtype, name: str) -> int:
-    dt = _ROW_DTYPES.get(dtype)
-    if dt is None:
-        raise W4A4Error(f"{name}: dtype {dtype}, expected float32, float16 or bfloat16")
-    return dt
-
-
-def _rows(t, name: str, m: int, k: int) -> int:
-    """t is [>= m, >= k] of a row type with unit column stride; its row stride."""
-    _row_dtype(getattr(t, "dtype", None), name)
-    _need_rows(t, name, None, m, k)
-    return max(t.stride(0), k)
-
-
-def _one_device(*ts):
-    """The GPU that every tensor given lives on."""
-    _require_cuda(*ts)
-    device = None
-    for t in ts:
-        if t is not None:
-            if device is not None and t.device != device:
-                raise W4A4Error(f"tensors on {device} and {t.device}, expected one device")
-            device = t.device
-    return device
-
-
-def _run(name: str, device, *args):
-    """Call an entry point on the device's current stream, with the device current."""
-    fn = getattr(lib(), name)
-    if device.index == torch.cuda.current_device():
-        status = fn(*args, _stream(device))
-    else:
-        with torch.cuda.device(device):
-            status = fn(*args, _stream(device))
-    _check(status, name)
+def _native():
+    """The native binding (csrc/binding.cpp): the calls below check their
+    arguments and allocate their outputs there."""
+    global _native_module
+    if _native_module is None:
+        lib()
+        try:
+            from . import _native as module
+        except ImportError as e:
+            raise W4A4Error(f"the native binding is not built ({e}); run `python -m hadamard_rotated_w4a4_amd.build`") from e
+        module.init(W4A4Error)
+        _native_module = module
+    return _native_module
 
 
 def mx4_scale_stride(k: int) -> int:
@@ -715,80 +693,18 @@ def act_format_operand_bytes(fmt: int, m: int, k: int) -> int:
     return int(lib().w4a4_act_format_operand_bytes(fmt, m, k))
 
 
-def _format_shapes(fmt, m, k):
-    """(code shape, code dtype, scale shape, scale dtype) of m rows in a format."""
-    if fmt in (ACT_INT4, ACT_INT4_SMALL):
-        return (m, k // 2), torch.uint8, (m, k // 32), torch.float32
-    if fmt == ACT_INT8:
-        return (m, k), torch.int8, (m, k // 32), torch.float32
-    if fmt in (ACT_MX4, ACT_MX4_H32):
-        return (m, k // 2), torch.uint8, (m, mx4_scale_stride(k)), torch.uint8
-    raise W4A4Error(f"unknown format {fmt}")
-
-
-def _check_rows_out(fmt, m, k, codes, scales, operand):
-    """Checks of the quantised outputs that are given."""
-    cs, ct, ss, st = _format_shapes(fmt, m, k)
-    if fmt == ACT_INT4_SMALL and m > 16:
-        raise W4A4Error(f"ACT_INT4_SMALL: {m} rows (at most 16)")
-    if codes is not None:
-        _need(codes, "codes", ct, cs[0] * cs[1])
-    if scales is not None:
-        _need(scales, "scales", st, ss[0] * ss[1] * st.itemsize)
-    if operand is not None:
-        if fmt in (ACT_MX4, ACT_MX4_H32):
-            raise W4A4Error("operand: MXFP4 rows have none")
-        _need(operand, "operand", torch.uint8, act_format_operand_bytes(fmt, m, k))
-
-
-def _rows_out(fmt, m, k, codes, scales, operand, device):
-    cs, ct, ss, st = _format_shapes(fmt, m, k)
-    if codes is None:
-        codes = torch.empty(cs, dtype=ct, device=device)
-    if scales is None:
-        scales = torch.empty(ss, dtype=st, device=device)
-    if operand is None and fmt == ACT_INT4_SMALL:
-        operand = torch.empty(max(1, act_format_operand_bytes(fmt, m, k)), dtype=torch.uint8, device=device)
-    return codes, scales, operand
-
-
-def _bytes(t) -> int:
-    return 0 if t is None else t.numel()
-
-
 def quantize_mx4(x: torch.Tensor, rotate: bool = True, k: int | None = None, codes: torch.Tensor | None = None,
                  scales: torch.Tensor | None = None):
     """x fp32/fp16/bf16 [m, >=k] (row stride x.stride(0)) -> MXFP4 rows: codes
     uint8 [m, k/2], scales uint8 [m, mx4_scale_stride(k)]."""
-    dt, k = _row_dtype(x.dtype, "x"), _k_of(x, k)
-    m, fmt = x.shape[0], ACT_MX4_H32 if rotate else ACT_MX4
-    ldx = _rows(x, "x", m, k)
-    _check_rows_out(fmt, m, k, codes, scales, None)
-    device = _one_device(x, codes, scales)
-    codes, scales, _ = _rows_out(fmt, m, k, codes, scales, None, device)
-    _run("w4a4_quantize_mx4", device, _ptr(x), dt, m, k, ldx, int(rotate), _ptr(codes), _ptr(scales))
-    return codes, scales
+    return (_native_module or _native()).quantize_mx4(x, rotate, k, codes, scales)
 
 
 def dequantize_act(codes: torch.Tensor, scales: torch.Tensor, k: int, fmt: int, out: torch.Tensor | None = None,
                    dtype: torch.dtype = torch.float32) -> torch.Tensor:
     """Quantised rows (any ACT_ format) read back as [m, k] of `dtype` (or of
     out's type, row stride out.stride(0))."""
-    if codes is None or codes.dim() != 2 or k < 0 or k % 32:
-        raise W4A4Error(f"codes must be a 2-D matrix and k = {k} a multiple of 32")
-    m = codes.shape[0]
-    cs, ct, ss, st = _format_shapes(fmt, m, k)
-    _need(codes, "codes", ct, cs[0] * cs[1])
-    _need(scales, "scales", st, ss[0] * ss[1] * st.itemsize)
-    if out is not None:
-        dtype = out.dtype
-        _rows(out, "out", m, k)
-    dt = _row_dtype(dtype, "dtype")
-    device = _one_device(codes, scales, out)
-    if out is None:
-        out = torch.empty((m, k), dtype=dtype, device=device)
-    _run("w4a4_dequantize_act", device, fmt, _ptr(codes), _ptr(scales), m, k, _ptr(out), dt, max(out.stride(0), k))
-    return out
+    return (_native_module or _native()).dequantize_act(codes, scales, k, fmt, out, dtype)
 
 
 def rms_norm_quantize(x: torch.Tensor, weight: torch.Tensor | None, eps: float, fmt: int,
@@ -800,28 +716,7 @@ def rms_norm_quantize(x: torch.Tensor, weight: torch.Tensor | None, eps: float, 
     (codes, scales, h).  h is written where given (it may be the residual, or x
     of the same type), or allocated when there is a residual; without either
     it is None and the norm reads x."""
-    if x is None or x.dim() != 2:
-        raise W4A4Error("x must be a 2-D matrix")
-    m, k = x.shape[0], _k_of(x, None)
-    xdt, ldx = _row_dtype(x.dtype, "x"), _rows(x, "x", m, k)
-    held = residual if residual is not None else h if h is not None else x
-    rdt = _row_dtype(held.dtype, "residual" if residual is not None else "h")
-    ldr = _rows(residual, "residual", m, k) if residual is not None else 0
-    ldh = _rows(h, "h", m, k) if h is not None else k
-    if h is not None and h.dtype != held.dtype:
-        raise W4A4Error(f"h: dtype {h.dtype}, expected the residual's {held.dtype}")
-    if weight is not None:
-        _need(weight, "weight", torch.float32, 4 * k)
-    if not eps > 0.0 or eps == float("inf"):
-        raise W4A4Error(f"eps = {eps}, expected a positive number")
-    _check_rows_out(fmt, m, k, codes, scales, operand)
-    device = _one_device(x, residual, weight, h, codes, scales, operand)
-    codes, scales, operand = _rows_out(fmt, m, k, codes, scales, operand, device)
-    if h is None and residual is not None:
-        h = torch.empty((m, k), dtype=held.dtype, device=device)
-    _run("w4a4_rms_norm_quantize", device, _ptr(x), xdt, ldx, _ptr(residual), rdt, ldr, _ptr(weight), eps, m, k, _ptr(h),
-         ldh, fmt, _ptr(codes), _ptr(scales), _ptr(operand), _bytes(operand))
-    return codes, scales, h
+    return (_native_module or _native()).rms_norm_quantize(x, weight, eps, fmt, residual, h, codes, scales, operand)
 
 
 def glu_quantize(gate: torch.Tensor, up: torch.Tensor, fmt: int, act: int = GLU_SILU, k: int | None = None,
@@ -829,36 +724,14 @@ def glu_quantize(gate: torch.Tensor, up: torch.Tensor, fmt: int, act: int = GLU_
                  operand: torch.Tensor | None = None):
     """act(gate) * up, both [m, >=k] of one type, written as quantised rows of
     format fmt: returns (codes, scales)."""
-    if gate is None or up is None or gate.dim() != 2 or up.dim() != 2:
-        raise W4A4Error("gate and up must be 2-D matrices")
-    if act not in (GLU_SILU, GLU_GELU_TANH):
-        raise W4A4Error(f"unknown activation {act}")
-    m, k = gate.shape[0], _k_of(gate, k)
-    dt = _row_dtype(gate.dtype, "gate")
-    ldg, ldu = _rows(gate, "gate", m, k), _rows(up, "up", m, k)
-    if up.dtype != gate.dtype:
-        raise W4A4Error(f"up: dtype {up.dtype}, expected {gate.dtype}")
-    _check_rows_out(fmt, m, k, codes, scales, operand)
-    device = _one_device(gate, up, codes, scales, operand)
-    codes, scales, operand = _rows_out(fmt, m, k, codes, scales, operand, device)
-    _run("w4a4_glu_quantize", device, _ptr(gate), _ptr(up), dt, m, k, ldg, ldu, act, fmt, _ptr(codes), _ptr(scales),
-         _ptr(operand), _bytes(operand))
-    return codes, scales
+    return (_native_module or _native()).glu_quantize(gate, up, fmt, act, k, codes, scales, operand)
 
 
 def repack_mx4(codes: torch.Tensor, scales: torch.Tensor, n: int, k: int,
                out: torch.Tensor | None = None) -> torch.Tensor:
     """MXFP4 weight rows (codes [n, k/2], scales [n, mx4_scale_stride(k)]) ->
     packed weight buffer (uint8, private layout)."""
-    _need(codes, "codes", torch.uint8, n * (k // 2))
-    _need(scales, "scales", torch.uint8, n * mx4_scale_stride(k))
-    if out is not None:
-        _need(out, "out", torch.uint8, mx4_packed_bytes(n, k))
-    device = _one_device(codes, scales, out)
-    if out is None:
-        out = torch.empty(mx4_packed_bytes(n, k), dtype=torch.uint8, device=device)
-    _run("w4a4_repack_mx4", device, _ptr(codes), _ptr(scales), n, k, _ptr(out))
-    return out
+    return (_native_module or _native()).repack_mx4(codes, scales, n, k, out)
 
 
 def prepare_weights_mx4(w: torch.Tensor, rotate: bool = True) -> torch.Tensor:
@@ -871,25 +744,6 @@ def gemm_mx4(packed: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, n:
              y: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
              dtype: torch.dtype = torch.float32) -> torch.Tensor:
     """MXFP4 product: [m, n] of `dtype` (or of y's type, row stride y.stride(0)).
-    The workspace is allocated here unless given (uint8, at least
+    The workspace is allocated there unless given (uint8, at least
     gemm_mx4_workspace_bytes)."""
-    if codes is None or codes.dim() != 2 or k < 0 or k % 32:
-        raise W4A4Error(f"codes must be a 2-D matrix and k = {k} a multiple of 32")
-    m = codes.shape[0]
-    _need(packed, "packed", torch.uint8, mx4_packed_bytes(n, k) if m and n else 0)
-    _need(codes, "codes", torch.uint8, m * (k // 2))
-    _need(scales, "scales", torch.uint8, m * mx4_scale_stride(k))
-    need = gemm_mx4_workspace_bytes(m, n, k)
-    if y is not None:
-        dtype = y.dtype
-        _rows(y, "y", m, n)
-    dt = _row_dtype(dtype, "y")
-    if workspace is not None:
-        _need(workspace, "workspace", torch.uint8, need)
-    device = _one_device(packed, codes, scales, y, workspace)
-    if y is None:
-        y = torch.empty((m, n), dtype=dtype, device=device)
-    workspace = _workspace(workspace, need, device)
-    _run("w4a4_gemm_mx4", device, _ptr(packed), _ptr(codes), _ptr(scales), _ptr(y), dt, m, n, k, max(y.stride(0), n),
-         _ptr(workspace), _bytes(workspace))
-    return y
+    return (_native_module or _native()).gemm_mx4(packed, codes, scales, n, k, y, workspace, dtype)

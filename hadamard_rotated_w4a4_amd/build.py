@@ -1,4 +1,5 @@
-"""Build libw4a4.so in-tree with hipcc for gfx950 (MI355X).
+"""Build libw4a4.so (hipcc, gfx950) and the native binding _native.so (g++,
+host code only) in-tree.
 
     python -m hadamard_rotated_w4a4_amd.build
 """
@@ -7,12 +8,14 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libw4a4.so")
 CEILINGS_LIB = os.path.join(PKG, "libw4a4_ceilings.so")  # measured ceilings for the benchmark
+NATIVE = os.path.join(PKG, "_native.so")  # the binding's native part
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = [os.path.join(CSRC, f) for f in ("w4a4.hip", "rows.hip", "mx4.hip")]
@@ -40,15 +43,29 @@ FLAGS = [
 
 def build(verbose: bool = False) -> str:
     """Compile the HIP sources into libw4a4.so and the ceiling probes into
-    libw4a4_ceilings.so (always recompiles)."""
+    libw4a4_ceilings.so, then the native binding (always recompiles)."""
     _compile(LIB, SOURCES, verbose)
     _compile(CEILINGS_LIB, [os.path.join(CSRC, "ceilings.hip")], verbose)
+    _compile_native(verbose)
     return LIB
 
 
-def _compile(lib: str, sources: list, verbose: bool) -> None:
-    tmp = lib + ".tmp"
-    cmd = [HIPCC, *FLAGS, "-I", os.path.join(ROOT, "include"), "-o", tmp, *sources]
+def _compile_native(verbose: bool) -> None:
+    """csrc/binding.cpp against PyTorch's headers and libw4a4.so beside it."""
+    import torch
+    home = os.path.dirname(torch.__file__)
+    includes = [os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
+                sysconfig.get_paths()["include"], "/opt/rocm/include", os.path.join(ROOT, "include")]
+    libs = os.path.join(home, "lib")
+    tmp = NATIVE + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           *(f"-isystem{i}" for i in includes), "-o", tmp, os.path.join(CSRC, "binding.cpp"), f"-L{PKG}", "-l:" + os.path.basename(LIB), f"-L{libs}", "-ltorch_python",
+           "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_hip", f"-Wl,-rpath,$ORIGIN:{libs}"]
+    _run(cmd, "g++", verbose)
+    os.replace(tmp, NATIVE)
+
+
+def _run(cmd: list, tool: str, verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
@@ -56,9 +73,15 @@ def _compile(lib: str, sources: list, verbose: bool) -> None:
     noise = "is not a recognized feature for this target"
     out = "\n".join(ln for ln in (res.stdout + res.stderr).splitlines() if noise not in ln)
     if res.returncode != 0:
-        raise RuntimeError(f"hipcc failed ({res.returncode}):\n{out}")
+        raise RuntimeError(f"{tool} failed ({res.returncode}):\n{out}")
     if verbose and out.strip():
         print(out)
+
+
+def _compile(lib: str, sources: list, verbose: bool) -> None:
+    tmp = lib + ".tmp"
+    cmd = [HIPCC, *FLAGS, "-I", os.path.join(ROOT, "include"), "-o", tmp, *sources]
+    _run(cmd, "hipcc", verbose)
     os.replace(tmp, lib)
 
 
