@@ -13,5 +13,6 @@ def __getattr__(name):
     # the binding imports torch; load it only when asked for
     if name == "ops":
         from . import _lib
+        globals()["ops"] = _lib  # found directly from here on
         return _lib
     raise AttributeError(name)

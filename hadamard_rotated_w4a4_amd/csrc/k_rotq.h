@@ -30,12 +30,13 @@ namespace w4a4 {
 
 constexpr float kInvSqrt32f = 0x1.6a09e6p-3f;  // fp32(1/sqrt(32)), bits 0x3E3504F3
 
-__device__ __forceinline__ float round_half_away(float x) {
-    const float t = truncf(x);
-    const float frac = fabsf(__fsub_rn(x, t));
-    return frac >= 0.5f ? __fadd_rn(t, x < 0.0f ? -1.0f : 1.0f) : t;
+// x rounded to the nearest integer, ties away from zero, for |x| < 256: x plus
+// the number below one half (with x's sign), truncated.  The sum's own rounding
+// carries a tie to the next integer and nothing below one (checked for every
+// fp32 in the range).
+__device__ __forceinline__ int round_half_away(float x) {
+    return (int)__fadd_rn(x, copysignf(0x1.fffffep-2f, x));
 }
-
 
 // Eight consecutive elements as fp32 (exact from fp16).  mode 2: 16-byte
 // aligned groups; mode 1: 4-element groups aligned (8 bytes fp16, 16 bytes
@@ -98,22 +99,14 @@ __device__ __forceinline__ void fwht32_quad(float v[8], int L) {
             v[i + h] = __fsub_rn(a0, a1);
         }
     }
-    {
-        const bool upper = L & 1;
+    // the upper lane of a pair takes lower - upper, as lower + (-upper)
+    const uint32_t flip1 = (uint32_t)(L & 1) << 31, flip2 = (uint32_t)(L & 2) << 30;
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-            const float p = quad_f32<QP_XOR1>(v[i]);
-            v[i] = upper ? __fsub_rn(p, v[i]) : __fadd_rn(v[i], p);  // (lower - upper) / (lower + upper)
-        }
-    }
-    {
-        const bool upper = L & 2;
+    for (int i = 0; i < 8; i++)
+        v[i] = __fadd_rn(quad_f32<QP_XOR1>(v[i]), __uint_as_float(__float_as_uint(v[i]) ^ flip1));
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-            const float p = quad_f32<QP_XOR2>(v[i]);
-            v[i] = upper ? __fsub_rn(p, v[i]) : __fadd_rn(v[i], p);
-        }
-    }
+    for (int i = 0; i < 8; i++)
+        v[i] = __fadd_rn(quad_f32<QP_XOR2>(v[i]), __uint_as_float(__float_as_uint(v[i]) ^ flip2));
 }
 
 // The values of one (row, block), held by a quad of lanes (lane L of the quad:
@@ -135,9 +128,10 @@ __device__ __forceinline__ void quantise_values(float v[8], int L, int q[8], flo
     const bool nonzero = d >= 1.17549435e-38f;  // FLT_MIN: zero and subnormal scales give a zero block
     const float id = nonzero ? __fdiv_rn(1.0f, d) : 0.0f;
     s = !nonzero ? 0.0f : ROTATE ? __fmul_rn(d, kInvSqrt32f) : d;
+    // |v id| is at most QMAX (1 + 2^-22): it rounds to QMAX at most, and to 0
+    // where id is 0
 #pragma unroll
-    for (int t = 0; t < 8; t++)
-        q[t] = nonzero ? (int)fminf((float)QMAX, fmaxf(-(float)QMAX, round_half_away(__fmul_rn(v[t], id)))) : 0;
+    for (int t = 0; t < 8; t++) q[t] = round_half_away(__fmul_rn(v[t], id));
 }
 
 // quantise_values of a block in memory (lane L's elements 8L .. 8L + 7 at

@@ -174,16 +174,25 @@ __host__ __device__ inline int64_t blocks_covered(int fmt, bool act, int64_t k) 
 // blocks, so that the records are written in runs.  Otherwise consecutive
 // quads take consecutive blocks of a row: every load and store is contiguous.
 constexpr int ROWS_THREADS = 256;
+// Blocks per row with ceil(2^64 / n), so that a quad's row is one high product:
+// exact for quads below 2^32 (the error, below n, times 2^32 is below 2^64 / n
+// as n < 2^20).
+struct RowBlocks {
+    uint32_t n;
+    uint64_t magic;  // 0 for n == 1
+};
+inline RowBlocks row_blocks(int64_t n) { return RowBlocks{(uint32_t)n, n > 1 ? ~0ull / (uint64_t)n + 1 : 0}; }
 template <bool TILED>
-__device__ __forceinline__ void block_of_quad(int64_t blocks, int64_t &row, int64_t &b) {
+__device__ __forceinline__ void block_of_quad(RowBlocks blocks, int64_t &row, int64_t &b) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     if constexpr (TILED) {
         b = (int64_t)blockIdx.x * RQ_BLOCKS + (wave >> 1);
         row = (int64_t)blockIdx.y * 32 + (wave & 1) * 16 + (lane >> 2);
     } else {
         const uint32_t i = blockIdx.x * (ROWS_THREADS / 4) + (tid >> 2);  // below 2^30 (the launch is below 2^32 threads)
-        row = i / (uint32_t)blocks;
-        b = i - (uint32_t)row * (uint32_t)blocks;
+        const uint32_t q = blocks.magic ? (uint32_t)__umul64hi(i, blocks.magic) : i;
+        row = q;
+        b = i - q * blocks.n;
     }
 }
 
@@ -195,12 +204,13 @@ struct PlainArgs {
     int64_t ld;  // elements
     int dt;
     bool vec;
+    RowBlocks blocks;
     RowsOut out;
 };
 template <int FMT>
 __global__ __launch_bounds__(ROWS_THREADS) void quantise_rows_kernel(PlainArgs a) {
     int64_t row, b;
-    block_of_quad<false>(mx4_stride(a.out.k), row, b);
+    block_of_quad<false>(a.blocks, row, b);
     const int L = threadIdx.x & 3;
     float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
     if (row < a.out.m && b < a.out.k / QK)
@@ -213,40 +223,44 @@ __global__ __launch_bounds__(ROWS_THREADS) void quantise_rows_kernel(PlainArgs a
 // ---------------------------------------------------------------------------
 constexpr int GLU_SILU = 0, GLU_GELU_TANH = 1;  // w4a4_glu_act
 
-// 1 / (1 + e^-z) to within 2^-40 relative: z is reduced to n ln 2 + r with
-// |r| <= ln 2 / 2 (ln 2 in two parts), e^r is its Taylor sum to r^11 / 11!
-// (the next term is below 2^-47), the quotient two Newton steps from the
-// hardware reciprocal.  Arguments past +-700 are clamped: e^700 is finite in
-// fp64 and the result rounds to 0 or 1 in fp32 either way.
-__device__ __forceinline__ double sigmoid64(double z) {
-    const double t = fmin(fmax(-z, -700.0), 700.0);
-    const double n = rint(t * 1.4426950408889634);
-    double r = fma(n, -0x1.62e42fefa38p-1, t);         // ln 2, leading 42 bits: n times it is exact
-    r = fma(n, -0x1.ef35793c7673p-45, r);              // ln 2 minus those
-    double p = 1.0 / 39916800.0;
-    p = fma(p, r, 1.0 / 3628800.0);
-    p = fma(p, r, 1.0 / 362880.0);
-    p = fma(p, r, 1.0 / 40320.0);
-    p = fma(p, r, 1.0 / 5040.0);
-    p = fma(p, r, 1.0 / 720.0);
-    p = fma(p, r, 1.0 / 120.0);
-    p = fma(p, r, 1.0 / 24.0);
-    p = fma(p, r, 1.0 / 6.0);
-    p = fma(p, r, 0.5);
-    p = fma(p, r, 1.0);
-    p = fma(p, r, 1.0);
-    const double d = 1.0 + ldexp(p, (int)n);
-    double q = __builtin_amdgcn_rcp(d);
-    q = fma(fma(-d, q, 1.0), q, q);
-    return fma(fma(-d, q, 1.0), q, q);
-}
-// act(g) u: silu(g) = g s(g); the tanh form of gelu, g (1 + tanh w) / 2 with
-// w = sqrt(2 / pi) (g + 0.044715 g^3), is g s(2 w).  One rounding, to fp32.
+// act(g) u in fp64 to within 2^-40, rounded once to fp32: silu(g) = g s(g) with
+// s(z) = 1 / (1 + e^-z); the tanh form of gelu, g (1 + tanh w) / 2 with w =
+// sqrt(2 / pi) (g + 0.044715 g^3), is g s(2 w).
+//
+// e^t: t = n ln 2 + r, |r| <= ln 2 / 2 (n from the low bits of t log2 e + 1.5
+// 2^52; n times the error of ln 2 in fp64 is below 2^-44); e^r by the degree 9
+// interpolant at the Chebyshev nodes of the interval (2^-45.5); n into the
+// exponent.  The quotient: the hardware reciprocal x of d, off by e = 1 - d x
+// (about 2^-23), corrected as x (1 + e + e^2).  g is clamped for the exponential
+// only, where fp64 would overflow past it (t within +-700: the result is u times
+// g or 0 in fp32 there).  About 22 fp64 operations an element.
 __device__ __forceinline__ float gated(float gate, float up, int act) {
-    const double g = gate;
-    double z = g;
-    if (act == GLU_GELU_TANH) z = 1.5957691216057308 * (g + 0.044715 * g * g * g);
-    return (float)(g * sigmoid64(z) * (double)up);
+    constexpr double kMagic = 0x1.8p52;
+    double t;
+    if (act == GLU_GELU_TANH) {
+        const double c = fminf(fmaxf(gate, -21.0f), 21.0f);
+        t = c * fma(c * c, -1.5957691216057308 * 0.044715, -1.5957691216057308);  // -2 w, within +-695
+    } else {
+        t = -(double)fminf(fmaxf(gate, -700.0f), 700.0f);
+    }
+    const double s = fma(t, 0x1.71547652b82fep+0, kMagic), n = s - kMagic;
+    const double r = fma(n, -0x1.62e42fefa39efp-1, t);
+    double p = 0x1.72ea9fa1a615ep-19;
+    p = fma(p, r, 0x1.a17dbfc6c99d6p-16);
+    p = fma(p, r, 0x1.a0198b67fb9ecp-13);
+    p = fma(p, r, 0x1.6c162be1ccf47p-10);
+    p = fma(p, r, 0x1.11111126c1431p-7);
+    p = fma(p, r, 0x1.55555588a2487p-5);
+    p = fma(p, r, 0x1.555555554f71ap-3);
+    p = fma(p, r, 0x1.ffffffffe75d7p-2);
+    p = fma(p, r, 0x1.000000000000bp+0);
+    p = fma(p, r, 0x1.000000000003dp+0);
+    const uint64_t bits = __builtin_bit_cast(uint64_t, p);  // in (0.7, 1.42); n within +-1010
+    const uint32_t lo = (uint32_t)__builtin_bit_cast(uint64_t, s);  // n as an integer
+    const double d = 1.0 + __builtin_bit_cast(double, (uint64_t)((uint32_t)(bits >> 32) + (lo << 20)) << 32 | (uint32_t)bits);
+    const double x = __builtin_amdgcn_rcp(d), e = fma(-d, x, 1.0);
+    const double v = (double)gate * (double)up * x;
+    return (float)fma(v, fma(e, e, e), v);
 }
 
 struct GluArgs {
@@ -254,12 +268,13 @@ struct GluArgs {
     int64_t ldg, ldu;  // elements
     int dt, act;
     bool vecg, vecu;
+    RowBlocks blocks;
     RowsOut out;
 };
 template <int FMT, bool TILED>
 __global__ __launch_bounds__(ROWS_THREADS) void glu_rows_kernel(GluArgs a) {
     int64_t row, b;
-    block_of_quad<TILED>(blocks_covered(FMT, TILED, a.out.k), row, b);
+    block_of_quad<TILED>(a.blocks, row, b);
     const int L = threadIdx.x & 3, esz = a.dt == ROW_F32 ? 4 : 2;
     float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
     if (row < a.out.m && b < a.out.k / QK) {
@@ -289,7 +304,7 @@ struct NormArgs {
     const float *weight;          // may be null: ones
     uint8_t *h;                   // may be null, or x or residual itself
     int64_t ldx, ldr, ldh;        // elements
-    double eps;
+    double eps, inv_k;
     int xdt, rdt;
     bool vecx, vecr, vech, vecw;
     RowsOut out;
@@ -328,11 +343,26 @@ __device__ __forceinline__ void norm_h8(const NormArgs &a, int64_t row, int64_t 
     }
     round_row8(a.rdt, v);
 }
-__device__ __forceinline__ void norm_scale8(const NormArgs &a, int64_t c, float rstd, float v[8]) {
-    float w[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
-    if (a.weight) load8(a.weight + c, a.vecw ? 2 : 0, w);
+__device__ __forceinline__ void norm_weight8(const NormArgs &a, int64_t c, float w[8]) {
+    if (a.weight) {
+        load8(a.weight + c, a.vecw ? 2 : 0, w);
+    } else {
 #pragma unroll
-    for (int t = 0; t < 8; t++) v[t] = __fmul_rn(__fmul_rn(v[t], rstd), w[t]);
+        for (int t = 0; t < 8; t++) w[t] = 1.0f;
+    }
+}
+__device__ __forceinline__ void norm_store8(const NormArgs &a, int64_t row, int64_t c, const float v[8]) {
+    if (a.h) store_row8(a.h + (row * a.ldh + c) * (a.rdt == ROW_F32 ? 4 : 2), a.rdt, a.vech, v);
+}
+__device__ __forceinline__ void zero8(float v[8]) {
+#pragma unroll
+    for (int t = 0; t < 8; t++) v[t] = 0.0f;
+}
+// 1 / sqrt(x) in fp64: the hardware root y, off by e = 1 - x y^2 (about 2^-23),
+// corrected as y (1 + e / 2 + 3 e^2 / 8).
+__device__ __forceinline__ double rsqrt64(double x) {
+    const double y = __builtin_amdgcn_rsq(x), e = fma(-(x * y), y, 1.0);
+    return fma(y * e, fma(0.375, e, 0.5), y);
 }
 
 template <int FMT, int CHUNKS>
@@ -348,30 +378,34 @@ __global__ __launch_bounds__(1024) void norm_rows_kernel(NormArgs a, bool act) {
     }
     const bool live = row < a.out.m;
 
-    float v[CHUNKS ? CHUNKS : 1][8];
+    constexpr int HELD = CHUNKS ? CHUNKS : 1;
+    float v[HELD][8], w[HELD][8];
     double sum = 0.0;
     if (live) {
         if constexpr (CHUNKS > 0) {
+            // the weights' loads too before the sum: the row waits for all of them once
 #pragma unroll
             for (int i = 0; i < CHUNKS; i++) {
-                const int64_t b = i * quads + (tid >> 2);
-                if (b < nb) norm_h8(a, row, b * QK + 8 * L, v[i]);
-                else
-#pragma unroll
-                    for (int t = 0; t < 8; t++) v[i][t] = 0.0f;
+                const int64_t b = i * quads + (tid >> 2), c = b * QK + 8 * L;
+                if (b < nb) {
+                    norm_h8(a, row, c, v[i]);
+                    norm_weight8(a, c, w[i]);
+                } else {
+                    zero8(v[i]);
+                    zero8(w[i]);
+                }
             }
 #pragma unroll
             for (int i = 0; i < CHUNKS; i++) {
                 const int64_t b = i * quads + (tid >> 2);
-                if (a.h && b < nb)
-                    store_row8(a.h + (row * a.ldh + b * QK + 8 * L) * (a.rdt == ROW_F32 ? 4 : 2), a.rdt, a.vech, v[i]);
+                if (b < nb) norm_store8(a, row, b * QK + 8 * L, v[i]);
 #pragma unroll
                 for (int t = 0; t < 8; t++) sum = fma((double)v[i][t], (double)v[i][t], sum);
             }
         } else {
             for (int64_t b = tid >> 2; b < nb; b += quads) {
                 norm_h8(a, row, b * QK + 8 * L, v[0]);
-                if (a.h) store_row8(a.h + (row * a.ldh + b * QK + 8 * L) * (a.rdt == ROW_F32 ? 4 : 2), a.rdt, a.vech, v[0]);
+                norm_store8(a, row, b * QK + 8 * L, v[0]);
 #pragma unroll
                 for (int t = 0; t < 8; t++) sum = fma((double)v[0][t], (double)v[0][t], sum);
             }
@@ -380,20 +414,21 @@ __global__ __launch_bounds__(1024) void norm_rows_kernel(NormArgs a, bool act) {
     sum = wave_sum(sum);
     if ((tid & 63) == 0) part[tid >> 6] = sum;
     __syncthreads();
-    sum = part[0];
-    for (int w = 1; w < waves; w++) sum += part[w];
-    const float rstd = (float)(1.0 / sqrt(sum / (double)k + a.eps));
+    sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < 16; i++) sum += i < waves ? part[i] : 0.0;  // i < waves is uniform
+    const float rstd = (float)rsqrt64(fma(sum, a.inv_k, a.eps));
 
     if constexpr (CHUNKS > 0) {
 #pragma unroll
         for (int i = 0; i < CHUNKS; i++) {
             const int64_t b = i * quads + (tid >> 2);
             if (b >= blocks) continue;  // uniform per quad
-            if (live && b < nb) {
-                norm_scale8(a, b * QK + 8 * L, rstd, v[i]);
-            } else {
+            if (live) {
 #pragma unroll
-                for (int t = 0; t < 8; t++) v[i][t] = 0.0f;
+                for (int t = 0; t < 8; t++) v[i][t] = __fmul_rn(__fmul_rn(v[i][t], rstd), w[i][t]);
+            } else {
+                zero8(v[i]);
             }
             emit_block<FMT>(v[i], L, row, b, a.out);
         }
@@ -404,10 +439,11 @@ __global__ __launch_bounds__(1024) void norm_rows_kernel(NormArgs a, bool act) {
                 // this thread's own stores above, when h is written (it may be x or residual itself)
                 if (a.h) load_row8(a.h + (row * a.ldh + c) * (a.rdt == ROW_F32 ? 4 : 2), a.rdt, a.vech, v[0]);
                 else norm_h8(a, row, c, v[0]);
-                norm_scale8(a, c, rstd, v[0]);
-            } else {
+                norm_weight8(a, c, w[0]);
 #pragma unroll
-                for (int t = 0; t < 8; t++) v[0][t] = 0.0f;
+                for (int t = 0; t < 8; t++) v[0][t] = __fmul_rn(__fmul_rn(v[0][t], rstd), w[0][t]);
+            } else {
+                zero8(v[0]);
             }
             emit_block<FMT>(v[0], L, row, b, a.out);
         }
@@ -425,12 +461,13 @@ struct ReadArgs {
     int64_t m, k, ld;  // ld: elements
     int dt;
     bool vec;
+    RowBlocks blocks;
 };
 template <int FMT>
 __global__ __launch_bounds__(ROWS_THREADS) void read_rows_kernel(ReadArgs a) {
     const int64_t nb = a.k / QK;
     int64_t row, b;
-    block_of_quad<false>(nb, row, b);
+    block_of_quad<false>(a.blocks, row, b);
     if (row >= a.m) return;
     const int L = threadIdx.x & 3;
     float v[8];
