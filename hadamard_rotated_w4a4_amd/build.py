@@ -60,7 +60,7 @@ def _compile_native(verbose: bool) -> None:
     tmp = NATIVE + ".tmp"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
            *(f"-isystem{i}" for i in includes), "-o", tmp, os.path.join(CSRC, "binding.cpp"), f"-L{PKG}", "-l:" + os.path.basename(LIB), f"-L{libs}", "-ltorch_python",
-           "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_hip", f"-Wl,-rpath,$ORIGIN:{libs}"]
+           "-ltorch", "-ltorch_cpu", "-ltorch_hip", "-lc10", "-lc10_hip", f"-Wl,-rpath,$ORIGIN:{libs}"]
     _run(cmd, "g++", verbose)
     os.replace(tmp, NATIVE)
 
