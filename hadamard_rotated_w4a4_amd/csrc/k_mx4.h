@@ -103,11 +103,17 @@ __device__ __forceinline__ void mx4_store(uint8_t *y, int dt, int64_t i, float v
 // ---------------------------------------------------------------------------
 // Tiled product (both sides as records): WM x WN waves, each owning TM x TN
 // tiles of 32 x 32.  The records go through a ring of NS slots of KS stages in
-// LDS, filled by direct global-to-LDS loads of contiguous memory, NS - 1 slots
-// ahead of the one computed; one barrier per slot.
+// LDS, filled by direct global-to-LDS loads NS - 1 slots ahead of the one
+// computed; one barrier per slot.
 //
-// In LDS a stage holds the row tiles' codes, the column tiles' (2 KB each),
-// then their scale bytes.
+// A slot is filled in units of 1 KB, one load instruction each and dealt to the
+// waves in turn: unit 2 (KS t + u) + j is the codes of instruction j of stage u
+// of tile t (row tiles first, then column tiles), the units after those the
+// scale bytes, 128 of a tile's stage to every 8 lanes.  In LDS unit i lies at
+// 1024 i.  A load instruction occupies the CU's address path for about 16
+// cycles whatever its width, and a wave waits while it is busy: so scales are
+// gathered into whole units, and a wave issues its loads one by one between
+// its MFMAs, not at the barrier.
 // ---------------------------------------------------------------------------
 template <int WM_, int WN_, int TM_, int TN_, int KS_, int NS_>
 struct Mx4Cfg {
@@ -115,40 +121,27 @@ struct Mx4Cfg {
     static_assert(KS == 1 || KS == 2, "the records hold whole slots: K padded to 256");
     static constexpr int WAVES = WM * WN, NT = 64 * WAVES;
     static constexpr int RT = WM * TM, CT = WN * TN, BM = 32 * RT, BN = 32 * CT;
-    static constexpr int SCALES = (RT + CT) * 2048;         // offset of the scales in a stage
-    static constexpr int PAIRS = (RT + CT + 1) / 2;         // of tiles: one scale load each
-    static constexpr int STAGE = SCALES + PAIRS * 256;      // bytes
-    static constexpr int CODE_LOADS = (2 * (RT + CT) + WAVES - 1) / WAVES;   // 1 KB each, per wave
-    static constexpr int SCALE_LOADS = (PAIRS + WAVES - 1) / WAVES;          // 256 B each, per wave
-    static constexpr int SLOT = KS * STAGE, LOADS = KS * (CODE_LOADS + SCALE_LOADS);
-    static_assert(RT % 2 == 0, "a pair of tiles is of one side");
-    static_assert(NS >= 2 && NS * SLOT <= 160 * 1024, "the ring fits the LDS");
-    static_assert(32 * TN * 32 * 2 * WAVES <= NS * SLOT, "so does a row of output tiles per wave");
+    static constexpr int PIECES = (RT + CT) * KS;                 // tile stages in a slot
+    static constexpr int CODE_UNITS = 2 * PIECES, UNITS = CODE_UNITS + (PIECES + 7) / 8;
+    static constexpr int SLOT = 1024 * UNITS;                     // bytes
+    static constexpr int LOADS = (UNITS + WAVES - 1) / WAVES;     // of a slot, per wave: this many for the first
+    static constexpr int FULL = UNITS - (LOADS - 1) * WAVES;      // FULL waves, one less for the others
+    static_assert(NS >= 3 && NS * SLOT <= 160 * 1024, "the ring fits the LDS");
+    static_assert(2048 * TN * WAVES <= NS * SLOT, "so does a row of 16-bit output tiles per wave");
 };
 
 __device__ __forceinline__ int mx4_swizzle(int row) { return ((row >> 1) ^ (row >> 2)) & 3; }
 
-// One global-to-LDS load of 16 (4) bytes per lane: lane l's bytes at base +
-// off land at LDS byte address lds + 16 l (4 l); base and lds are uniform.
-__device__ __forceinline__ void mx4_load16(const uint8_t *base, uint32_t off, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds) : "memory");
-}
-__device__ __forceinline__ void mx4_load4(const uint8_t *base, uint32_t off, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dword %0, %1" ::"v"(off), "s"(base), "s"(lds) : "memory");
+// One global-to-LDS load of 16 bytes per lane: the 16 bytes at lane l's p land
+// at LDS byte address lds + 16 l (lds is uniform).
+__device__ __forceinline__ void mx4_load16(const uint8_t *p, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(lds) : "memory");
 }
 template <class T>
 __device__ __forceinline__ T mx4_lds(const uint8_t *p) {
     return *reinterpret_cast<const volatile __attribute__((address_space(3))) T *>(
         (const __attribute__((address_space(3))) uint8_t *)p);
 }
-// A wave-uniform pointer, placed in SGPRs.
-__device__ __forceinline__ const uint8_t *mx4_uniform(const uint8_t *p) {
-    const uint64_t v = (uint64_t)(uintptr_t)p;
-    const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)v);
-    const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
-    return (const uint8_t *)(uintptr_t)((uint64_t)hi << 32 | (uint64_t)lo);
-}
-
 // Tile of workgroup id, XCD-aware: workgroups are dealt to the 8 XCDs
 // round-robin, so ids x, x + 8, ... share an L2; the row tiles of a column
 // tile take ids x + 8 y and read its weights from HBM about once.
@@ -162,7 +155,7 @@ __device__ __forceinline__ void mx4_tile_of(int64_t id, int64_t nx, int64_t ny, 
 template <class C>
 __global__ __launch_bounds__(C::NT) void gemm_mx4_tile_kernel(Mx4Args a) {
     __shared__ __align__(1024) uint8_t smem[C::NS * C::SLOT];
-    constexpr int RT = C::RT, CT = C::CT, TM = C::TM, TN = C::TN, KS = C::KS, NS = C::NS, STEPS = 2 * KS;
+    constexpr int RT = C::RT, CT = C::CT, TM = C::TM, TN = C::TN, KS = C::KS, NS = C::NS, STEPS = 2 * KS, L = C::LOADS;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / C::WN, wn = wave % C::WN, h = lane >> 5, r = lane & 31;
@@ -177,45 +170,37 @@ __global__ __launch_bounds__(C::NT) void gemm_mx4_tile_kernel(Mx4Args a) {
     int64_t bx, by;
     mx4_tile_of(id, a.columns, (a.m + C::BM - 1) / C::BM, bx, by);
     const int64_t rt0 = by * RT, ct0 = a.first + bx * CT;
-    const int64_t lo = z * slots / a.splits, t_lo = lo * KS;
+    const int64_t lo = z * slots / a.splits;
     const int nst = (int)((z + 1) * slots / a.splits - lo);
 
-    // ---- this wave's loads: code load i (of 2 (RT + CT)) is half i % 2 of
-    // tile i / 2, row tiles first; scale load i (of PAIRS) tiles 2 i and 2 i + 1,
-    // lanes 32..63 the second.  Tiles past the matrix are clamped (their outputs are not stored).
+    // ---- this wave's loads: units wave, wave + WAVES, ...  Tiles past the
+    // matrix are clamped (their outputs are not stored).
     const uint32_t smem_base = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)smem;
-    auto record = [&](int t) {  // of tile t at stage t_lo
-        return t < RT ? a.rows + (min(rt0 + t, rtiles - 1) * rec_stages + t_lo) * MX4_REC
-                      : a.packed + (min(ct0 + t - RT, ctiles - 1) * rec_stages + t_lo) * MX4_REC;
-    };
-    const uint8_t *cbase[C::CODE_LOADS], *sbase[C::SCALE_LOADS];
-    uint32_t cdst[C::CODE_LOADS], sdst[C::SCALE_LOADS], soff[C::SCALE_LOADS];
+    const bool full = wave < C::FULL;
+    const uint8_t *src[L];
 #pragma unroll
-    for (int d = 0; d < C::CODE_LOADS; d++) {
-        const int i = min(wave + C::WAVES * d, 2 * (RT + CT) - 1);
-        cdst[d] = (uint32_t)(i * 1024);
-        cbase[d] = mx4_uniform(record(i >> 1) + (i & 1) * 1024);
+    for (int d = 0; d < L; d++) {
+        const int i = wave + C::WAVES * d;
+        // the lane's tile stage, and its 16 bytes of that record
+        const int piece = i < C::CODE_UNITS ? i >> 1 : min((i - C::CODE_UNITS) * 8 + (lane >> 3), C::PIECES - 1);
+        const int at = i < C::CODE_UNITS ? (i & 1) * 1024 + lane * 16 : MX4_SCALE_OFF + (lane & 7) * 16;
+        const int t = min(piece / KS, RT + CT - 1), u = piece % KS;
+        const uint8_t *side = t < RT ? a.rows : a.packed;
+        const int64_t tile = t < RT ? min(rt0 + t, rtiles - 1) : min(ct0 + t - RT, ctiles - 1);
+        src[d] = side + (tile * rec_stages + lo * KS + u) * MX4_REC + at;
     }
-#pragma unroll
-    for (int d = 0; d < C::SCALE_LOADS; d++) {
-        const int i = min(wave + C::WAVES * d, C::PAIRS - 1);
-        const uint8_t *p0 = record(2 * i), *p1 = record(min(2 * i + 1, RT + CT - 1));
-        sdst[d] = (uint32_t)(C::SCALES + i * 256);
-        sbase[d] = mx4_uniform(p0 + MX4_SCALE_OFF);
-        soff[d] = (h ? (uint32_t)(p1 - p0) : 0u) + 4 * r;
-    }
-    const uint32_t voff = lane * 16;
-    auto issue = [&](int s) {
-        const uint32_t lds = __builtin_amdgcn_readfirstlane(smem_base + (s % NS) * C::SLOT);
-#pragma unroll
-        for (int u = 0; u < KS; u++) {
-            const int64_t at = (int64_t)(s * KS + u) * MX4_REC;
-#pragma unroll
-            for (int d = 0; d < C::CODE_LOADS; d++) mx4_load16(cbase[d] + at, voff, lds + u * C::STAGE + cdst[d]);
-#pragma unroll
-            for (int d = 0; d < C::SCALE_LOADS; d++) mx4_load4(sbase[d] + at, soff[d], lds + u * C::STAGE + sdst[d]);
-        }
+    // load d of the next slot not yet asked for, into ring slot `into`
+    auto load = [&](int d, int into) {
+        if (d == L - 1 && !full) return;
+        mx4_load16(src[d], __builtin_amdgcn_readfirstlane(smem_base + into * C::SLOT + (wave + C::WAVES * d) * 1024));
+        src[d] += KS * MX4_REC;
     };
+    // until at most n slots' loads are in flight
+#define MX4_WAIT(n)                                                                                  \
+    do {                                                                                             \
+        if (full) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((n) * L) : "memory");          \
+        else asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((n) * (L - 1)) : "memory");         \
+    } while (0)
 
     v16f acc[TM][TN];
 #pragma unroll
@@ -225,64 +210,87 @@ __global__ __launch_bounds__(C::NT) void gemm_mx4_tile_kernel(Mx4Args a) {
 #pragma unroll
             for (int v = 0; v < 16; v++) acc[i][j][v] = 0.0f;
 
-    // Fragments are read one step (instruction) ahead: while the MFMAs of a
-    // step run, the next step's operands arrive.  The wait and barrier before a
-    // slot's last step publish slot s + 1, and free slot s, whose last reads
-    // have returned by then, for slot s + NS.
-    v4u af[2][TM], bf[2][TN];
-    uint32_t sa[TM], sb[TN], na[TM], nb[TN];
-    auto fragments = [&](int s, int q) {  // step q of slot s; with a stage's first step, its scales
-        const uint8_t *st = smem + (s % NS) * C::SLOT + (q >> 1) * C::STAGE;
-        const uint8_t *ap = st + wm * TM * 2048 + (q & 1) * 1024 + lane * 16;
-        const uint8_t *bp = st + (RT + wn * TN) * 2048 + (q & 1) * 1024 + lane * 16;
-        const uint8_t *sc = st + C::SCALES + 4 * r;
-#pragma unroll
-        for (int i = 0; i < TN; i++) {
-            bf[q & 1][i] = mx4_lds<v4u>(bp + i * 2048);
-            if (!(q & 1)) nb[i] = mx4_lds<uint32_t>(sc + (RT + wn * TN + i) * 128);
-        }
-#pragma unroll
-        for (int i = 0; i < TM; i++) {
-            af[q & 1][i] = mx4_lds<v4u>(ap + i * 2048);
-            if (!(q & 1)) na[i] = mx4_lds<uint32_t>(sc + (wm * TM + i) * 128);
-        }
+    // A slot's fragments are all read into registers one slot ahead: while the
+    // MFMAs of slot s run, those of slot s + 1 arrive.  At the barrier between
+    // them slot s + 1's reads have returned, so its place in the ring is free for
+    // slot s + 1 + NS, and slot s + 2 has landed.  A wave thus waits for one LDS
+    // round trip a slot, behind a slot's MFMAs.
+    struct Fragments {
+        v4u a[STEPS][TM], b[STEPS][TN];
+        uint32_t sa[KS][TM], sb[KS][TN];
     };
+    auto read = [&](int s, Fragments &f) {
+        const uint8_t *p = smem + (s % NS) * C::SLOT;
+        const uint8_t *sc = p + C::CODE_UNITS * 1024 + 4 * r;
+        p += lane * 16;
 #pragma unroll
-    for (int s = 0; s < NS; s++)
-        if (s < nst) issue(s);
-    if (nst >= NS) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(C::LOADS * (NS - 1)) : "memory");
-    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    fragments(0, 0);
-    for (int s = 0; s < nst; s++) {
+        for (int u = 0; u < KS; u++) {
+#pragma unroll
+            for (int i = 0; i < TN; i++) f.sb[u][i] = mx4_lds<uint32_t>(sc + ((RT + wn * TN + i) * KS + u) * 128);
+#pragma unroll
+            for (int i = 0; i < TM; i++) f.sa[u][i] = mx4_lds<uint32_t>(sc + ((wm * TM + i) * KS + u) * 128);
+        }
 #pragma unroll
         for (int q = 0; q < STEPS; q++) {
-            if (!(q & 1)) {  // a new stage's scales: bytes 0 and 2 of the shifted dword are the lane's
 #pragma unroll
-                for (int i = 0; i < TM; i++) sa[i] = na[i] >> (8 * h);
+            for (int i = 0; i < TN; i++) f.b[q][i] = mx4_lds<v4u>(p + (RT + wn * TN + i) * KS * 2048 + q * 1024);
 #pragma unroll
-                for (int i = 0; i < TN; i++) sb[i] = nb[i] >> (8 * h);
-            }
-            if (q + 1 < STEPS) {
-                fragments(s, q + 1);
-            } else {
-                if (s + NS - 1 < nst) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(C::LOADS * (NS - 2)) : "memory");
-                else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-                __builtin_amdgcn_s_barrier();
-                fragments(min(s + 1, nst - 1), 0);
-                if (s + NS < nst) issue(s + NS);
-            }
-            __builtin_amdgcn_sched_barrier(0);
+            for (int i = 0; i < TM; i++) f.a[q][i] = mx4_lds<v4u>(p + (wm * TM + i) * KS * 2048 + q * 1024);
+        }
+    };
+    // Slot s from cur, slot s + 1 into next, loads of slot s + NS.
+    auto slot = [&](int s, Fragments &cur, Fragments &next) {
+        const bool more = s + NS < nst;
+        const int into = s % NS;
+        read(min(s + 1, nst - 1), next);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int q = 0; q < STEPS; q++) {
+            uint32_t sa[TM], sb[TN];  // bytes 0 and 2 of the shifted dword are the lane's
+#pragma unroll
+            for (int i = 0; i < TM; i++) sa[i] = cur.sa[q >> 1][i] >> (8 * h);
+#pragma unroll
+            for (int i = 0; i < TN; i++) sb[i] = cur.sb[q >> 1][i] >> (8 * h);
 #pragma unroll
             for (int i = 0; i < TM; i++)
 #pragma unroll
-                for (int j = 0; j < TN; j++)
-                    acc[i][j] = (q & 1) ? mx4_mfma<1>(af[1][i], bf[1][j], acc[i][j], sa[i], sb[j])
-                                        : mx4_mfma<0>(af[0][i], bf[0][j], acc[i][j], sa[i], sb[j]);
-            __builtin_amdgcn_sched_barrier(0);
+                for (int j = 0; j < TN; j++) {
+                    acc[i][j] = (q & 1) ? mx4_mfma<1>(cur.a[q][i], cur.b[q][j], acc[i][j], sa[i], sb[j])
+                                        : mx4_mfma<0>(cur.a[q][i], cur.b[q][j], acc[i][j], sa[i], sb[j]);
+                    // the next loads, spread over the slot's MFMAs
+                    constexpr int SPREAD = STEPS * TM * TN;
+                    const int x = (q * TM + i) * TN + j;
+                    if (more) {
+#pragma unroll
+                        for (int d = 0; d < L; d++)
+                            if (d >= x * L / SPREAD && d < (x + 1) * L / SPREAD) load(d, into);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
         }
+        if (more) MX4_WAIT(NS - 2);
+        else MX4_WAIT(0);
+        __builtin_amdgcn_s_barrier();
+    };
+#pragma unroll
+    for (int s = 0; s < NS; s++)
+        if (s < nst)
+#pragma unroll
+            for (int d = 0; d < L; d++) load(d, s);
+    if (nst >= NS) MX4_WAIT(NS - 1);
+    else MX4_WAIT(0);
+    __builtin_amdgcn_s_barrier();
+    Fragments even, odd;
+    read(0, even);
+    if (nst >= NS) MX4_WAIT(NS - 2);
+    else MX4_WAIT(0);
+    __builtin_amdgcn_s_barrier();
+    for (int s = 0; s < nst; s += 2) {
+        slot(s, even, odd);
+        if (s + 1 < nst) slot(s + 1, odd, even);
     }
     __syncthreads();
+#undef MX4_WAIT
 
     // ---- outputs.  A 32 x 32 tile's registers hold 32 columns of two rows per
     // register: 128 contiguous bytes a row in fp32, stored as they are.  16-bit
@@ -307,7 +315,7 @@ __global__ __launch_bounds__(C::NT) void gemm_mx4_tile_kernel(Mx4Args a) {
         return;
     }
     constexpr int PIECES = TN * 4;  // of 16 bytes in a row
-    uint16_t *mine = reinterpret_cast<uint16_t *>(smem) + wave * 32 * TN * 32;
+    uint16_t *mine = reinterpret_cast<uint16_t *>(smem) + wave * TN * 1024;
     uint16_t *y = reinterpret_cast<uint16_t *>(a.y);
     const bool vec = (reinterpret_cast<uintptr_t>(a.y) & 15) == 0 && a.ldy % 8 == 0;
 #pragma unroll
