@@ -130,8 +130,6 @@ struct Mx4Cfg {
     static_assert(2048 * TN * WAVES <= NS * SLOT, "so does a row of 16-bit output tiles per wave");
 };
 
-__device__ __forceinline__ int mx4_swizzle(int row) { return ((row >> 1) ^ (row >> 2)) & 3; }
-
 // One global-to-LDS load of 16 bytes per lane: the 16 bytes at lane l's p land
 // at LDS byte address lds + 16 l (lds is uniform).
 __device__ __forceinline__ void mx4_load16(const uint8_t *p, uint32_t lds) {
@@ -356,42 +354,76 @@ __global__ __launch_bounds__(256) void mx4_reduce_kernel(Mx4Args a) {
 }
 
 // ---------------------------------------------------------------------------
-// m <= 32: the weights are streamed once, straight into registers.
+// Few rows: the weights are streamed straight into registers, once per block of
+// ROWS rows.
 //
-// A workgroup takes one 32-column tile over the whole of K; its waves take the
-// stages round-robin, each with its next DEPTH records in flight, and their
-// sums meet in LDS, added in wave order.  The rows' codes and scales are
-// staged in LDS by direct loads (the tiled kernel's row layout, rows past
-// ROWS left out: with 16 rows the matrix instruction's other 16 read the same
-// ones), CHUNK stages at a time; the first weight loads are issued before them.
+// A workgroup takes one 32-column tile (blockIdx.x) of one block of rows
+// (blockIdx.y) over the whole of K; its waves take the stages round-robin, each with its next DEPTH records in flight, and their
+// sums meet in LDS, added in wave order.  The rows' codes and scales are staged
+// in LDS, CHUNK stages at a time (the LDS bounds how many workgroups share a
+// CU), the codes by direct loads issued before the weights': a row's four
+// 16-byte chunks of a stage lie at chunk ^ f(row), so that reading one chunk of
+// 16 or 32 rows spreads over all banks, and a load still takes 64 contiguous
+// bytes a row.  With ROWS = 16 the matrix instruction's other 16 rows read the
+// same ones (their outputs are dropped).
 // ---------------------------------------------------------------------------
-template <int ROWS_, int WAVES_, int DEPTH_>
+__device__ __forceinline__ int mx4_swizzle(int row) { return ((row >> 1) ^ (row >> 2)) & 3; }
+
+template <int ROWS_, int WAVES_, int DEPTH_, int CHUNK_KB_>
 struct Mx4Stream {
     static constexpr int ROWS = ROWS_, WAVES = WAVES_, DEPTH = DEPTH_, NT = 64 * WAVES;
+    static constexpr int TM = ROWS > 32 ? ROWS / 32 : 1;  // row tiles
     static constexpr int STAGE = ROWS * (MX4_ROW_BYTES + 4);  // LDS bytes of a stage: codes, then scales
+    // what fits in the LDS share, in whole turns of the rings
+    static constexpr int CHUNK = CHUNK_KB_ * 1024 / STAGE / (WAVES * DEPTH) * (WAVES * DEPTH);
+    static_assert(CHUNK > 0, "one turn of the rings at least");
 };
-// Stages staged at once: what fits in 144 KB, in whole turns of the rings.
-template <class C>
-__host__ __device__ constexpr int mx4_stream_chunk() {
-    return 144 * 1024 / C::STAGE / (C::WAVES * C::DEPTH) * (C::WAVES * C::DEPTH);
-}
 template <class C>
 __host__ inline size_t mx4_stream_lds(int64_t k) {
-    const int64_t st = mx4_stages(k), chunk = mx4_stream_chunk<C>();
-    const size_t staged = (size_t)((st < chunk ? st : chunk) * C::STAGE), red = (size_t)C::WAVES * C::ROWS * 32 * 4;
+    const int64_t st = mx4_stages(k);
+    const size_t staged = (size_t)((st < C::CHUNK ? st : C::CHUNK) * C::STAGE), red = (size_t)C::WAVES * C::ROWS * 32 * 4;
     return staged > red ? staged : red;
 }
 
 template <class C>
 __global__ __launch_bounds__(C::NT) void gemm_mx4_stream_kernel(Mx4Args a) {
     extern __shared__ __align__(1024) uint8_t smem[];
-    constexpr int ROWS = C::ROWS, WAVES = C::WAVES, DEPTH = C::DEPTH, CHUNK = mx4_stream_chunk<C>();
-    const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, r = lane & 31, ar = r % ROWS;
+    constexpr int ROWS = C::ROWS, WAVES = C::WAVES, DEPTH = C::DEPTH, CHUNK = C::CHUNK, TM = C::TM;
+    const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, r = lane & 31, ar = ROWS < 32 ? r % ROWS : r;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int64_t nb = a.k / QK, tile = blockIdx.x, stride = mx4_stride(a.k);
+    const int64_t nb = a.k / QK, tile = blockIdx.x, row0 = (int64_t)blockIdx.y * ROWS, stride = mx4_stride(a.k);
     const int stages = (int)mx4_stages(a.k);
     const uint8_t *rec = a.packed + tile * mx4_rec_stages(a.k) * MX4_REC;
+    const uint32_t smem_base = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)smem;
 
+    // codes of stages t0 .. t0 + cnt - 1: 1 KB (16 rows of a stage) a load
+    auto stage_codes = [&](int t0, int cnt) {
+        const int row = lane >> 2, chunk = (lane & 3) ^ mx4_swizzle(row);  // f has period 16
+        for (int i = wave; i < cnt * (ROWS / 16); i += WAVES) {
+            const int64_t b = min((int64_t)(t0 + i / (ROWS / 16)) * MX4_BLOCKS + chunk, nb - 1);
+            const int64_t src = min(row0 + i % (ROWS / 16) * 16 + row, a.m - 1);
+            mx4_load16(a.codes + src * (a.k / 2) + b * 16, __builtin_amdgcn_readfirstlane(smem_base + i * 1024));
+        }
+    };
+    // their scales, by way of registers
+    constexpr int HELD = (CHUNK * ROWS + C::NT - 1) / C::NT;
+    uint32_t held[HELD];
+    auto load_scales = [&](int t0, int cnt) {
+#pragma unroll
+        for (int j = 0; j < HELD; j++) {
+            const int i = min(tid + j * C::NT, cnt * ROWS - 1), t = i / ROWS, row = i % ROWS;
+            held[j] = *reinterpret_cast<const uint32_t *>(a.scales + min(row0 + row, a.m - 1) * stride +
+                                                          (int64_t)(t0 + t) * MX4_BLOCKS);
+        }
+    };
+    auto store_scales = [&](int t0, int cnt) {
+        uint32_t *scl = reinterpret_cast<uint32_t *>(smem + cnt * ROWS * MX4_ROW_BYTES);
+#pragma unroll
+        for (int j = 0; j < HELD; j++) {
+            const int i = tid + j * C::NT;
+            if (i < cnt * ROWS) scl[i] = mx4_live_scales(held[j], t0 + i / ROWS, nb);
+        }
+    };
     // this wave's stages: wave, wave + WAVES, ...; past the end the last one
     // again (not computed), so that every wave has the same loads in flight
     struct Rec { v4u c0, c1; uint32_t s; } ring[DEPTH];
@@ -401,40 +433,52 @@ __global__ __launch_bounds__(C::NT) void gemm_mx4_stream_kernel(Mx4Args a) {
         R.c1 = *reinterpret_cast<const v4u *>(p + 1024 + 16 * lane);
         R.s = *reinterpret_cast<const uint32_t *>(p + MX4_SCALE_OFF + 4 * r);
     };
+
+    const int first = min(CHUNK, stages);
+    stage_codes(0, first);
+    load_scales(0, first);
+    asm volatile("" ::: "memory");  // in this order: the waits for the rows leave the weights in flight
 #pragma unroll
     for (int d = 0; d < DEPTH; d++) load(wave + WAVES * d, ring[d]);
 
-    v16f acc = {};
+    v16f acc[TM];
+#pragma unroll
+    for (int i = 0; i < TM; i++)
+#pragma unroll
+        for (int v = 0; v < 16; v++) acc[i][v] = 0.0f;
     const int sw = mx4_swizzle(ar);
     for (int t0 = 0; t0 < stages; t0 += CHUNK) {
         const int cnt = min(CHUNK, stages - t0);
-        uint8_t *scl = smem + cnt * ROWS * MX4_ROW_BYTES;
-        if (t0) __syncthreads();
-        // rows' chunks: thread i takes 16 bytes of stage i / (4 ROWS), row i / 4 % ROWS
-        for (int i = tid; i < cnt * ROWS * 4; i += C::NT) {
-            const int t = i / (4 * ROWS), row = i / 4 % ROWS, pos = i & 3;
-            const int64_t b = min((int64_t)(t0 + t) * MX4_BLOCKS + (pos ^ mx4_swizzle(row)), nb - 1);
-            *reinterpret_cast<uint4 *>(smem + i * 16) =
-                *reinterpret_cast<const uint4 *>(a.codes + min((int64_t)row, a.m - 1) * (a.k / 2) + b * 16);
+        if (t0) {
+            __syncthreads();  // every wave is done with the last chunk
+            stage_codes(t0, cnt);
+            load_scales(t0, cnt);
         }
-        for (int i = tid; i < cnt * ROWS; i += C::NT) {
-            const int t = i / ROWS, row = i % ROWS;
-            const uint32_t s = *reinterpret_cast<const uint32_t *>(a.scales + min((int64_t)row, a.m - 1) * stride +
-                                                                   (int64_t)(t0 + t) * MX4_BLOCKS);
-            reinterpret_cast<uint32_t *>(scl)[i] = mx4_live_scales(s, t0 + t, nb);
-        }
+        store_scales(t0, cnt);
+        if (t0) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        else asm volatile("s_waitcnt vmcnt(%0)" ::"n"(3 * DEPTH) : "memory");
         __syncthreads();
+        const uint8_t *scl = smem + cnt * ROWS * MX4_ROW_BYTES;
         for (int t = t0 + wave; t < t0 + cnt; t += WAVES * DEPTH) {
 #pragma unroll
             for (int d = 0; d < DEPTH; d++) {
                 const int u = t + WAVES * d;
                 if (u < t0 + cnt) {
                     const uint8_t *p = smem + (u - t0) * ROWS * MX4_ROW_BYTES + ar * MX4_ROW_BYTES;
-                    const v4u x0 = mx4_lds<v4u>(p + (h ^ sw) * 16), x1 = mx4_lds<v4u>(p + ((2 + h) ^ sw) * 16);
-                    const uint32_t sa = mx4_lds<uint32_t>(scl + ((u - t0) * ROWS + ar) * 4) >> (8 * h);
+                    v4u x0[TM], x1[TM];
+                    uint32_t sa[TM];
+#pragma unroll
+                    for (int i = 0; i < TM; i++) {
+                        x0[i] = mx4_lds<v4u>(p + i * 32 * MX4_ROW_BYTES + (h ^ sw) * 16);
+                        x1[i] = mx4_lds<v4u>(p + i * 32 * MX4_ROW_BYTES + ((2 + h) ^ sw) * 16);
+                        sa[i] = mx4_lds<uint32_t>(scl + ((u - t0) * ROWS + i * 32 + ar) * 4) >> (8 * h);
+                    }
                     const uint32_t sb = ring[d].s >> (8 * h);
-                    acc = mx4_mfma<0>(x0, ring[d].c0, acc, sa, sb);
-                    acc = mx4_mfma<1>(x1, ring[d].c1, acc, sa, sb);
+#pragma unroll
+                    for (int i = 0; i < TM; i++) {
+                        acc[i] = mx4_mfma<0>(x0[i], ring[d].c0, acc[i], sa[i], sb);
+                        acc[i] = mx4_mfma<1>(x1[i], ring[d].c1, acc[i], sa[i], sb);
+                    }
                     load(u + WAVES * DEPTH, ring[d]);
                 }
             }
@@ -444,10 +488,10 @@ __global__ __launch_bounds__(C::NT) void gemm_mx4_stream_kernel(Mx4Args a) {
     // sums of the waves: [wave][row][column]
     float *red = reinterpret_cast<float *>(smem);
 #pragma unroll
-    for (int v = 0; v < ROWS / 2; v++) red[(wave * ROWS + mfma32_row(v, lane)) * 32 + r] = acc[v];
+    for (int v = 0; v < ROWS / 2; v++) red[(wave * ROWS + (v >> 4) * 32 + mfma32_row(v & 15, lane)) * 32 + r] = acc[v >> 4][v & 15];
     __syncthreads();
     for (int i = tid; i < ROWS * 32; i += C::NT) {
-        const int64_t row = i / 32, col = tile * TILE_N + i % 32;
+        const int64_t row = row0 + i / 32, col = tile * TILE_N + i % 32;
         float s = red[i];
 #pragma unroll
         for (int w = 1; w < WAVES; w++) s += red[w * ROWS * 32 + i];

@@ -35,13 +35,37 @@ w4a4_status w4a4_repack_mx4(const uint8_t *codes, const uint8_t *scales, int64_t
 
 namespace {
 
-using Stream16 = Mx4Stream<16, 8, 3>;
-using Stream32 = Mx4Stream<32, 8, 3>;
-constexpr int64_t kStreamRows = 32;  // m up to this takes the streaming kernels
+// The streaming kernels: up to 16, 32 or 64 rows a block, waves, records in
+// flight, LDS share in KB.  Measured: 16 rows, 8 waves for K up to 5120 (17408
+// columns 11.3 us against 11.9 with 16 waves), 16 waves past it (5120 x 8192
+// 6.8 us against 7.4); 32 rows, 16 waves with a CU's whole LDS while every
+// column tile has a CU (5120 x 8192 8.2 us against 10.2), else 8 (17408 x 5120
+// 13.7 us against 16.5).
+using Stream16 = Mx4Stream<16, 8, 2, 52>;
+using Stream16LongK = Mx4Stream<16, 16, 2, 78>;
+using Stream32 = Mx4Stream<32, 8, 2, 53>;
+using Stream32Few = Mx4Stream<32, 16, 2, 144>;
+using Stream64Few = Mx4Stream<64, 16, 1, 144>;
+constexpr int64_t kPlanCus = 256;  // the plans are pure functions of the sizes: the workspace's size depends on them
 
 template <class C>
 void launch_stream(const Mx4Args &a, hipStream_t s) {
-    gemm_mx4_stream_kernel<C><<<(unsigned)(padded_n(a.n) / TILE_N), C::NT, mx4_stream_lds<C>(a.k), s>>>(a);
+    const dim3 grid((unsigned)(padded_n(a.n) / TILE_N), (unsigned)((a.m + C::ROWS - 1) / C::ROWS));
+    gemm_mx4_stream_kernel<C><<<grid, C::NT, mx4_stream_lds<C>(a.k), s>>>(a);
+}
+// m past 32 streams only while every (block of 64 rows, column tile) has a CU of
+// its own: then it needs no records of the rows and no second launch (64 x
+// 1024 x 5120 7.0 us against 12.5 tiled, 64 x 5120 x 17408 23 against 29), but
+// with several workgroups on a CU the tiles' reuse wins (64 x 17408 x 5120 21
+// against 16).
+bool streams(int64_t m, int64_t n) { return m <= 32 || (m + 63) / 64 * (padded_n(n) / TILE_N) <= kPlanCus; }
+void launch_streams(const Mx4Args &a, hipStream_t s) {
+    const bool few = padded_n(a.n) / TILE_N <= kPlanCus;
+    if (a.m > 32) launch_stream<Stream64Few>(a, s);
+    else if (a.m > 16 && few) launch_stream<Stream32Few>(a, s);
+    else if (a.m > 16) launch_stream<Stream32>(a, s);
+    else if (a.k > 5120) launch_stream<Stream16LongK>(a, s);
+    else launch_stream<Stream16>(a, s);
 }
 
 // Tile shapes of the tiled product.
@@ -73,9 +97,7 @@ const TileShape kShapes[] = {shape<T64x64>(3, 0.17, 0.38), shape<T64x128>(2, 0.2
                              shape<T256x192>(1, 0.74, 1.00), shape<T256x256>(1, 0.86, 1.30)};
 
 // Modelled time of one launch: rounds of resident workgroups; a partial round
-// lies between the two times by how much of the chip it fills.  256 CUs: a
-// pure function of the sizes, because the workspace's size depends on the plan.
-constexpr int64_t kPlanCus = 256;
+// lies between the two times by how much of the chip it fills.
 double tiles_time(const TileShape &t, int64_t tiles, double stages) {
     const int64_t slots = kPlanCus * t.per_cu, whole = tiles / slots, left = tiles % slots;
     const double last = left == 0 ? 0.0 : t.alone + (t.full - t.alone) * (double)left / (double)slots;
@@ -121,7 +143,7 @@ TilePlan tile_plan(int64_t m, int64_t n, int64_t k) {
 extern "C" {
 
 size_t w4a4_gemm_mx4_workspace_bytes(int64_t m, int64_t n, int64_t k) {
-    if (m < 0 || n < 0 || k < 0 || k % QK || m <= kStreamRows || n == 0 || k == 0 || !within_bounds(m, n, k)) return 0;
+    if (m < 0 || n < 0 || k < 0 || k % QK || n == 0 || k == 0 || !within_bounds(m, n, k) || streams(m, n)) return 0;
     const TilePlan p = tile_plan(m, n, k);  // the rows as records, then the splits' partial sums
     return up256_bytes(mx4_packed_bytes(m, k)) + (p.splits > 1 ? up256_bytes(p.splits * m * n * 4) : 0);
 }
@@ -162,12 +184,8 @@ w4a4_status w4a4_gemm_mx4(const void *packed_w, const uint8_t *codes, const uint
     a.ldy = ldy;
     a.dt = ydt;
     a.splits = 1;
-    if (m <= SMA_ROWS) {
-        launch_stream<Stream16>(a, s);
-        return hip_status("gemm_mx4_stream_kernel");
-    }
-    if (m <= kStreamRows) {
-        launch_stream<Stream32>(a, s);
+    if (streams(m, n)) {
+        launch_streams(a, s);
         return hip_status("gemm_mx4_stream_kernel");
     }
     const w4a4_status st = w4a4_repack_mx4(codes, scales, m, k, workspace, stream);
