@@ -38,29 +38,50 @@ struct RowsOut {
     int64_t m, k;
 };
 
-// Eight elements of type dt at byte address p as fp32.  vec: 16-byte aligned.
-__device__ __forceinline__ void load_row8(const uint8_t *p, int dt, bool vec, float v[8]) {
-    if (dt == ROW_F32) {
-        load8(reinterpret_cast<const float *>(p), vec ? 2 : 0, v);
-    } else if (dt == ROW_F16) {
-        load8(reinterpret_cast<const __half *>(p), vec ? 2 : 0, v);
-    } else {
-        uint32_t w[4];
-        if (vec) {
-            const uint4 u = *reinterpret_cast<const uint4 *>(p);
-            w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
-        } else {
-            const uint16_t *h = reinterpret_cast<const uint16_t *>(p);
+// Eight elements of a row, as loaded: 16 bytes of a 2-byte type, 32 of fp32.
+// Loading and converting are apart so that a thread can have every load of its
+// row in flight before it waits for the first.
+struct Raw8 {
+    v4u lo, hi;
+};
+// vec: the address is 16-byte aligned.
+__device__ __forceinline__ Raw8 load_raw8(const uint8_t *p, int dt, bool vec) {
+    Raw8 x;
+    if (vec) {
+        x.lo = *reinterpret_cast<const v4u *>(p);
+        if (dt == ROW_F32) x.hi = *reinterpret_cast<const v4u *>(p + 16);
+    } else if (dt == ROW_F32) {
+        const uint32_t *w = reinterpret_cast<const uint32_t *>(p);
 #pragma unroll
-            for (int i = 0; i < 4; i++) w[i] = (uint32_t)h[2 * i] | (uint32_t)h[2 * i + 1] << 16;
-        }
+        for (int i = 0; i < 4; i++) x.lo[i] = w[i];
+#pragma unroll
+        for (int i = 0; i < 4; i++) x.hi[i] = w[4 + i];
+    } else {
+        const uint16_t *h = reinterpret_cast<const uint16_t *>(p);
+#pragma unroll
+        for (int i = 0; i < 4; i++) x.lo[i] = (uint32_t)h[2 * i] | (uint32_t)h[2 * i + 1] << 16;
+    }
+    return x;
+}
+__device__ __forceinline__ void to_f32(const Raw8 &x, int dt, float v[8]) {
+    if (dt == ROW_F32) {
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+            v[i] = __uint_as_float(x.lo[i]);
+            v[4 + i] = __uint_as_float(x.hi[i]);
+        }
+    } else if (dt == ROW_F16) {
+#pragma unroll
+        for (int i = 0; i < 4; i++) halves_to_float(x.lo[i], v[2 * i], v[2 * i + 1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            v[2 * i] = __uint_as_float(x.lo[i] << 16);
+            v[2 * i + 1] = __uint_as_float(x.lo[i] & 0xFFFF0000u);
         }
     }
 }
+__device__ __forceinline__ int row_size(int dt) { return dt == ROW_F32 ? 4 : 2; }
 
 // fp32 -> 16-bit types, to nearest even.
 __device__ __forceinline__ uint16_t f16_bits(float x) { return __half_as_ushort(__float2half_rn(x)); }
@@ -214,7 +235,7 @@ __global__ __launch_bounds__(ROWS_THREADS) void quantise_rows_kernel(PlainArgs a
     const int L = threadIdx.x & 3;
     float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
     if (row < a.out.m && b < a.out.k / QK)
-        load_row8(a.x + (row * a.ld + b * QK + 8 * L) * (a.dt == ROW_F32 ? 4 : 2), a.dt, a.vec, v);
+        to_f32(load_raw8(a.x + (row * a.ld + b * QK + 8 * L) * row_size(a.dt), a.dt, a.vec), a.dt, v);
     emit_block<FMT>(v, L, row, b, a.out);
 }
 
@@ -275,12 +296,14 @@ template <int FMT, bool TILED>
 __global__ __launch_bounds__(ROWS_THREADS) void glu_rows_kernel(GluArgs a) {
     int64_t row, b;
     block_of_quad<TILED>(a.blocks, row, b);
-    const int L = threadIdx.x & 3, esz = a.dt == ROW_F32 ? 4 : 2;
+    const int L = threadIdx.x & 3, esz = row_size(a.dt);
     float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
     if (row < a.out.m && b < a.out.k / QK) {
         float g[8], u[8];
-        load_row8(a.gate + (row * a.ldg + b * QK + 8 * L) * esz, a.dt, a.vecg, g);
-        load_row8(a.up + (row * a.ldu + b * QK + 8 * L) * esz, a.dt, a.vecu, u);
+        const Raw8 rg = load_raw8(a.gate + (row * a.ldg + b * QK + 8 * L) * esz, a.dt, a.vecg);
+        const Raw8 ru = load_raw8(a.up + (row * a.ldu + b * QK + 8 * L) * esz, a.dt, a.vecu);
+        to_f32(rg, a.dt, g);
+        to_f32(ru, a.dt, u);
 #pragma unroll
         for (int t = 0; t < 8; t++) v[t] = gated(g[t], u[t], a.act);
     }
@@ -319,40 +342,60 @@ __device__ __forceinline__ double dpp_f64(double x) {
     const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROWS, 0xF, false);
     return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
-__device__ __forceinline__ double wave_sum(double x) {
+__device__ __forceinline__ double lane_f64(double x, int lane) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, lane);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double shifted_sum(double x) {  // lane 15 of each row of 16 gets the row's sum
     x += dpp_f64<0x111, 0xF>(x);  // row_shr:1
     x += dpp_f64<0x112, 0xF>(x);  // row_shr:2
     x += dpp_f64<0x114, 0xF>(x);  // row_shr:4
-    x += dpp_f64<0x118, 0xF>(x);  // row_shr:8: lane 15 of each row holds the row's sum
+    x += dpp_f64<0x118, 0xF>(x);  // row_shr:8
+    return x;
+}
+__device__ __forceinline__ double row_sum(double x) { return lane_f64(shifted_sum(x), 15); }  // of the first row
+__device__ __forceinline__ double wave_sum(double x) {
+    x = shifted_sum(x);
     x += dpp_f64<0x142, 0xA>(x);  // row_bcast:15 into rows 1 and 3
     x += dpp_f64<0x143, 0xC>(x);  // row_bcast:31 into rows 2 and 3
-    const uint64_t u = __builtin_bit_cast(uint64_t, x);
-    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, 63);
-    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), 63);
-    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+    return lane_f64(x, 63);
 }
 
-// This lane's 8 elements of h at column c of the row.
-__device__ __forceinline__ void norm_h8(const NormArgs &a, int64_t row, int64_t c, float v[8]) {
-    load_row8(a.x + (row * a.ldx + c) * (a.xdt == ROW_F32 ? 4 : 2), a.xdt, a.vecx, v);
+// What this lane loads for 8 elements at column c of the row, and h of them.
+struct NormRaw {
+    Raw8 x, r, w;
+};
+__device__ __forceinline__ NormRaw norm_load8(const NormArgs &a, int64_t row, int64_t c, bool weight) {
+    NormRaw n;
+    n.x = load_raw8(a.x + (row * a.ldx + c) * row_size(a.xdt), a.xdt, a.vecx);
+    if (a.residual) n.r = load_raw8(a.residual + (row * a.ldr + c) * row_size(a.rdt), a.rdt, a.vecr);
+    if (weight && a.weight) n.w = load_raw8(reinterpret_cast<const uint8_t *>(a.weight + c), ROW_F32, a.vecw);
+    return n;
+}
+__device__ __forceinline__ void norm_h8(const NormArgs &a, const NormRaw &n, float v[8]) {
+    to_f32(n.x, a.xdt, v);
     if (a.residual) {
         float r[8];
-        load_row8(a.residual + (row * a.ldr + c) * (a.rdt == ROW_F32 ? 4 : 2), a.rdt, a.vecr, r);
+        to_f32(n.r, a.rdt, r);
 #pragma unroll
         for (int t = 0; t < 8; t++) v[t] = __fadd_rn(v[t], r[t]);
     }
     round_row8(a.rdt, v);
 }
-__device__ __forceinline__ void norm_weight8(const NormArgs &a, int64_t c, float w[8]) {
-    if (a.weight) {
-        load8(a.weight + c, a.vecw ? 2 : 0, w);
-    } else {
+__device__ __forceinline__ void norm_scale8(const NormArgs &a, const Raw8 &weight, float rstd, float v[8]) {
 #pragma unroll
-        for (int t = 0; t < 8; t++) w[t] = 1.0f;
+    for (int t = 0; t < 8; t++) v[t] = __fmul_rn(v[t], rstd);
+    if (a.weight) {
+        float w[8];
+        to_f32(weight, ROW_F32, w);
+#pragma unroll
+        for (int t = 0; t < 8; t++) v[t] = __fmul_rn(v[t], w[t]);
     }
 }
 __device__ __forceinline__ void norm_store8(const NormArgs &a, int64_t row, int64_t c, const float v[8]) {
-    if (a.h) store_row8(a.h + (row * a.ldh + c) * (a.rdt == ROW_F32 ? 4 : 2), a.rdt, a.vech, v);
+    if (a.h) store_row8(a.h + (row * a.ldh + c) * row_size(a.rdt), a.rdt, a.vech, v);
 }
 __device__ __forceinline__ void zero8(float v[8]) {
 #pragma unroll
@@ -379,32 +422,30 @@ __global__ __launch_bounds__(1024) void norm_rows_kernel(NormArgs a, bool act) {
     const bool live = row < a.out.m;
 
     constexpr int HELD = CHUNKS ? CHUNKS : 1;
-    float v[HELD][8], w[HELD][8];
+    float v[HELD][8];
+    NormRaw raw[HELD];
     double sum = 0.0;
     if (live) {
         if constexpr (CHUNKS > 0) {
-            // the weights' loads too before the sum: the row waits for all of them once
+            // every load of the row, the weights' too, before the first wait
 #pragma unroll
             for (int i = 0; i < CHUNKS; i++) {
-                const int64_t b = i * quads + (tid >> 2), c = b * QK + 8 * L;
-                if (b < nb) {
-                    norm_h8(a, row, c, v[i]);
-                    norm_weight8(a, c, w[i]);
-                } else {
-                    zero8(v[i]);
-                    zero8(w[i]);
-                }
+                const int64_t b = i * quads + (tid >> 2);
+                if (b < nb) raw[i] = norm_load8(a, row, b * QK + 8 * L, true);
             }
 #pragma unroll
             for (int i = 0; i < CHUNKS; i++) {
                 const int64_t b = i * quads + (tid >> 2);
-                if (b < nb) norm_store8(a, row, b * QK + 8 * L, v[i]);
+                if (b < nb) {
+                    norm_h8(a, raw[i], v[i]);
+                    norm_store8(a, row, b * QK + 8 * L, v[i]);
 #pragma unroll
-                for (int t = 0; t < 8; t++) sum = fma((double)v[i][t], (double)v[i][t], sum);
+                    for (int t = 0; t < 8; t++) sum = fma((double)v[i][t], (double)v[i][t], sum);
+                }
             }
         } else {
             for (int64_t b = tid >> 2; b < nb; b += quads) {
-                norm_h8(a, row, b * QK + 8 * L, v[0]);
+                norm_h8(a, norm_load8(a, row, b * QK + 8 * L, false), v[0]);
                 norm_store8(a, row, b * QK + 8 * L, v[0]);
 #pragma unroll
                 for (int t = 0; t < 8; t++) sum = fma((double)v[0][t], (double)v[0][t], sum);
@@ -414,9 +455,9 @@ __global__ __launch_bounds__(1024) void norm_rows_kernel(NormArgs a, bool act) {
     sum = wave_sum(sum);
     if ((tid & 63) == 0) part[tid >> 6] = sum;
     __syncthreads();
-    sum = 0.0;
-#pragma unroll
-    for (int i = 0; i < 16; i++) sum += i < waves ? part[i] : 0.0;  // i < waves is uniform
+    // the waves' sums, one to a lane, in a fixed order (rows of 16 lanes hold the same)
+    sum = (tid & 15) < waves ? part[tid & 15] : 0.0;
+    sum = row_sum(sum);
     const float rstd = (float)rsqrt64(fma(sum, a.inv_k, a.eps));
 
     if constexpr (CHUNKS > 0) {
@@ -424,24 +465,19 @@ __global__ __launch_bounds__(1024) void norm_rows_kernel(NormArgs a, bool act) {
         for (int i = 0; i < CHUNKS; i++) {
             const int64_t b = i * quads + (tid >> 2);
             if (b >= blocks) continue;  // uniform per quad
-            if (live) {
-#pragma unroll
-                for (int t = 0; t < 8; t++) v[i][t] = __fmul_rn(__fmul_rn(v[i][t], rstd), w[i][t]);
-            } else {
-                zero8(v[i]);
-            }
+            if (live && b < nb) norm_scale8(a, raw[i].w, rstd, v[i]);
+            else zero8(v[i]);
             emit_block<FMT>(v[i], L, row, b, a.out);
         }
     } else {
         for (int64_t b = tid >> 2; b < blocks; b += quads) {
             if (live && b < nb) {
                 const int64_t c = b * QK + 8 * L;
+                raw[0] = norm_load8(a, row, c, true);
                 // this thread's own stores above, when h is written (it may be x or residual itself)
-                if (a.h) load_row8(a.h + (row * a.ldh + c) * (a.rdt == ROW_F32 ? 4 : 2), a.rdt, a.vech, v[0]);
-                else norm_h8(a, row, c, v[0]);
-                norm_weight8(a, c, w[0]);
-#pragma unroll
-                for (int t = 0; t < 8; t++) v[0][t] = __fmul_rn(__fmul_rn(v[0][t], rstd), w[0][t]);
+                if (a.h) to_f32(load_raw8(a.h + (row * a.ldh + c) * row_size(a.rdt), a.rdt, a.vech), a.rdt, v[0]);
+                else norm_h8(a, raw[0], v[0]);
+                norm_scale8(a, raw[0].w, rstd, v[0]);
             } else {
                 zero8(v[0]);
             }
@@ -497,7 +533,7 @@ __global__ __launch_bounds__(ROWS_THREADS) void read_rows_kernel(ReadArgs a) {
             }
         }
     }
-    store_row8(a.y + (row * a.ld + b * QK + 8 * L) * (a.dt == ROW_F32 ? 4 : 2), a.dt, a.vec, v);
+    store_row8(a.y + (row * a.ld + b * QK + 8 * L) * row_size(a.dt), a.dt, a.vec, v);
 }
 
 }  // namespace w4a4

@@ -137,13 +137,17 @@ template <int FMT, int CHUNKS>
 void launch_norm_chunks(const NormArgs &a, int64_t rows, int64_t threads, hipStream_t s) {
     norm_rows_kernel<FMT, CHUNKS><<<(unsigned)rows, (unsigned)threads, 0, s>>>(a, a.out.act != nullptr);
 }
-// A row's pieces of 8 elements over as many threads as a workgroup holds, in
-// 1, 2 or 4 pieces each; longer rows (past 32768) walk twice.
+// A row's pieces of 8 elements over a workgroup's threads, in 1, 2 or 4 pieces
+// each; rows past 32768 walk twice.  Few rows wait for one row's chain of loads,
+// sum and stores: as many threads as a workgroup holds (1 x 5120 3.5 us against
+// 4.2 with half).  With two rows a CU and more, fewer waves with two pieces each
+// do less of what every wave repeats (2048 x 5120 19.1 us against 21.2).
 template <int FMT>
 void launch_norm(const NormArgs &a, hipStream_t s) {
     const int64_t rows = rows_covered(FMT, a.out.act != nullptr, a.out.m);
     const int64_t pieces = blocks_covered(FMT, a.out.act != nullptr, a.out.k) * 4;
-    const int64_t chunks = pieces <= 1024 ? 1 : pieces <= 2048 ? 2 : pieces <= 4096 ? 4 : 0;
+    const int64_t most = rows >= 512 && pieces <= 4 * 512 ? 512 : 1024;
+    const int64_t chunks = pieces <= most ? 1 : pieces <= 2 * most ? 2 : pieces <= 4 * most ? 4 : 0;
     const int64_t threads = chunks ? ((pieces + chunks - 1) / chunks + 63) / 64 * 64 : 1024;
     switch (chunks) {
     case 1: return launch_norm_chunks<FMT, 1>(a, rows, threads, s);
