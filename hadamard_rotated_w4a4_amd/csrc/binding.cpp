@@ -179,9 +179,16 @@ Format format(int64_t f, int64_t m, int64_t k) {
     }
     refuse("unknown format " + str(f));
 }
+// A buffer given as a matrix has the format's width: its rows are the format's rows.
+void need_width(const at::Tensor &t, const char *name, int64_t cols) {
+    if (t.defined() && t.dim() == 2 && t.size(1) != cols)
+        refuse(std::string(name) + ": rows of " + str(t.size(1)) + ", expected " + str(cols));
+}
 void need_codes(const Format &f, const at::Tensor &codes, const at::Tensor &scales) {
     need(codes, "codes", f.code_type, f.m * f.code_cols);
     need(scales, "scales", f.scale_type, f.m * f.scale_cols * (f.scale_type == at::kFloat ? 4 : 1));
+    need_width(codes, "codes", f.code_cols);
+    need_width(scales, "scales", f.scale_cols);
 }
 void check_outputs(const Format &f, const at::Tensor &codes, const at::Tensor &scales, const at::Tensor &operand) {
     if (f.fmt == W4A4_ACT_INT4_SMALL && f.m > 16) refuse("ACT_INT4_SMALL: " + str(f.m) + " rows (at most 16)");

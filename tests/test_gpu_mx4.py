@@ -246,3 +246,71 @@ def test_results_do_not_depend_on_the_other_rows(ops):
     whole = ops.gemm_mx4(packed, ac, asc, n, k)
     for m in (1, 16, 33):
         assert torch.equal(ops.gemm_mx4(packed, ac[:m], asc[:m], n, k), whole[:m])
+
+
+def device_operand(g, rows, k):
+    """Random rows with scales of 2^-1 and 1, and their values in 64 bits; the
+    padding scale bytes hold 255."""
+    codes = torch.randint(0, 256, (rows, k // 2), dtype=torch.uint8, device="cuda", generator=g)
+    scales = torch.full((rows, twin.stride(k)), 255, dtype=torch.uint8, device="cuda")
+    scales[:, :k // 32] = torch.randint(126, 128, (rows, k // 32), dtype=torch.uint8, device="cuda", generator=g)
+    return codes, scales
+
+
+def values(ops, codes, scales, k):
+    return ops.dequantize_act(codes, scales, k, ops.ACT_MX4).double()
+
+
+# every tile shape, whole, with K splits and with the rest in a second shape;
+# streams of 16, 32 and 64 rows, short and long K, one and several row blocks
+PLANS = [(65, 5101, 17408), (130, 5101, 8224), (302, 10201, 96), (65, 34801, 96), (65, 10201, 17408), (302, 34801, 5152),
+         (200, 34801, 96), (400, 10201, 17408), (700, 17401, 96), (200, 17401, 17408), (400, 34801, 1056),
+         (700, 34801, 2080), (16, 9001, 5120), (9, 9001, 17408), (20, 9001, 5120), (27, 1000, 17408), (50, 8161, 5152),
+         (250, 2041, 5152), (1000, 481, 2080), (4090, 130, 544)]
+
+
+@pytest.mark.parametrize("m,n,k", PLANS)
+def test_product_of_every_plan(ops, m, n, k):
+    """Exact, as above: units of 2^-4, sums of 17408 random products of at
+    most 36 whole units of 1 stay far below 2^20."""
+    say(f"gemm_mx4 plan m={m} n={n} k={k}")
+    g = torch.Generator(device="cuda").manual_seed(m + n + k)
+    (ac, asc), (wc, wsc) = device_operand(g, m, k), device_operand(g, n, k)
+    packed = ops.repack_mx4(wc, wsc, n, k)
+    want = (values(ops, ac, asc, k) @ values(ops, wc, wsc, k).t().contiguous()).float()
+    for dtype in (torch.float32, torch.bfloat16):
+        y = torch.full((m + 1, n + 7), 7.0, dtype=dtype, device="cuda")
+        ops.gemm_mx4(packed, ac, asc, n, k, y=y[:m, :n])
+        torch.cuda.synchronize()
+        bad = (y[:m, :n] != want.to(dtype)).nonzero()
+        assert bad.numel() == 0, f"{dtype}: {bad.shape[0]} of {m * n} outputs differ, first at {bad[0].tolist()}"
+        assert (y[m:] == 7).all() and (y[:, n:] == 7).all()
+
+
+def test_outputs_past_32_bit_offsets(ops):
+    m, n, k = 33000, 34816, 96
+    say(f"gemm_mx4 4 GB outputs m={m} n={n} k={k}")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    (ac, asc), (wc, wsc) = device_operand(g, m, k), device_operand(g, n, k)
+    packed = ops.repack_mx4(wc, wsc, n, k)
+    y = ops.gemm_mx4(packed, ac, asc, n, k)
+    for at in (slice(0, 40), slice(2 ** 32 // (4 * n) - 20, 2 ** 32 // (4 * n) + 20), slice(m - 40, m)):
+        assert torch.equal(y[at], ops.gemm_mx4(packed, ac[at].clone(), asc[at].clone(), n, k)), at
+
+
+def test_weights_past_32_bit_offsets(ops):
+    n, k = 500000, 17408
+    say(f"repack_mx4 and gemm_mx4 4 GB weights n={n} k={k}")
+    g = torch.Generator(device="cuda").manual_seed(4)
+    wc, wsc = device_operand(g, n, k)
+    packed = ops.repack_mx4(wc, wsc, n, k)
+    assert packed.numel() > 2 ** 32
+    edge = 2 ** 32 // (k // 2)  # the plain codes' row there
+    last = 2 ** 32 // (packed.numel() // ((n + 31) // 32)) * 32  # the records' first row there
+    for m in (1, 30, 70):
+        ac, asc = device_operand(g, m, k)
+        y = ops.gemm_mx4(packed, ac, asc, n, k)
+        a = values(ops, ac, asc, k)
+        for at in (slice(0, 40), slice(edge - 20, edge + 20), slice(last - 20, last + 20), slice(n - 40, n)):
+            want = a @ values(ops, wc[at].clone(), wsc[at].clone(), k).t().contiguous()
+            assert torch.equal(y[:, at], want.float()), (m, at)

@@ -312,3 +312,53 @@ def test_empty_rows(ops):
     assert ops.quantize_mx4(z)[1].shape == (4, 0)
     assert ops.dequantize_act(torch.zeros((4, 0), dtype=torch.uint8, device="cuda"), torch.zeros((4, 0), dtype=torch.uint8, device="cuda"), 0, ops.ACT_MX4).shape == (4, 0)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("m,k", [(512, 4128), (515, 5120), (600, 8224), (511, 4128), (1030, 96)])
+def test_norm_of_many_rows(ops, m, k):
+    """From 512 rows a thread holds more of a row."""
+    say(f"rms_norm_quantize m={m} k={k}")
+    rng = np.random.default_rng(m + k)
+    x, xn = rows(rng, m, k, torch.float32)
+    r, rn = rows(rng, m, k, torch.bfloat16)
+    w = (1 + 0.1 * rng.standard_normal(k)).astype(np.float32)
+    hn, v = twin.norm(xn, rn, torch.bfloat16, w, 1e-6)
+    for fmt, operand in (("int8", False), ("int4", True)):
+        out = Outputs(ops, fmt, m, k, operand)
+        _, _, h = ops.rms_norm_quantize(x, torch.from_numpy(w).cuda(), 1e-6, FORMATS[fmt], residual=r, **out.args)
+        out.check(v)
+        assert np.array_equal(h.float().cpu().numpy(), hn)
+
+
+def test_rows_past_32_bit_offsets(ops):
+    """Tensors of more than 4 GB: the last rows and those around byte 2^32 are
+    what the same rows give in a call of their own."""
+    m, k = 65000, 17408
+    say(f"4 GB tensors m={m} k={k}")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.empty((m, k), device="cuda")
+    x.normal_(generator=g)
+    edge = 2 ** 32 // (4 * k)
+    spots = [slice(0, 5), slice(edge - 5, edge + 5), slice(m - 7, m)]
+    w = torch.rand(k, device="cuda", generator=g)
+
+    c, s = ops.quantize_mx4(x)
+    back = ops.dequantize_act(c, s, k, ops.ACT_MX4_H32)
+    for at in spots:
+        c1, s1 = ops.quantize_mx4(x[at].clone())
+        assert torch.equal(c[at], c1) and torch.equal(s[at], s1), at
+        assert torch.equal(back[at], ops.dequantize_act(c1, s1, k, ops.ACT_MX4_H32)), at
+    del back
+    c, s, h = ops.rms_norm_quantize(x, w, 1e-6, ops.ACT_INT8, residual=x)
+    for at in spots:
+        one = x[at].clone()
+        c1, s1, h1 = ops.rms_norm_quantize(one, w, 1e-6, ops.ACT_INT8, residual=one)
+        assert torch.equal(c[at], c1) and torch.equal(s[at], s1) and torch.equal(h[at], h1), at
+    del h
+    z = x.view(torch.bfloat16)  # 2 k wide: gate and up of a joint product
+    c, s = ops.glu_quantize(z[:, :k], z[:, k:], ops.ACT_MX4)
+    for at in spots:
+        one = z[at].clone()
+        c1, s1 = ops.glu_quantize(one[:, :k], one[:, k:], ops.ACT_MX4)
+        assert torch.equal(c[at], c1) and torch.equal(s[at], s1), at
+    torch.cuda.synchronize()

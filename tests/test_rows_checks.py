@@ -221,3 +221,35 @@ def test_binding_product_checks():
     raises("codes must be", ops.gemm_mx4, packed, c, s, N, 40)
     raises("codes: .* bytes", ops.repack_mx4, u8(N, K // 2 - 1), u8(N, 8), N, K)
     raises("out: .* bytes", ops.repack_mx4, u8(N, K // 2), u8(N, 8), N, K, out=packed[:-1])
+
+
+def test_binding_refuses_rows_of_another_width():
+    """Buffers large enough, but rows of another k's width."""
+    c, s = u8(M, K), u8(M, 8)
+    raises("codes: rows of 96, expected 48", ops.dequantize_act, c, s, K, ops.ACT_MX4)
+    raises("scales: rows of 16, expected 8", ops.dequantize_act, u8(M, K // 2), u8(M, 16), K, ops.ACT_MX4)
+    raises("scales: rows of 4, expected 3", ops.dequantize_act, zeros(M, K, dtype=torch.int8), zeros(M, 4), K, ops.ACT_INT8)
+    packed = u8(ops.mx4_packed_bytes(N, K))
+    raises("codes: rows of 96", ops.gemm_mx4, packed, c, s, N, K)
+    raises("scales: rows of 16", ops.gemm_mx4, packed, u8(M, K // 2), u8(M, 16), N, K)
+    raises("codes: rows of 96", ops.repack_mx4, u8(N, K), u8(N, 8), N, K)
+    raises("codes: rows of 96", ops.quantize_mx4, zeros(M, K), codes=c)
+    raises("scales: rows of 16", ops.glu_quantize, zeros(M, K), zeros(M, K), ops.ACT_MX4, scales=u8(M, 16))
+    raises(GPU_ONLY, ops.quantize_mx4, zeros(M, K), codes=u8(M * K), scales=u8(M + 3, 8))  # larger buffers are fine
+
+
+def test_mx4_product_workspace(L):
+    """The rows as records, and the partial sums where K is split; nothing for
+    the streamed sizes."""
+    size = L.w4a4_gemm_mx4_workspace_bytes
+    assert size(32, 17408, 5120) == 0 and size(64, 8192, 512) == 0 and size(0, 64, 64) == 0 and size(64, 0, 64) == 0
+    assert size(-1, 64, 64) == 0 and size(64, 64, 48) == 0 and size(64, 64, 0) == 0
+    rows = L.w4a4_mx4_packed_bytes(302, 64)
+    assert size(302, 10240, 64) == (rows + 255) // 256 * 256
+    split = size(65, 5120, 17408) - (L.w4a4_mx4_packed_bytes(65, 17408) + 255) // 256 * 256
+    assert split > 0 and split % (65 * 5120 * 4) == 0
+    f, need = L.w4a4_gemm_mx4, size(302, 10240, 64)
+    args = [P(A), P(A), P(A), P(A), F32, 302, 10240, 64, 10240]
+    assert f(*args, None, need, None) == INVALID
+    assert f(*args, P(A + 16), need, None) == MISALIGNED
+    assert f(*args, P(A), need - 1, None) == WS
