@@ -44,23 +44,13 @@ struct RowsOut {
 struct Raw8 {
     v4u lo, hi;
 };
-// vec: the address is 16-byte aligned.
-__device__ __forceinline__ Raw8 load_raw8(const uint8_t *p, int dt, bool vec) {
+// 16 bytes an instruction whatever the alignment of the rows: the hardware takes
+// any element-aligned address.
+typedef v4u v4u_any __attribute__((aligned(2)));
+__device__ __forceinline__ Raw8 load_raw8(const uint8_t *p, int dt) {
     Raw8 x;
-    if (vec) {
-        x.lo = *reinterpret_cast<const v4u *>(p);
-        if (dt == ROW_F32) x.hi = *reinterpret_cast<const v4u *>(p + 16);
-    } else if (dt == ROW_F32) {
-        const uint32_t *w = reinterpret_cast<const uint32_t *>(p);
-#pragma unroll
-        for (int i = 0; i < 4; i++) x.lo[i] = w[i];
-#pragma unroll
-        for (int i = 0; i < 4; i++) x.hi[i] = w[4 + i];
-    } else {
-        const uint16_t *h = reinterpret_cast<const uint16_t *>(p);
-#pragma unroll
-        for (int i = 0; i < 4; i++) x.lo[i] = (uint32_t)h[2 * i] | (uint32_t)h[2 * i + 1] << 16;
-    }
+    x.lo = *reinterpret_cast<const v4u_any *>(p);
+    if (dt == ROW_F32) x.hi = *reinterpret_cast<const v4u_any *>(p + 16);
     return x;
 }
 __device__ __forceinline__ void to_f32(const Raw8 &x, int dt, float v[8]) {
@@ -98,31 +88,22 @@ __device__ __forceinline__ void round_row8(int dt, float v[8]) {
     }
 }
 
-// Eight values rounded to type dt at byte address p.  vec: 16-byte aligned.
-__device__ __forceinline__ void store_row8(uint8_t *p, int dt, bool vec, const float v[8]) {
+// Eight values rounded to type dt at byte address p (element-aligned).
+__device__ __forceinline__ void store_row8(uint8_t *p, int dt, const float v[8]) {
+    v4u lo, hi;
     if (dt == ROW_F32) {
-        float *f = reinterpret_cast<float *>(p);
-        if (vec) {
-            reinterpret_cast<float4 *>(f)[0] = make_float4(v[0], v[1], v[2], v[3]);
-            reinterpret_cast<float4 *>(f)[1] = make_float4(v[4], v[5], v[6], v[7]);
-        } else {
 #pragma unroll
-            for (int i = 0; i < 8; i++) f[i] = v[i];
-        }
-        return;
-    }
-    uint16_t h[8];
-#pragma unroll
-    for (int i = 0; i < 8; i++) h[i] = dt == ROW_F16 ? f16_bits(v[i]) : bf16_bits(v[i]);
-    if (vec) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; i++) w[i] = (uint32_t)h[2 * i] | (uint32_t)h[2 * i + 1] << 16;
-        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int i = 0; i < 4; i++) lo[i] = __float_as_uint(v[i]), hi[i] = __float_as_uint(v[4 + i]);
+        reinterpret_cast<v4u_any *>(p)[1] = hi;
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; i++) reinterpret_cast<uint16_t *>(p)[i] = h[i];
+        for (int i = 0; i < 4; i++) {
+            const uint16_t a = dt == ROW_F16 ? f16_bits(v[2 * i]) : bf16_bits(v[2 * i]);
+            const uint16_t b = dt == ROW_F16 ? f16_bits(v[2 * i + 1]) : bf16_bits(v[2 * i + 1]);
+            lo[i] = (uint32_t)a | (uint32_t)b << 16;
+        }
     }
+    *reinterpret_cast<v4u_any *>(p) = lo;
 }
 
 // One block as MXFP4: e = floor(log2 max|v|) - 2 (at least -127), the codes
@@ -224,7 +205,6 @@ struct PlainArgs {
     const uint8_t *x;
     int64_t ld;  // elements
     int dt;
-    bool vec;
     RowBlocks blocks;
     RowsOut out;
 };
@@ -235,7 +215,7 @@ __global__ __launch_bounds__(ROWS_THREADS) void quantise_rows_kernel(PlainArgs a
     const int L = threadIdx.x & 3;
     float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
     if (row < a.out.m && b < a.out.k / QK)
-        to_f32(load_raw8(a.x + (row * a.ld + b * QK + 8 * L) * row_size(a.dt), a.dt, a.vec), a.dt, v);
+        to_f32(load_raw8(a.x + (row * a.ld + b * QK + 8 * L) * row_size(a.dt), a.dt), a.dt, v);
     emit_block<FMT>(v, L, row, b, a.out);
 }
 
@@ -288,7 +268,6 @@ struct GluArgs {
     const uint8_t *gate, *up;
     int64_t ldg, ldu;  // elements
     int dt, act;
-    bool vecg, vecu;
     RowBlocks blocks;
     RowsOut out;
 };
@@ -300,8 +279,8 @@ __global__ __launch_bounds__(ROWS_THREADS) void glu_rows_kernel(GluArgs a) {
     float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
     if (row < a.out.m && b < a.out.k / QK) {
         float g[8], u[8];
-        const Raw8 rg = load_raw8(a.gate + (row * a.ldg + b * QK + 8 * L) * esz, a.dt, a.vecg);
-        const Raw8 ru = load_raw8(a.up + (row * a.ldu + b * QK + 8 * L) * esz, a.dt, a.vecu);
+        const Raw8 rg = load_raw8(a.gate + (row * a.ldg + b * QK + 8 * L) * esz, a.dt);
+        const Raw8 ru = load_raw8(a.up + (row * a.ldu + b * QK + 8 * L) * esz, a.dt);
         to_f32(rg, a.dt, g);
         to_f32(ru, a.dt, u);
 #pragma unroll
@@ -329,7 +308,6 @@ struct NormArgs {
     int64_t ldx, ldr, ldh;        // elements
     double eps, inv_k;
     int xdt, rdt;
-    bool vecx, vecr, vech, vecw;
     RowsOut out;
 };
 
@@ -369,9 +347,9 @@ struct NormRaw {
 };
 __device__ __forceinline__ NormRaw norm_load8(const NormArgs &a, int64_t row, int64_t c, bool weight) {
     NormRaw n;
-    n.x = load_raw8(a.x + (row * a.ldx + c) * row_size(a.xdt), a.xdt, a.vecx);
-    if (a.residual) n.r = load_raw8(a.residual + (row * a.ldr + c) * row_size(a.rdt), a.rdt, a.vecr);
-    if (weight && a.weight) n.w = load_raw8(reinterpret_cast<const uint8_t *>(a.weight + c), ROW_F32, a.vecw);
+    n.x = load_raw8(a.x + (row * a.ldx + c) * row_size(a.xdt), a.xdt);
+    if (a.residual) n.r = load_raw8(a.residual + (row * a.ldr + c) * row_size(a.rdt), a.rdt);
+    if (weight && a.weight) n.w = load_raw8(reinterpret_cast<const uint8_t *>(a.weight + c), ROW_F32);
     return n;
 }
 __device__ __forceinline__ void norm_h8(const NormArgs &a, const NormRaw &n, float v[8]) {
@@ -395,7 +373,7 @@ __device__ __forceinline__ void norm_scale8(const NormArgs &a, const Raw8 &weigh
     }
 }
 __device__ __forceinline__ void norm_store8(const NormArgs &a, int64_t row, int64_t c, const float v[8]) {
-    if (a.h) store_row8(a.h + (row * a.ldh + c) * row_size(a.rdt), a.rdt, a.vech, v);
+    if (a.h) store_row8(a.h + (row * a.ldh + c) * row_size(a.rdt), a.rdt, v);
 }
 __device__ __forceinline__ void zero8(float v[8]) {
 #pragma unroll
@@ -475,7 +453,7 @@ __global__ __launch_bounds__(1024) void norm_rows_kernel(NormArgs a, bool act) {
                 const int64_t c = b * QK + 8 * L;
                 raw[0] = norm_load8(a, row, c, true);
                 // this thread's own stores above, when h is written (it may be x or residual itself)
-                if (a.h) to_f32(load_raw8(a.h + (row * a.ldh + c) * row_size(a.rdt), a.rdt, a.vech), a.rdt, v[0]);
+                if (a.h) to_f32(load_raw8(a.h + (row * a.ldh + c) * row_size(a.rdt), a.rdt), a.rdt, v[0]);
                 else norm_h8(a, raw[0], v[0]);
                 norm_scale8(a, raw[0].w, rstd, v[0]);
             } else {
@@ -496,7 +474,6 @@ struct ReadArgs {
     uint8_t *y;
     int64_t m, k, ld;  // ld: elements
     int dt;
-    bool vec;
     RowBlocks blocks;
 };
 template <int FMT>
@@ -533,7 +510,7 @@ __global__ __launch_bounds__(ROWS_THREADS) void read_rows_kernel(ReadArgs a) {
             }
         }
     }
-    store_row8(a.y + (row * a.ld + b * QK + 8 * L) * row_size(a.dt), a.dt, a.vec, v);
+    store_row8(a.y + (row * a.ld + b * QK + 8 * L) * row_size(a.dt), a.dt, v);
 }
 
 }  // namespace w4a4

@@ -23,8 +23,6 @@ inline bool known(w4a4_dtype t) { return t == W4A4_DTYPE_F32 || t == W4A4_DTYPE_
 inline int64_t size_of(w4a4_dtype t) { return t == W4A4_DTYPE_F32 ? 4 : 2; }
 inline bool known_format(int f) { return f >= FMT_INT4 && f <= FMT_MX4_H32; }
 inline bool is_mx4(int f) { return f == FMT_MX4 || f == FMT_MX4_H32; }
-// rows of ld elements of type t: every group of 8 elements 16-byte aligned
-inline bool vector_rows(const void *p, int64_t ld, w4a4_dtype t) { return aligned(p, 16) && ld * size_of(t) % 16 == 0; }
 
 // The quantised outputs of a producer: sizes known to be >= 0 and in bounds,
 // work to do.
@@ -75,7 +73,7 @@ w4a4_status w4a4_quantize_mx4(const void *x, w4a4_dtype dt, int64_t m, int64_t k
     if (m == 0 || k == 0) return W4A4_OK;
     if (!x) return W4A4_ERR_INVALID_VALUE;
     const int fmt = rotate ? FMT_MX4_H32 : FMT_MX4;
-    PlainArgs a{static_cast<const uint8_t *>(x), ldx, dt, vector_rows(x, ldx, dt), row_blocks(mx4_stride(k)),
+    PlainArgs a{static_cast<const uint8_t *>(x), ldx, dt, row_blocks(mx4_stride(k)),
                  RowsOut{codes, scales, nullptr, m, k}};
     const int64_t threads = m * mx4_stride(k) * 4;
     if (!grid_fits(threads + ROWS_THREADS)) return W4A4_ERR_INVALID_VALUE;
@@ -102,7 +100,7 @@ w4a4_status w4a4_dequantize_act(w4a4_act_format fmt, const void *codes, const vo
     if (!aligned(codes, 16) || !aligned(scales, is_mx4(fmt) ? 8 : 4) || !aligned(y, size_of(dt)))
         return W4A4_ERR_MISALIGNED;
     const ReadArgs a{static_cast<const uint8_t *>(codes), scales, static_cast<uint8_t *>(y), m, k, ldy, dt,
-                     vector_rows(y, ldy, dt), row_blocks(k / QK)};
+                     row_blocks(k / QK)};
     const unsigned grid = blocks_for(threads, ROWS_THREADS);
     hipStream_t s = as_stream(stream);
     switch (fmt) {
@@ -171,7 +169,7 @@ w4a4_status w4a4_glu_quantize(const void *gate, const void *up, w4a4_dtype dt, i
     if (m == 0 || k == 0) return W4A4_OK;
     if (!gate || !up) return W4A4_ERR_INVALID_VALUE;
     const GluArgs a{static_cast<const uint8_t *>(gate), static_cast<const uint8_t *>(up), ldg, ldu, dt, act,
-                    vector_rows(gate, ldg, dt), vector_rows(up, ldu, dt), row_blocks(blocks_covered(fmt, operand, k)),
+                    row_blocks(blocks_covered(fmt, operand, k)),
                     RowsOut{static_cast<uint8_t *>(codes), scales, static_cast<uint8_t *>(operand), m, k}};
     if (!grid_fits(rows_covered(fmt, operand, m) * blocks_covered(fmt, operand, k) * 4 + ROWS_THREADS))
         return W4A4_ERR_INVALID_VALUE;
@@ -203,8 +201,7 @@ w4a4_status w4a4_rms_norm_quantize(const void *x, w4a4_dtype xdt, int64_t ldx, c
     // in place: the same elements only
     if ((h == x && (xdt != rdt || ldh != ldx)) || (h && h == residual && ldh != ldr)) return W4A4_ERR_INVALID_VALUE;
     const NormArgs a{static_cast<const uint8_t *>(x), static_cast<const uint8_t *>(residual), weight,
-                     static_cast<uint8_t *>(h), ldx, ldr, ldh, eps, 1.0 / (double)k, xdt, rdt, vector_rows(x, ldx, xdt),
-                     vector_rows(residual, ldr, rdt), vector_rows(h, ldh, rdt), aligned(weight, 16),
+                     static_cast<uint8_t *>(h), ldx, ldr, ldh, eps, 1.0 / (double)k, xdt, rdt,
                      RowsOut{static_cast<uint8_t *>(codes), scales, static_cast<uint8_t *>(operand), m, k}};
     if (!grid_fits(rows_covered(fmt, operand, m) * 1024)) return W4A4_ERR_INVALID_VALUE;
     const w4a4_status st = check_outputs(fmt, a.out, operand_bytes);
