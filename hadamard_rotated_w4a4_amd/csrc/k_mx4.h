@@ -291,13 +291,12 @@ __global__ __launch_bounds__(C::NT) void gemm_mx4_tile_kernel(Mx4Args a) {
 #undef MX4_WAIT
 
     // ---- outputs.  A 32 x 32 tile's registers hold 32 columns of two rows per
-    // register: 128 contiguous bytes a row in fp32, stored as they are.  16-bit
-    // outputs go through the wave's own part of the LDS, a row of tiles at a
-    // time, and leave as 16 bytes per lane, 64 TN contiguous bytes a row.
+    // register: 128 contiguous bytes a row in fp32, stored as they are, and so are
+    // 16-bit outputs whose rows are not 16-byte aligned.  Those that are go through
+    // the wave's own part of the LDS, a row of tiles at a time, and leave as 16
+    // bytes per lane, 64 TN contiguous bytes a row.
     const int64_t col0 = (ct0 + wn * TN) * TILE_N;
-    if (a.dt == ROW_F32 || a.splits > 1) {
-        float *out = a.splits > 1 ? a.partial + z * a.m * a.n : reinterpret_cast<float *>(a.y);
-        const int64_t ld = a.splits > 1 ? a.n : a.ldy;
+    auto store_all = [&](auto store) {
 #pragma unroll
         for (int i = 0; i < TM; i++)
 #pragma unroll
@@ -307,15 +306,19 @@ __global__ __launch_bounds__(C::NT) void gemm_mx4_tile_kernel(Mx4Args a) {
 #pragma unroll
                 for (int v = 0; v < 16; v++) {
                     const int64_t o = row + mfma32_row(v, lane);
-                    if (o < a.m) out[o * ld + col] = acc[i][j][v];
+                    if (o < a.m) store(o, col, acc[i][j][v]);
                 }
             }
+    };
+    if (a.dt == ROW_F32 || a.splits > 1) {
+        float *out = a.splits > 1 ? a.partial + z * a.m * a.n : reinterpret_cast<float *>(a.y);
+        const int64_t ld = a.splits > 1 ? a.n : a.ldy;
+        store_all([&](int64_t row, int64_t col, float v) { out[row * ld + col] = v; });
         return;
     }
+    uint16_t *y = reinterpret_cast<uint16_t *>(a.y);
     constexpr int PIECES = TN * 4;  // of 16 bytes in a row
     uint16_t *mine = reinterpret_cast<uint16_t *>(smem) + wave * TN * 1024;
-    uint16_t *y = reinterpret_cast<uint16_t *>(a.y);
-    const bool vec = (reinterpret_cast<uintptr_t>(a.y) & 15) == 0 && a.ldy % 8 == 0;
 #pragma unroll
     for (int i = 0; i < TM; i++) {
 #pragma unroll
@@ -329,15 +332,14 @@ __global__ __launch_bounds__(C::NT) void gemm_mx4_tile_kernel(Mx4Args a) {
         for (int q = 0; q < 32 * PIECES / 64; q++) {
             const int lr = (q * 64 + lane) / PIECES, lc = (q * 64 + lane) % PIECES * 8;
             const int64_t row = (rt0 + wm * TM + i) * 32 + lr, col = col0 + lc;
-            const uint4 u = *reinterpret_cast<const uint4 *>(mine + lr * (TN * 32) + lc);
+            const v4u u = *reinterpret_cast<const v4u *>(mine + lr * (TN * 32) + lc);
             if (row >= a.m) continue;
-            if (vec && col + 8 <= a.n) {
-                *reinterpret_cast<uint4 *>(y + row * a.ldy + col) = u;
+            if (col + 8 <= a.n) {
+                *reinterpret_cast<v4u_any *>(y + row * a.ldy + col) = u;
             } else {
-                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
                 for (int e = 0; e < 8; e++)
-                    if (col + e < a.n) y[row * a.ldy + col + e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+                    if (col + e < a.n) y[row * a.ldy + col + e] = (uint16_t)(u[e >> 1] >> (16 * (e & 1)));
             }
         }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");

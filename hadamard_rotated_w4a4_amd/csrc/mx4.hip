@@ -72,6 +72,7 @@ void launch_streams(const Mx4Args &a, hipStream_t s) {
 using T64x64 = Mx4Cfg<2, 2, 1, 1, 2, 3>;
 using T64x128 = Mx4Cfg<2, 4, 1, 1, 2, 3>;
 using T128x128 = Mx4Cfg<2, 4, 2, 1, 1, 4>;
+using T160x128 = Mx4Cfg<5, 2, 1, 2, 1, 4>;
 using T256x192 = Mx4Cfg<4, 2, 2, 3, 1, 4>;
 using T256x256 = Mx4Cfg<4, 2, 2, 4, 1, 4>;
 
@@ -94,7 +95,8 @@ constexpr TileShape shape(int64_t per_cu, double alone, double full) {
     return TileShape{C::BM, C::BN, per_cu, alone, full, launch_tile<C>};
 }
 const TileShape kShapes[] = {shape<T64x64>(3, 0.17, 0.38), shape<T64x128>(2, 0.21, 0.50), shape<T128x128>(2, 0.40, 0.80),
-                             shape<T256x192>(1, 0.74, 1.00), shape<T256x256>(1, 0.86, 1.30)};
+                             shape<T160x128>(1, 0.34, 0.56), shape<T256x192>(1, 0.74, 1.00),
+                             shape<T256x256>(1, 0.86, 1.30)};
 
 // Modelled time of one launch: rounds of resident workgroups; a partial round
 // lies between the two times by how much of the chip it fills.

@@ -263,10 +263,12 @@ def values(ops, codes, scales, k):
 
 # every tile shape, whole, with K splits and with the rest in a second shape;
 # streams of 16, 32 and 64 rows, short and long K, one and several row blocks
-PLANS = [(65, 5101, 17408), (130, 5101, 8224), (302, 10201, 96), (65, 34801, 96), (65, 10201, 17408), (302, 34801, 5152),
-         (200, 34801, 96), (400, 10201, 17408), (700, 17401, 96), (200, 17401, 17408), (400, 34801, 1056),
-         (700, 34801, 2080), (16, 9001, 5120), (9, 9001, 17408), (20, 9001, 5120), (27, 1000, 17408), (50, 8161, 5152),
-         (250, 2041, 5152), (1000, 481, 2080), (4090, 130, 544)]
+PLANS = [(65, 5101, 17408), (130, 5101, 8224), (302, 10201, 96), (65, 34801, 96), (65, 10201, 17408),
+         (302, 34801, 5152), (200, 34801, 96), (400, 10201, 17408), (700, 17401, 96), (200, 17401, 17408),
+         (400, 34801, 1056), (700, 34801, 2080), (302, 5101, 17408), (300, 10208, 8224), (33, 17401, 17408),
+         (65, 8225, 17408), (450, 2081, 17408), (150, 34801, 5152), (1000, 5101, 17408), (400, 17401, 96),
+         (1000, 20513, 5152), (16, 9001, 5120), (9, 9001, 17408), (20, 9001, 5120), (27, 1000, 17408),
+         (50, 8161, 5152), (250, 2041, 5152), (1000, 481, 2080), (4090, 130, 544)]
 
 
 @pytest.mark.parametrize("m,n,k", PLANS)
