@@ -40,7 +40,8 @@ __host__ __device__ inline int64_t mx4_packed_bytes(int64_t n, int64_t k) {
     return padded_n(n) / TILE_N * mx4_rec_stages(k) * MX4_REC;
 }
 
-// One thread per (tile, stage, lane).
+// One thread per (tile, stage, lane).  Bound by memory for weights (5120 x 17408
+// 23 us, 4.1 TB/s) and by a launch's latency for rows (302 x 17408 3.6 us).
 __global__ __launch_bounds__(256) void repack_mx4_kernel(const uint8_t *__restrict__ codes,
                                                          const uint8_t *__restrict__ scales, int64_t n, int64_t k,
                                                          uint8_t *__restrict__ packed) {
@@ -114,6 +115,22 @@ __device__ __forceinline__ void mx4_store(uint8_t *y, int dt, int64_t i, float v
 // cycles whatever its width, and a wave waits while it is busy: so scales are
 // gathered into whole units, and a wave issues its loads one by one between
 // its MFMAs, not at the barrier.
+//
+// What bounds it: a 256 x 256 tile's slot holds 1024 matrix-core cycles a SIMD and
+// 770 cycles of LDS reads, and takes about 2600 cycles at 2.4 GHz where a launch
+// fills the chip: random codes draw so much power that the clock falls to 1.9 GHz
+// (512 x 32768 x 5120, one full round: 58 us, 3.0 PFLOP/s; with zero codes 48).
+// About 10 us of that are the start, the first loads and the output's way to
+// memory, which the one round leaves in the open.  Small tiles wait for LDS reads
+// and barriers: 302 x 5120 x 17408 in 160 x 128 tiles and three K splits spends
+// 25.7 us in the tiles, 5.7 in the sums and 3.6 in the rows' records.
+//
+// Tried and slower or no faster: the rows read in place instead of from records
+// (302 x 5120 x 17408 47.7 us against 38.9 with the same tiles: their 64- and
+// 128-byte pieces cost the address path what the records save); the weights
+// straight to registers (the same time, with a deeper chain of latencies); rings
+// of more slots; two groups of waves on halves of K; fragments waited for by
+// count instead of in full.
 // ---------------------------------------------------------------------------
 template <int WM_, int WN_, int TM_, int TN_, int KS_, int NS_>
 struct Mx4Cfg {
@@ -346,7 +363,8 @@ __global__ __launch_bounds__(C::NT) void gemm_mx4_tile_kernel(Mx4Args a) {
     }
 }
 
-// y = the splits' partial sums added in ascending order.
+// y = the splits' partial sums added in ascending order (the order is fixed: the
+// same inputs give the same bits).  302 x 5120, three splits: 5.7 us.
 __global__ __launch_bounds__(256) void mx4_reduce_kernel(Mx4Args a) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= a.m * a.n) return;
@@ -359,9 +377,14 @@ __global__ __launch_bounds__(256) void mx4_reduce_kernel(Mx4Args a) {
 // Few rows: the weights are streamed straight into registers, once per block of
 // ROWS rows.
 //
+// Bound by the weights' way from memory: 16 x 17408 x 5120 10.3 us, 48.9 MB, 4.7
+// TB/s (a copy reaches 5.15); 1 x 1024 x 5120, 32 workgroups and 2.8 MB, 3.8 us of
+// launch and load latency.
+//
 // A workgroup takes one 32-column tile (blockIdx.x) of one block of rows
-// (blockIdx.y) over the whole of K; its waves take the stages round-robin, each with its next DEPTH records in flight, and their
-// sums meet in LDS, added in wave order.  The rows' codes and scales are staged
+// (blockIdx.y) over the whole of K; its waves take the stages round-robin, each
+// with its next DEPTH records in flight, and their sums meet in LDS, added in wave
+// order.  The rows' codes and scales are staged
 // in LDS, CHUNK stages at a time (the LDS bounds how many workgroups share a
 // CU), the codes by direct loads issued before the weights': a row's four
 // 16-byte chunks of a stage lie at chunk ^ f(row), so that reading one chunk of

@@ -614,7 +614,10 @@ w4a4_status w4a4_glu_quantize(const void *gate, const void *up, w4a4_dtype dt, i
  *                  element-aligned; only the m x n block is written.
  *   workspace      w4a4_gemm_mx4_workspace_bytes(m, n, k) bytes, 256-byte
  *                  aligned (may be NULL when that is 0); contents on entry are
- *                  ignored, calls that share one must not overlap.
+ *                  ignored, calls that share one must not overlap, replays of
+ *                  captured calls among them.  It holds the rows in the
+ *                  weights' layout and, where K is split, the splits' fp32
+ *                  sums; m <= 32 and few columns need none.
  * k == 0 writes zeros.  Sizes and errors as w4a4_gemm.
  */
 size_t w4a4_mx4_packed_bytes(int64_t n, int64_t k);
