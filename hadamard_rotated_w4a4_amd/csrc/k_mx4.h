@@ -160,9 +160,8 @@ __device__ __forceinline__ T mx4_lds(const uint8_t *p) {
 // Tile of workgroup id, XCD-aware: workgroups are dealt to the 8 XCDs
 // round-robin, so ids x, x + 8, ... share an L2; the row tiles of a column
 // tile take ids x + 8 y and read its weights from HBM about once.
-__device__ __forceinline__ void mx4_tile_of(int64_t id, int64_t nx, int64_t ny, int64_t &bx, int64_t &by) {
-    const int64_t group = id / (8 * ny), in = id % (8 * ny);
-    const int64_t width = min((int64_t)8, nx - group * 8);
+__device__ __forceinline__ void mx4_tile_of(uint32_t id, uint32_t nx, uint32_t ny, uint32_t &bx, uint32_t &by) {
+    const uint32_t group = id / (8 * ny), in = id % (8 * ny), width = min(8u, nx - group * 8);
     bx = group * 8 + in % width;
     by = in / width;
 }
@@ -174,19 +173,22 @@ __global__ __launch_bounds__(C::NT) void gemm_mx4_tile_kernel(Mx4Args a) {
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / C::WN, wn = wave % C::WN, h = lane >> 5, r = lane & 31;
-    const int64_t rec_stages = mx4_rec_stages(a.k), slots = (mx4_stages(a.k) + KS - 1) / KS;
+    const int64_t rec_stages = mx4_rec_stages(a.k);
+    const uint32_t slots = (uint32_t)(mx4_stages(a.k) + KS - 1) / KS;  // of K: at most 2^17
     const int64_t rtiles = padded_n(a.m) / TILE_N, ctiles = padded_n(a.n) / TILE_N;
 
-    int64_t id = blockIdx.x, z = 0;
-    if (a.splits > 1) {
-        z = id % a.splits;
-        id /= a.splits;
+    // 32-bit index arithmetic: a 64-bit division takes hundreds of cycles, and the
+    // few here are ahead of the first load
+    uint32_t id = blockIdx.x, z = 0, bx, by;
+    const uint32_t splits = (uint32_t)a.splits;
+    if (splits > 1) {
+        z = id % splits;
+        id /= splits;
     }
-    int64_t bx, by;
-    mx4_tile_of(id, a.columns, (a.m + C::BM - 1) / C::BM, bx, by);
-    const int64_t rt0 = by * RT, ct0 = a.first + bx * CT;
-    const int64_t lo = z * slots / a.splits;
-    const int nst = (int)((z + 1) * slots / a.splits - lo);
+    mx4_tile_of(id, (uint32_t)a.columns, (uint32_t)((a.m + C::BM - 1) / C::BM), bx, by);
+    const int64_t rt0 = (int64_t)by * RT, ct0 = a.first + (int64_t)bx * CT;
+    const uint32_t lo = z * slots / splits;
+    const int nst = (int)((z + 1) * slots / splits - lo);
 
     // ---- this wave's loads: units wave, wave + WAVES, ...  Tiles past the
     // matrix are clamped (their outputs are not stored).
@@ -202,7 +204,7 @@ __global__ __launch_bounds__(C::NT) void gemm_mx4_tile_kernel(Mx4Args a) {
         const int t = min(piece / KS, RT + CT - 1), u = piece % KS;
         const uint8_t *side = t < RT ? a.rows : a.packed;
         const int64_t tile = t < RT ? min(rt0 + t, rtiles - 1) : min(ct0 + t - RT, ctiles - 1);
-        src[d] = side + (tile * rec_stages + lo * KS + u) * MX4_REC + at;
+        src[d] = side + (tile * rec_stages + (int64_t)lo * KS + u) * MX4_REC + at;
     }
     // load d of the next slot not yet asked for, into ring slot `into`
     auto load = [&](int d, int into) {
@@ -308,31 +310,30 @@ __global__ __launch_bounds__(C::NT) void gemm_mx4_tile_kernel(Mx4Args a) {
 #undef MX4_WAIT
 
     // ---- outputs.  A 32 x 32 tile's registers hold 32 columns of two rows per
-    // register: 128 contiguous bytes a row in fp32, stored as they are, and so are
-    // 16-bit outputs whose rows are not 16-byte aligned.  Those that are go through
-    // the wave's own part of the LDS, a row of tiles at a time, and leave as 16
-    // bytes per lane, 64 TN contiguous bytes a row.
-    const int64_t col0 = (ct0 + wn * TN) * TILE_N;
-    auto store_all = [&](auto store) {
+    // register: 128 contiguous bytes a row in fp32, stored as they are.  16-bit
+    // outputs go through the wave's own part of the LDS, a row of tiles at a time,
+    // and leave as 16 bytes per lane, 64 TN contiguous bytes a row.
+    if (a.dt == ROW_F32 || a.splits > 1) {
+        float *out = a.splits > 1 ? a.partial + z * a.m * a.n : reinterpret_cast<float *>(a.y);
+        const int64_t ld = a.splits > 1 ? a.n : a.ldy;
 #pragma unroll
         for (int i = 0; i < TM; i++)
 #pragma unroll
             for (int j = 0; j < TN; j++) {
-                const int64_t row = (rt0 + wm * TM + i) * 32, col = col0 + j * 32 + r;
-                if (col >= a.n) continue;
+                const int64_t row = (rt0 + wm * TM + i) * TILE_N, col = (ct0 + wn * TN + j) * TILE_N;
+                float *p = out + row * ld + col + (4 * h * ld + r);  // register v: row v % 4 + 8 (v / 4) + 4 h, column r
+                if (row + 32 <= a.m && col + 32 <= a.n) {
 #pragma unroll
-                for (int v = 0; v < 16; v++) {
-                    const int64_t o = row + mfma32_row(v, lane);
-                    if (o < a.m) store(o, col, acc[i][j][v]);
+                    for (int v = 0; v < 16; v++) p[(v % 4 + 8 * (v / 4)) * ld] = acc[i][j][v];
+                } else if (col + r < a.n) {
+#pragma unroll
+                    for (int v = 0; v < 16; v++)
+                        if (row + mfma32_row(v, lane) < a.m) p[(v % 4 + 8 * (v / 4)) * ld] = acc[i][j][v];
                 }
             }
-    };
-    if (a.dt == ROW_F32 || a.splits > 1) {
-        float *out = a.splits > 1 ? a.partial + z * a.m * a.n : reinterpret_cast<float *>(a.y);
-        const int64_t ld = a.splits > 1 ? a.n : a.ldy;
-        store_all([&](int64_t row, int64_t col, float v) { out[row * ld + col] = v; });
         return;
     }
+    const int64_t col0 = (ct0 + wn * TN) * TILE_N;
     uint16_t *y = reinterpret_cast<uint16_t *>(a.y);
     constexpr int PIECES = TN * 4;  // of 16 bytes in a row
     uint16_t *mine = reinterpret_cast<uint16_t *>(smem) + wave * TN * 1024;
