@@ -24,6 +24,8 @@
 // k / 32 by 127).
 #pragma once
 
+#include <type_traits>
+
 #include "common.h"
 #include "k_rows.h"
 
@@ -143,6 +145,12 @@ struct Mx4Cfg {
     static constexpr int SLOT = 1024 * UNITS;                     // bytes
     static constexpr int LOADS = (UNITS + WAVES - 1) / WAVES;     // of a slot, per wave: this many for the first
     static constexpr int FULL = UNITS - (LOADS - 1) * WAVES;      // FULL waves, one less for the others
+    // Loads and waits decided inside asm blocks, so that a slot is one scheduling
+    // region: its MFMAs issue ahead of its waits, behind the next slot's LDS reads.
+    // 64 x 64 tiles gain most (302 x 5120 x 17408 34.4 us against 38.5, 128 x 128
+    // 512 x 34816 x 5120 78 against 81).  Not for 8 tiles of 32 x 32 a wave, whose
+    // registers then spill (512 x 32768 x 5120 131 us against 63).
+    static constexpr bool STRAIGHT = TM * TN <= 6;
     static_assert(NS >= 3 && NS * SLOT <= 160 * 1024, "the ring fits the LDS");
     static_assert(2048 * TN * WAVES <= NS * SLOT, "so does a row of 16-bit output tiles per wave");
 };
@@ -152,6 +160,25 @@ struct Mx4Cfg {
 __device__ __forceinline__ void mx4_load16(const uint8_t *p, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(lds) : "memory");
 }
+// The same, if on (uniform); see Mx4Cfg::STRAIGHT.
+__device__ __forceinline__ void mx4_load16(const uint8_t *p, uint32_t lds, int on) {
+    asm volatile(
+        "s_cmp_eq_u32 %2, 0\n\ts_cbranch_scc1 1f\n\ts_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off\n1:" ::"v"(p),
+        "s"(lds), "s"(__builtin_amdgcn_readfirstlane(on))
+        : "memory", "scc");
+}
+// Until at most A (which = 0), B (which = 1) or no vector loads are in flight.
+template <int A, int B>
+__device__ __forceinline__ void mx4_wait(int which) {
+    asm volatile(
+        "s_cmp_eq_u32 %2, 0\n\ts_cbranch_scc0 1f\n\ts_waitcnt vmcnt(%0)\n\ts_branch 3f\n1:\n\ts_cmp_eq_u32 %2, 1\n\t"
+        "s_cbranch_scc0 2f\n\ts_waitcnt vmcnt(%1)\n\ts_branch 3f\n2:\n\ts_waitcnt vmcnt(0)\n3:" ::"n"(A),
+        "n"(B), "s"(__builtin_amdgcn_readfirstlane(which))
+        : "memory", "scc");
+}
+// Until this wave's LDS reads have returned, in a form that the compiler counts
+// (it would wait for them again at their first use, and for later ones with them).
+__device__ __forceinline__ void mx4_wait_lds() { __builtin_amdgcn_s_waitcnt(0xC07F); }
 template <class T>
 __device__ __forceinline__ T mx4_lds(const uint8_t *p) {
     return *reinterpret_cast<const volatile __attribute__((address_space(3))) T *>(
@@ -206,18 +233,34 @@ __global__ __launch_bounds__(C::NT) void gemm_mx4_tile_kernel(Mx4Args a) {
         const int64_t tile = t < RT ? min(rt0 + t, rtiles - 1) : min(ct0 + t - RT, ctiles - 1);
         src[d] = side + (tile * rec_stages + (int64_t)lo * KS + u) * MX4_REC + at;
     }
-    // load d of the next slot not yet asked for, into ring slot `into`
-    auto load = [&](int d, int into) {
-        if (d == L - 1 && !full) return;
-        mx4_load16(src[d], __builtin_amdgcn_readfirstlane(smem_base + into * C::SLOT + (wave + C::WAVES * d) * 1024));
+    // load d of the next slot not yet asked for, into ring slot `into`, if on (sure: it is)
+    auto load = [&](int d, int into, auto sure, int on) {
+        const uint32_t lds = __builtin_amdgcn_readfirstlane(smem_base + into * C::SLOT + (wave + C::WAVES * d) * 1024);
+        const bool every = d < L - 1 || C::FULL == C::WAVES;  // every wave has this load
+        if constexpr (C::STRAIGHT) {
+            if (every && decltype(sure)::value) mx4_load16(src[d], lds);
+            else mx4_load16(src[d], lds, every || full ? on : 0);
+        } else if (on && (every || full)) {
+            mx4_load16(src[d], lds);
+        }
         src[d] += KS * MX4_REC;
     };
-    // until at most n slots' loads are in flight
-#define MX4_WAIT(n)                                                                                  \
-    do {                                                                                             \
-        if (full) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((n) * L) : "memory");          \
-        else asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((n) * (L - 1)) : "memory");         \
-    } while (0)
+    // Until this wave's LDS reads are back and at most n slots' loads are in flight
+    // (on = 0: none), and the other waves are there.
+    auto wait = [&](auto n, int on) {
+        constexpr int A = decltype(n)::value * L, B = decltype(n)::value * (L - 1);
+        if constexpr (C::STRAIGHT) {
+            mx4_wait_lds();
+            mx4_wait<A, B>(!on ? 2 : full ? 0 : 1);
+        } else if (!on) {
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        } else if (full) {
+            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(A) : "memory");
+        } else {
+            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(B) : "memory");
+        }
+        __builtin_amdgcn_s_barrier();
+    };
 
     v16f acc[TM][TN];
 #pragma unroll
@@ -255,9 +298,9 @@ __global__ __launch_bounds__(C::NT) void gemm_mx4_tile_kernel(Mx4Args a) {
             for (int i = 0; i < TM; i++) f.a[q][i] = mx4_lds<v4u>(p + (wm * TM + i) * KS * 2048 + q * 1024);
         }
     };
-    // Slot s from cur, slot s + 1 into next, loads of slot s + NS.
-    auto slot = [&](int s, Fragments &cur, Fragments &next) {
-        const bool more = s + NS < nst;
+    // Slot s from cur, slot s + 1 into next, loads of slot s + NS (sure: there is one).
+    auto slot = [&](auto sure, int s, Fragments &cur, Fragments &next) {
+        const int more = decltype(sure)::value || s + NS < nst;
         const int into = s % NS;
         read(min(s + 1, nst - 1), next);
         __builtin_amdgcn_sched_barrier(0);
@@ -277,37 +320,36 @@ __global__ __launch_bounds__(C::NT) void gemm_mx4_tile_kernel(Mx4Args a) {
                     // the next loads, spread over the slot's MFMAs
                     constexpr int SPREAD = STEPS * TM * TN;
                     const int x = (q * TM + i) * TN + j;
-                    if (more) {
 #pragma unroll
-                        for (int d = 0; d < L; d++)
-                            if (d >= x * L / SPREAD && d < (x + 1) * L / SPREAD) load(d, into);
-                    }
+                    for (int d = 0; d < L; d++)
+                        if (d >= x * L / SPREAD && d < (x + 1) * L / SPREAD) load(d, into, sure, more);
                     __builtin_amdgcn_sched_barrier(0);
                 }
         }
-        if (more) MX4_WAIT(NS - 2);
-        else MX4_WAIT(0);
-        __builtin_amdgcn_s_barrier();
+        wait(std::integral_constant<int, NS - 2>{}, more);
     };
 #pragma unroll
     for (int s = 0; s < NS; s++)
-        if (s < nst)
 #pragma unroll
-            for (int d = 0; d < L; d++) load(d, s);
-    if (nst >= NS) MX4_WAIT(NS - 1);
-    else MX4_WAIT(0);
-    __builtin_amdgcn_s_barrier();
+        for (int d = 0; d < L; d++) load(d, s, std::false_type{}, s < nst);
+    wait(std::integral_constant<int, NS - 1>{}, nst >= NS);
     Fragments even, odd;
     read(0, even);
-    if (nst >= NS) MX4_WAIT(NS - 2);
-    else MX4_WAIT(0);
-    __builtin_amdgcn_s_barrier();
-    for (int s = 0; s < nst; s += 2) {
-        slot(s, even, odd);
-        if (s + 1 < nst) slot(s + 1, odd, even);
+    wait(std::integral_constant<int, NS - 2>{}, nst >= NS);
+    int s = 0;
+    if constexpr (C::STRAIGHT) {
+        for (; s + NS + 1 < nst; s += 2) {
+            slot(std::true_type{}, s, even, odd);
+            slot(std::true_type{}, s + 1, odd, even);
+        }
+    }
+    for (;;) {
+        slot(std::false_type{}, s, even, odd);
+        if (++s == nst) break;
+        slot(std::false_type{}, s, odd, even);
+        if (++s == nst) break;
     }
     __syncthreads();
-#undef MX4_WAIT
 
     // ---- outputs.  A 32 x 32 tile's registers hold 32 columns of two rows per
     // register: 128 contiguous bytes a row in fp32, stored as they are.  16-bit

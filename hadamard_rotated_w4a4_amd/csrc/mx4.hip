@@ -94,7 +94,7 @@ template <class C>
 constexpr TileShape shape(int64_t per_cu, double alone, double full) {
     return TileShape{C::BM, C::BN, per_cu, alone, full, launch_tile<C>};
 }
-const TileShape kShapes[] = {shape<T64x64>(3, 0.17, 0.38), shape<T64x128>(2, 0.21, 0.50), shape<T128x128>(2, 0.40, 0.80),
+const TileShape kShapes[] = {shape<T64x64>(3, 0.15, 0.36), shape<T64x128>(2, 0.21, 0.50), shape<T128x128>(2, 0.40, 0.80),
                              shape<T160x128>(1, 0.34, 0.56), shape<T256x192>(1, 0.74, 1.00),
                              shape<T256x256>(1, 0.86, 1.30)};
 
