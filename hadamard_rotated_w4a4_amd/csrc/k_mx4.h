@@ -123,16 +123,15 @@ __device__ __forceinline__ void mx4_store(uint8_t *y, int dt, int64_t i, float v
 // fills the chip: random codes draw so much power that the clock falls to 1.9 GHz
 // (512 x 32768 x 5120, one full round: 58 us, 3.0 PFLOP/s; with zero codes 48).
 // About 10 us of that are the start, the first loads and the output's way to
-// memory, which the one round leaves in the open.  Small tiles wait for LDS reads
-// and barriers: 302 x 5120 x 17408 in 160 x 128 tiles and three K splits spends
-// 25.7 us in the tiles, 5.7 in the sums and 3.6 in the rows' records.
+// memory, which the one round leaves in the open.  Small tiles wait for LDS reads,
+// the loads' writes there and barriers: 302 x 5120 x 17408 spends 30.7 us in 64 x
+// 64 tiles, 18 % of it in matrix instructions, and 3.9 in the rows' records.
 //
 // Tried and slower or no faster: the rows read in place instead of from records
 // (302 x 5120 x 17408 47.7 us against 38.9 with the same tiles: their 64- and
 // 128-byte pieces cost the address path what the records save); the weights
 // straight to registers (the same time, with a deeper chain of latencies); rings
-// of more slots; two groups of waves on halves of K; fragments waited for by
-// count instead of in full.
+// of more slots; two groups of waves on halves of K.
 // ---------------------------------------------------------------------------
 template <int WM_, int WN_, int TM_, int TN_, int KS_, int NS_>
 struct Mx4Cfg {

@@ -108,10 +108,11 @@ double tiles_time(const TileShape &t, int64_t tiles, double stages) {
 
 // The tiled product's launches: shape `a` over the first `columns` of its
 // column tiles with `splits` K splits, then shape `b` over the rest (none: -1).
-// The least modelled time wins.  Both sides, measured: 302 x 5120 x 17408 three
-// splits of 160 x 128 35.4 us, whole 64 x 128 39.3, 64 x 64 42.2; 512 x 34816 x
-// 5120 one round of 256 x 256 and the rest in 64 x 64 68 us, all in 256 x 192
-// 80; 200 x 17408 x 17408 three splits of 256 x 256 71.8, whole 128 x 128 88.4;
+// The least modelled time wins.  Both sides, measured: 302 x 5120 x 17408 64 x 64
+// 35.0 us, three splits of 160 x 128 35.5, 64 x 64 in two splits 43.2; 140 x 10240
+// x 17408 three splits of 160 x 128 39.0, 64 x 128 41.0, 64 x 64 43.1; 512 x 34816
+// x 5120 one round of 256 x 256 and the rest in 64 x 64 68 us, all in 256 x 192
+// 78; 200 x 17408 x 17408 three splits of 256 x 256 71.8, whole 128 x 128 88.4;
 // 2048 x 5120 x 5120 256 x 192 44.2.  Over 14 sizes the choice was 6 % slower than
 // the best of the shapes and splits tried on average, 22 % at worst (100 x 17408 x
 // 17408); K below about 1024 is where it errs most (up to 15 %).
