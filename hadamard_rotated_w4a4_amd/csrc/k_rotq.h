@@ -32,8 +32,9 @@ constexpr float kInvSqrt32f = 0x1.6a09e6p-3f;  // fp32(1/sqrt(32)), bits 0x3E350
 
 // x rounded to the nearest integer, ties away from zero, for |x| < 256: x plus
 // the number below one half (with x's sign), truncated.  The sum's own rounding
-// carries a tie to the next integer and nothing below one (checked for every
-// fp32 in the range).
+// carries a tie to the next integer and nothing below one: both sides are steps
+// that never fall, so they agree everywhere if they do on each tie and just
+// below it (tests/test_rounding.py).
 __device__ __forceinline__ int round_half_away(float x) {
     return (int)__fadd_rn(x, copysignf(0x1.fffffep-2f, x));
 }
@@ -128,10 +129,13 @@ __device__ __forceinline__ void quantise_values(float v[8], int L, int q[8], flo
     const bool nonzero = d >= 1.17549435e-38f;  // FLT_MIN: zero and subnormal scales give a zero block
     const float id = nonzero ? __fdiv_rn(1.0f, d) : 0.0f;
     s = !nonzero ? 0.0f : ROTATE ? __fmul_rn(d, kInvSqrt32f) : d;
-    // |v id| is at most QMAX (1 + 2^-22): it rounds to QMAX at most, and to 0
-    // where id is 0
+    // |v id| is at most QMAX (1 + 2^-22), so it rounds to QMAX at most with or
+    // without a clamp; a product that is NaN (an infinite d, a NaN among unrotated
+    // values) is clamped to the lower end, -QMAX, or 0 in a zero block (the median
+    // of three with a NaN among them is their least).
+    const float top = nonzero ? (float)QMAX : 0.0f;
 #pragma unroll
-    for (int t = 0; t < 8; t++) q[t] = round_half_away(__fmul_rn(v[t], id));
+    for (int t = 0; t < 8; t++) q[t] = round_half_away(__builtin_amdgcn_fmed3f(__fmul_rn(v[t], id), -top, top));
 }
 
 // quantise_values of a block in memory (lane L's elements 8L .. 8L + 7 at

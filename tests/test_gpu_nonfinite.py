@@ -1,0 +1,84 @@
+"""Infinities and NaN in quantised rows: what reaches a block, and what does not.
+
+Codes and scales are compared for equality with a plain form written here."""
+import numpy as np
+import pytest
+
+import rows_twin as twin
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+FORMATS = {"int4": 0, "int4_small": 1, "int8": 2, "mx4": 3, "mx4_h32": 4}
+INF, NAN = np.float32(np.inf), np.float32(np.nan)
+
+
+@pytest.fixture(scope="module")
+def ops():
+    from hadamard_rotated_w4a4_amd import _lib
+    _lib.lib()
+    return _lib
+
+
+def say(msg):
+    print(f"[gpu nonfinite] {msg}", flush=True)
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def int_rows(v, top, rotate, nan_scale):
+    """Blocks on the int4 or int8 grid, non-finite values included: a NaN product
+    of value and inverse scale takes code -top, unless the block is a zero
+    block.  nan_scale: a NaN among the block's values makes its scale NaN
+    (and zero codes); otherwise the maximum ignores it."""
+    with np.errstate(all="ignore"):
+        b = v.reshape(v.shape[0], -1, 32)
+        u = twin.butterflies(b) if rotate else b
+        a = np.abs(u)
+        amax = a.max(-1) if nan_scale else np.where(np.isnan(a), np.float32(0), a).max(-1)
+        d = amax / np.float32(top)
+        live = d >= np.float32(1.17549435e-38)
+        inv = np.where(live, np.float32(1) / np.where(live, d, np.float32(1)), np.float32(0)).astype(np.float32)
+        t = u * inv[..., None]
+        q = np.copysign(np.floor(np.abs(t.astype(np.float64)) + 0.5), t)
+        q = np.where(np.isnan(t), -top, np.clip(q, -top, top))
+        q = np.where(live[..., None], q, 0).astype(np.int8)
+        s = np.where(live, d * twin.C32 if rotate else d, np.where(np.isnan(d), d, np.float32(0)))
+    return q.reshape(v.shape), s.astype(np.float32)
+
+
+@pytest.mark.parametrize("call,top,rotate", [("rotate_quantize_act", 7, True), ("rotate_quantize_act8", 127, True), ("quantize_act", 7, False)])
+def test_quantisers_of_a_matrix_keep_their_codes(ops, call, top, rotate):
+    """The quantisers of a matrix in memory: a product that is NaN (an infinite
+    scale, or a NaN among unrotated values) has code -top, a block of NaN only
+    is a zero block."""
+    say(f"{call}")
+    x = np.random.default_rng(5).standard_normal((6, 128)).astype(np.float32)
+    x[0, 40], x[1, 33], x[2, 70] = INF, -INF, NAN
+    x[3, 0:2] = INF, -INF
+    x[4, 64:96] = NAN
+    x[5, :32] = 3e38 * np.sign(x[5, :32])  # sums of both signs overflow in the rotation
+    q, s = int_rows(x, top, rotate, False)
+    codes, scales = getattr(ops, call)(dev(x))
+    torch.cuda.synchronize()
+    assert np.array_equal(scales.cpu().numpy(), s, equal_nan=True)
+    assert np.array_equal(codes.cpu().numpy(), q if top == 127 else twin.int4_bytes(q))
+
+
+def test_int4_rounding_borders(ops):
+    """Values on and one fp32 either side of every half and whole step, against
+    an inverse scale of exactly 1: half away from zero."""
+    say("quantize_act borders")
+    edge = np.arange(0.5, 7.0, 0.5, dtype=np.float32)
+    near = np.concatenate((edge, np.nextafter(edge, INF), np.nextafter(edge, -INF), [np.float32(1e-30), np.float32(0.0)])).astype(np.float32)
+    near = np.insert(near, 31, 7.0)
+    x = np.zeros((2, 64), np.float32)
+    x[0, :near.size], x[1, :near.size] = near, -near
+    x[:, 63] = 7.0
+    q, s = int_rows(x, 7, False, False)
+    assert (s == 1).all()
+    codes, scales = ops.quantize_act(dev(x))
+    torch.cuda.synchronize()
+    assert np.array_equal(scales.cpu().numpy(), s) and np.array_equal(codes.cpu().numpy(), twin.int4_bytes(q))
