@@ -112,23 +112,30 @@ __device__ __forceinline__ void fwht32_quad(float v[8], int L) {
 
 // The values of one (row, block), held by a quad of lanes (lane L of the quad:
 // elements 8L .. 8L + 7 in v), quantised: the butterflies (unless ROTATE is
-// false), the absmax, the scale s and this lane's 8 codes.  Every lane of the
-// quad must take part (the butterflies and the absmax exchange values through
-// quad permutes).
-template <int QMAX, bool ROTATE>
+// false), the absmax, the scale s and this lane's 8 codes.  KEEP_NAN: a NaN among
+// the values makes s NaN, and an infinity s infinite, so that the block does not
+// read back as numbers; else the absmax ignores NaN.  Every lane of the quad must
+// take part (the butterflies and the absmax exchange values through quad
+// permutes).
+template <bool KEEP_NAN>
+__device__ __forceinline__ float larger(float a, float b) {
+    if constexpr (KEEP_NAN) return __builtin_elementwise_maximum(a, b);  // NaN if either is: v_maximum3_f32
+    else return fmaxf(a, b);
+}
+template <int QMAX, bool ROTATE, bool KEEP_NAN = false>
 __device__ __forceinline__ void quantise_values(float v[8], int L, int q[8], float &s) {
     if constexpr (ROTATE) fwht32_quad(v, L);
 
     float amax = 0.0f;
 #pragma unroll
-    for (int t = 0; t < 8; t++) amax = fmaxf(amax, fabsf(v[t]));
-    amax = fmaxf(amax, quad_f32<QP_XOR1>(amax));
-    amax = fmaxf(amax, quad_f32<QP_XOR2>(amax));
+    for (int t = 0; t < 8; t++) amax = larger<KEEP_NAN>(amax, fabsf(v[t]));
+    amax = larger<KEEP_NAN>(amax, quad_f32<QP_XOR1>(amax));
+    amax = larger<KEEP_NAN>(amax, quad_f32<QP_XOR2>(amax));
 
     const float d = __fdiv_rn(amax, (float)QMAX);
     const bool nonzero = d >= 1.17549435e-38f;  // FLT_MIN: zero and subnormal scales give a zero block
     const float id = nonzero ? __fdiv_rn(1.0f, d) : 0.0f;
-    s = !nonzero ? 0.0f : ROTATE ? __fmul_rn(d, kInvSqrt32f) : d;
+    s = !nonzero ? (KEEP_NAN && d != d ? d : 0.0f) : ROTATE ? __fmul_rn(d, kInvSqrt32f) : d;
     // |v id| is at most QMAX (1 + 2^-22), so it rounds to QMAX at most with or
     // without a clamp; a product that is NaN (an infinite d, a NaN among unrotated
     // values) is clamped to the lower end, -QMAX, or 0 in a zero block (the median

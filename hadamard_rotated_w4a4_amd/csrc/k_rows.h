@@ -157,7 +157,7 @@ __device__ __forceinline__ void emit_block(float v[8], int L, int64_t row, int64
         constexpr int QMAX = FMT == FMT_INT8 ? 127 : 7;
         int q[8];
         float s;
-        quantise_values<QMAX, true>(v, L, q, s);
+        quantise_values<QMAX, true, true>(v, L, q, s);
         store_quantised<QMAX>(q, s, L, row, b, o.m, o.k, o.codes, static_cast<float *>(o.scales),
                               FMT == FMT_INT4_SMALL ? nullptr : o.act, FMT == FMT_INT4_SMALL ? o.act : nullptr);
     }

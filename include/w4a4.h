@@ -503,6 +503,10 @@ w4a4_status w4a4_gemm_id_routed(const void *packed_w, int64_t n_expert, const ui
  *   W4A4_ACT_MX4         MXFP4 rows (w4a4_quantize_mx4), not rotated; no
  *                        operand (NULL).
  *   W4A4_ACT_MX4_H32     MXFP4 rows of the rotated blocks.
+ * A block whose values, after the rotation, hold a NaN or an infinity does not
+ * read back as numbers: MXFP4 scale byte 255; from the int4 and int8 producers
+ * a NaN scale with zero codes or, with infinities only, an infinite scale.
+ * Products give such a row no finite output.
  * The three size queries return the bytes of each buffer (0 for invalid
  * sizes, and where a format has no operand).  Host only, pure.
  */

@@ -1,6 +1,8 @@
 """Infinities and NaN in quantised rows: what reaches a block, and what does not.
 
-Codes and scales are compared for equality with a plain form written here."""
+The producers' codes and scales are compared for equality with a plain form
+written here; a block whose values are not all finite must not read back as
+finite numbers, and no other block may change."""
 import numpy as np
 import pytest
 
@@ -47,6 +49,43 @@ def int_rows(v, top, rotate, nan_scale):
         q = np.where(live[..., None], q, 0).astype(np.int8)
         s = np.where(live, d * twin.C32 if rotate else d, np.where(np.isnan(d), d, np.float32(0)))
     return q.reshape(v.shape), s.astype(np.float32)
+
+
+def check(fmt, codes, scales, v):
+    torch.cuda.synchronize()
+    c, s = codes.cpu().numpy(), scales.cpu().numpy()
+    if fmt.startswith("mx4"):
+        wc, ws = twin.mx4_rows(v, fmt == "mx4_h32")
+    else:
+        wc, ws = int_rows(v, 127 if fmt == "int8" else 7, True, True)
+        wc = twin.int4_bytes(wc) if fmt.startswith("int4") else wc
+    assert np.array_equal(s.reshape(ws.shape), ws, equal_nan=True), f"scales {s.reshape(ws.shape)[:, :6]}, expected {ws[:, :6]}"
+    assert np.array_equal(c.reshape(wc.shape), wc)
+
+
+def reads_non_finite(ops, fmt, codes, scales, k, blocks):
+    """Exactly the given (row, block) pairs read back as no finite number."""
+    f = ops.ACT_MX4 if fmt == "mx4" else FORMATS[fmt]
+    y = ops.dequantize_act(codes, scales, k, f).cpu().numpy().reshape(codes.shape[0], -1, 32)
+    lost = ~np.isfinite(y)
+    want = np.zeros(lost.shape[:2], bool)
+    for r, b in blocks:
+        want[r, b] = True
+    assert np.array_equal(lost.any(-1), want) and np.array_equal(lost.all(-1), want)
+
+
+@pytest.mark.parametrize("fmt", list(FORMATS))
+def test_norm_of_a_row_with_a_nan(ops, fmt):
+    say(f"rms_norm_quantize NaN {fmt}")
+    k = 160
+    x = np.random.default_rng(2).standard_normal((3, k)).astype(np.float32)
+    x[1, 7] = NAN
+    with np.errstate(all="ignore"):
+        _, v = twin.norm(x, None, torch.float32, None, 1e-6)
+    operand = torch.zeros(ops.act_format_operand_bytes(1, 3, k), dtype=torch.uint8, device="cuda") if fmt == "int4_small" else None
+    codes, scales, _ = ops.rms_norm_quantize(dev(x), None, 1e-6, FORMATS[fmt], operand=operand)
+    check(fmt, codes, scales, v)
+    reads_non_finite(ops, fmt, codes, scales, k, [(1, b) for b in range(5)])
 
 
 @pytest.mark.parametrize("call,top,rotate", [("rotate_quantize_act", 7, True), ("rotate_quantize_act8", 127, True), ("quantize_act", 7, False)])
