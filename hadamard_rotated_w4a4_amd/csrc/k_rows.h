@@ -390,9 +390,10 @@ __device__ __forceinline__ void zero8(float v[8]) {
     for (int t = 0; t < 8; t++) v[t] = 0.0f;
 }
 // 1 / sqrt(x) in fp64: the hardware root y, off by e = 1 - x y^2 (about 2^-23),
-// corrected as y (1 + e / 2 + 3 e^2 / 8).
+// corrected as y (1 + e / 2 + 3 e^2 / 8).  At infinity y is 0 and e would be NaN:
+// an infinity in a row makes its root 0.
 __device__ __forceinline__ double rsqrt64(double x) {
-    const double y = __builtin_amdgcn_rsq(x), e = fma(-(x * y), y, 1.0);
+    const double y = __builtin_amdgcn_rsq(x), e = y == 0.0 ? 0.0 : fma(-(x * y), y, 1.0);
     return fma(y * e, fma(0.375, e, 0.5), y);
 }
 

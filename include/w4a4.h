@@ -567,7 +567,9 @@ w4a4_status w4a4_dequantize_act(w4a4_act_format fmt, const void *codes, const vo
  *                                 fp64, one rounding: s does not depend on
  *                                 the order of the sum)
  *   v_i = fl(fl(h_i * s) * weight_i)            (fp32)
- * and v quantised in format fmt as the calls named above quantise x.
+ * and v quantised in format fmt as the calls named above quantise x.  An
+ * infinity in h makes s 0: its own block is lost (see the formats), the row's
+ * others are zero.  A NaN in h loses the row.
  *   x         [m][ldx] of type xdt.
  *   residual  [m][ldr] of type rdt, or NULL.
  *   weight    [k] fp32, or NULL for ones; 4-byte aligned.

@@ -75,6 +75,30 @@ def reads_non_finite(ops, fmt, codes, scales, k, blocks):
 
 
 @pytest.mark.parametrize("fmt", list(FORMATS))
+@pytest.mark.parametrize("k", [96, 5120, 8224, 32800])  # one, two and four pieces a thread, and rows walked twice
+def test_norm_of_a_row_that_overflows(ops, fmt, k):
+    """Finite inputs whose fp16 sum is infinite: the root is 0, the infinity's
+    own block is lost, the row's others are zero; other rows are untouched."""
+    say(f"rms_norm_quantize {fmt} k={k}")
+    rng = np.random.default_rng(k)
+    m = 4
+    x = rng.standard_normal((m, k)).astype(np.float32)
+    r = rng.standard_normal((m, k)).astype(np.float16)
+    x[1, 33], r[1, 33] = 60000, 60000
+    x[2, 64], r[2, 64] = -60000, -60000
+    w = (1 + 0.1 * rng.standard_normal(k)).astype(np.float32)
+    with np.errstate(all="ignore"):
+        hn, v = twin.norm(x, r.astype(np.float32), torch.float16, w, 1e-6)
+    assert np.isinf(hn[1, 33]) and np.isinf(hn[2, 64]) and np.isfinite(hn[[0, 3]]).all()
+    both = torch.zeros(ops.act_format_operand_bytes(FORMATS[fmt], m, k), dtype=torch.uint8, device="cuda")
+    for operand in ([both] if fmt == "int4_small" else [None] if fmt.startswith("mx4") else [None, both]):
+        codes, scales, h = ops.rms_norm_quantize(dev(x), dev(w), 1e-6, FORMATS[fmt], residual=dev(r), operand=operand)
+        assert np.array_equal(h.float().cpu().numpy(), hn)
+        check(fmt, codes, scales, v)
+        reads_non_finite(ops, fmt, codes, scales, k, [(1, 1), (2, 2)])
+
+
+@pytest.mark.parametrize("fmt", list(FORMATS))
 def test_norm_of_a_row_with_a_nan(ops, fmt):
     say(f"rms_norm_quantize NaN {fmt}")
     k = 160
