@@ -240,7 +240,8 @@ constexpr int GLU_SILU = 0, GLU_GELU_TANH = 1;  // w4a4_glu_act
 // exponent.  The quotient: the hardware reciprocal x of d, off by e = 1 - d x
 // (about 2^-23), corrected as x (1 + e + e^2).  g is clamped for the exponential
 // only, where fp64 would overflow past it (t within +-700: the result is u times
-// g or 0 in fp32 there).  About 22 fp64 operations an element.
+// g or 0 in fp32 there; a gate of minus infinity stays infinite).  About 22 fp64
+// operations an element.
 __device__ __forceinline__ float gated(float gate, float up, int act) {
     constexpr double kMagic = 0x1.8p52;
     double t;
@@ -266,8 +267,9 @@ __device__ __forceinline__ float gated(float gate, float up, int act) {
     const uint32_t lo = (uint32_t)__builtin_bit_cast(uint64_t, s);  // n as an integer
     const double d = 1.0 + __builtin_bit_cast(double, (uint64_t)((uint32_t)(bits >> 32) + (lo << 20)) << 32 | (uint32_t)bits);
     const double x = __builtin_amdgcn_rcp(d), e = fma(-d, x, 1.0);
-    const double v = (double)gate * (double)up * x;
-    return (float)fma(v, fma(e, e, e), v);
+    // the quotient corrected before the product (gate up is exact): an infinite
+    // gate or up stays infinite
+    return (float)((double)gate * (double)up * fma(x, fma(e, e, e), x));
 }
 
 struct GluArgs {

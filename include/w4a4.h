@@ -594,7 +594,9 @@ w4a4_status w4a4_rms_norm_quantize(const void *x, w4a4_dtype xdt, int64_t ldx, c
  * down projection, dense or per routed expert row): v = fp32(act(gate) * up),
  * with act(g) = g / (1 + e^-g) (W4A4_GLU_SILU) or its tanh-form GELU, g / (1 +
  * e^-2w), w = sqrt(2/pi) (g + 0.044715 g^3) (W4A4_GLU_GELU_TANH), evaluated in
- * fp64 to within 2^-40 and rounded once; then v quantised in format fmt.
+ * fp64 to within 2^-40 and rounded once; then v quantised in format fmt.  An
+ * infinite gate or up makes v an infinity (or a NaN, where the other factor is
+ * 0 or the gate is minus infinity): its block is lost, as the formats say.
  *   gate, up  [m][ldg], [m][ldu] of type dt (two column ranges of one packed
  *             gate|up product, or two matrices).
  * Other arguments and errors as w4a4_rms_norm_quantize.

@@ -112,6 +112,62 @@ def test_norm_of_a_row_with_a_nan(ops, fmt):
     reads_non_finite(ops, fmt, codes, scales, k, [(1, b) for b in range(5)])
 
 
+@pytest.mark.parametrize("fmt", list(FORMATS))
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+def test_glu_of_infinities_and_nan(ops, fmt, act):
+    say(f"glu_quantize {fmt} {act}")
+    m, k = 9, 128
+    rng = np.random.default_rng(3)
+    g, u = (rng.standard_normal((m, k)).astype(np.float32) for _ in range(2))
+    g[0, 40], u[0, 40] = INF, 0.5       # infinite
+    g[1, 40], u[1, 40] = 1.5, -INF
+    g[2, 0], u[2, 0] = 3e38, 3e38       # overflows in the one rounding to fp32
+    g[3, 70], u[3, 70] = INF, 0.0       # NaN
+    g[4, 70], u[4, 70] = 0.0, INF
+    g[5, 127] = NAN
+    u[6, 127] = NAN
+    g[7, 3], g[7, 4], u[7, 3:5] = INF, INF, (1.0, -1.0)  # two of opposite signs
+    with np.errstate(all="ignore"):
+        v = twin.gated(g, u, getattr(twin, act))
+    lost = [(0, 1), (1, 1), (2, 0), (3, 2), (4, 2), (5, 3), (6, 3), (7, 0)]
+    operand = torch.zeros(ops.act_format_operand_bytes(1, m, k), dtype=torch.uint8, device="cuda") if fmt == "int4_small" else None
+    a = ops.GLU_SILU if act == "silu" else ops.GLU_GELU_TANH
+    codes, scales = ops.glu_quantize(dev(g), dev(u), FORMATS[fmt], act=a, operand=operand)
+    check(fmt, codes, scales, v)
+    reads_non_finite(ops, fmt, codes, scales, k, lost)
+    # a gate of minus infinity: the formula has no value there
+    g[8, 100] = -INF
+    codes, scales = ops.glu_quantize(dev(g), dev(u), FORMATS[fmt], act=a, operand=operand)
+    reads_non_finite(ops, fmt, codes, scales, k, lost + [(8, 3)])
+
+
+@pytest.mark.parametrize("m", [5, 40])
+def test_an_overflow_reaches_the_product_of_the_operand(ops, m):
+    """Rows of a prepared product are lost with their block, and only those."""
+    say(f"glu_quantize -> prepared products, m={m}")
+    n, k = 64, 256
+    rng = np.random.default_rng(m)
+    g, u = (dev(rng.standard_normal((m, k)).astype(np.float32)) for _ in range(2))
+    packed = ops.prepare_weights(dev((rng.standard_normal((n, k)) * 0.02).astype(np.float32)))
+
+    def products():
+        out = []
+        for fmt in ([ops.ACT_INT4, ops.ACT_INT8] if m > 16 else [ops.ACT_INT4_SMALL]):
+            operand = torch.zeros(ops.act_format_operand_bytes(fmt, m, k), dtype=torch.uint8, device="cuda")
+            ops.glu_quantize(g, u, fmt, operand=operand)
+            f = {ops.ACT_INT4: ops.gemm_prepared, ops.ACT_INT8: ops.gemm_a8_prepared, ops.ACT_INT4_SMALL: ops.gemm_prepared_small}[fmt]
+            out.append(f(packed, operand, m, n, k).cpu().numpy())
+        return out
+
+    clean = products()
+    g[2, 37], u[2, 37] = float("inf"), 1.0
+    g[4, 200] = float("nan")
+    for y, want in zip(products(), clean):
+        hit = np.zeros(m, bool)
+        hit[[2, 4]] = True
+        assert not np.isfinite(y[hit]).any() and np.array_equal(y[~hit], want[~hit])
+
+
 @pytest.mark.parametrize("call,top,rotate", [("rotate_quantize_act", 7, True), ("rotate_quantize_act8", 127, True), ("quantize_act", 7, False)])
 def test_quantisers_of_a_matrix_keep_their_codes(ops, call, top, rotate):
     """The quantisers of a matrix in memory: a product that is NaN (an infinite
