@@ -93,6 +93,7 @@ def lib() -> ctypes.CDLL:
             "w4a4_mx4_packed_bytes": ([I64, I64], SZ),
             "w4a4_repack_mx4": ([P, P, I64, I64, P, P], ST),
             "w4a4_gemm_mx4_workspace_bytes": ([I64, I64, I64], SZ),
+            "w4a4_gemm_mx4_plan": ([I64, I64, I64, ctypes.c_char_p, SZ], SZ),
             "w4a4_gemm_mx4": ([P, P, P, P, ST, I64, I64, I64, I64, P, SZ, P], ST),
         }
         for name, (args, res) in sigs.items():
@@ -686,6 +687,14 @@ def mx4_packed_bytes(n: int, k: int) -> int:
 
 def gemm_mx4_workspace_bytes(m: int, n: int, k: int) -> int:
     return int(lib().w4a4_gemm_mx4_workspace_bytes(m, n, k))
+
+
+def gemm_mx4_plan(m: int, n: int, k: int) -> str:
+    """The kernels that gemm_mx4 launches for these sizes (include/w4a4.h); ""
+    for empty or invalid sizes."""
+    text = ctypes.create_string_buffer(64)
+    lib().w4a4_gemm_mx4_plan(m, n, k, text, len(text))
+    return text.value.decode()
 
 
 def act_format_operand_bytes(fmt: int, m: int, k: int) -> int:

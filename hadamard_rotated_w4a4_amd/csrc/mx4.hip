@@ -3,6 +3,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <cstdio>
 
 #include "abi.h"
 #include "common.h"
@@ -59,13 +60,18 @@ void launch_stream(const Mx4Args &a, hipStream_t s) {
 // with several workgroups on a CU the tiles' reuse wins (64 x 17408 x 5120 21
 // against 16).
 bool streams(int64_t m, int64_t n) { return m <= 32 || (m + 63) / 64 * (padded_n(n) / TILE_N) <= kPlanCus; }
-void launch_streams(const Mx4Args &a, hipStream_t s) {
-    const bool few = padded_n(a.n) / TILE_N <= kPlanCus;
-    if (a.m > 32) launch_stream<Stream64Few>(a, s);
-    else if (a.m > 16 && few) launch_stream<Stream32Few>(a, s);
-    else if (a.m > 16) launch_stream<Stream32>(a, s);
-    else if (a.k > 5120) launch_stream<Stream16LongK>(a, s);
-    else launch_stream<Stream16>(a, s);
+struct StreamShape {
+    int rows, waves;
+    void (*launch)(const Mx4Args &, hipStream_t);
+};
+template <class C>
+constexpr StreamShape stream_shape() {
+    return StreamShape{C::ROWS, C::WAVES, launch_stream<C>};
+}
+StreamShape stream_plan(int64_t m, int64_t n, int64_t k) {
+    if (m > 32) return stream_shape<Stream64Few>();
+    if (m > 16) return padded_n(n) / TILE_N <= kPlanCus ? stream_shape<Stream32Few>() : stream_shape<Stream32>();
+    return k > 5120 ? stream_shape<Stream16LongK>() : stream_shape<Stream16>();
 }
 
 // Tile shapes of the tiled product.
@@ -158,6 +164,23 @@ size_t w4a4_gemm_mx4_workspace_bytes(int64_t m, int64_t n, int64_t k) {
     return up256_bytes(mx4_packed_bytes(m, k)) + (p.splits > 1 ? up256_bytes(p.splits * m * n * 4) : 0);
 }
 
+size_t w4a4_gemm_mx4_plan(int64_t m, int64_t n, int64_t k, char *text, size_t bytes) {
+    if (bytes) text[0] = 0;
+    if (m <= 0 || n <= 0 || k <= 0 || k % QK || !within_bounds(m, n, k)) return 0;
+    int len;
+    if (streams(m, n)) {
+        const StreamShape c = stream_plan(m, n, k);
+        len = std::snprintf(text, bytes, "stream %dx%d", c.rows, c.waves);
+    } else {
+        const TilePlan p = tile_plan(m, n, k);
+        const TileShape &a = kShapes[p.a], &b = kShapes[p.b < 0 ? 0 : p.b];
+        if (p.b >= 0) len = std::snprintf(text, bytes, "tile %dx%d + %dx%d", (int)a.bm, (int)a.bn, (int)b.bm, (int)b.bn);
+        else if (p.splits > 1) len = std::snprintf(text, bytes, "tile %dx%d split %d", (int)a.bm, (int)a.bn, (int)p.splits);
+        else len = std::snprintf(text, bytes, "tile %dx%d", (int)a.bm, (int)a.bn);
+    }
+    return (size_t)len;
+}
+
 w4a4_status w4a4_gemm_mx4(const void *packed_w, const uint8_t *codes, const uint8_t *scales, void *y, w4a4_dtype ydt,
                           int64_t m, int64_t n, int64_t k, int64_t ldy, void *workspace, size_t workspace_bytes,
                           void *stream) {
@@ -195,7 +218,7 @@ w4a4_status w4a4_gemm_mx4(const void *packed_w, const uint8_t *codes, const uint
     a.dt = ydt;
     a.splits = 1;
     if (streams(m, n)) {
-        launch_streams(a, s);
+        stream_plan(m, n, k).launch(a, s);
         return hip_status("gemm_mx4_stream_kernel");
     }
     const w4a4_status st = w4a4_repack_mx4(codes, scales, m, k, workspace, stream);

@@ -627,11 +627,21 @@ w4a4_status w4a4_glu_quantize(const void *gate, const void *up, w4a4_dtype dt, i
  *                  weights' layout and, where K is split, the splits' fp32
  *                  sums; m <= 32 and few columns need none.
  * k == 0 writes zeros.  Sizes and errors as w4a4_gemm.
+ *
+ * w4a4_gemm_mx4_plan: the kernels that w4a4_gemm_mx4 launches for these sizes,
+ * for tests and measurements, as a line of text in `text` (at most bytes - 1
+ * characters and a zero; may be NULL when bytes is 0): "stream RxW" (weights
+ * streamed for blocks of R rows, W waves a workgroup), "tile MxN", "tile MxN
+ * split S" (S splits of K, then their sum) or "tile MxN + PxQ" (whole rounds of
+ * one shape, the remaining columns in another).  Returns the text's length; 0
+ * for empty or invalid sizes.  The names may change with the kernels.  Host
+ * only, pure.
  */
 size_t w4a4_mx4_packed_bytes(int64_t n, int64_t k);
 w4a4_status w4a4_repack_mx4(const uint8_t *codes, const uint8_t *scales, int64_t n, int64_t k, void *packed,
                             void *stream);
 size_t w4a4_gemm_mx4_workspace_bytes(int64_t m, int64_t n, int64_t k);
+size_t w4a4_gemm_mx4_plan(int64_t m, int64_t n, int64_t k, char *text, size_t bytes);
 w4a4_status w4a4_gemm_mx4(const void *packed_w, const uint8_t *codes, const uint8_t *scales, void *y, w4a4_dtype ydt,
                           int64_t m, int64_t n, int64_t k, int64_t ldy, void *workspace, size_t workspace_bytes,
                           void *stream);
