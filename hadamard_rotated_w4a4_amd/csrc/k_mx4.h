@@ -157,14 +157,14 @@ struct Mx4Cfg {
 // One global-to-LDS load of 16 bytes per lane: the 16 bytes at lane l's p land
 // at LDS byte address lds + 16 l (lds is uniform).
 __device__ __forceinline__ void mx4_load16(const uint8_t *p, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(lds) : "memory");
+    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(lds) : "memory", "m0");
 }
 // The same, if on (uniform); see Mx4Cfg::STRAIGHT.
 __device__ __forceinline__ void mx4_load16(const uint8_t *p, uint32_t lds, int on) {
     asm volatile(
         "s_cmp_eq_u32 %2, 0\n\ts_cbranch_scc1 1f\n\ts_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off\n1:" ::"v"(p),
         "s"(lds), "s"(__builtin_amdgcn_readfirstlane(on))
-        : "memory", "scc");
+        : "memory", "m0", "scc");
 }
 // Until at most A (which = 0), B (which = 1) or no vector loads are in flight.
 template <int A, int B>

@@ -1,0 +1,68 @@
+"""What the compiler made of the kernels' inline assembly, read from the assembly
+of code built here (CPU only: hipcc cross-compiles)."""
+import os
+import re
+import subprocess
+
+import pytest
+
+pytest.importorskip("torch")
+
+from hadamard_rotated_w4a4_amd import build as hip  # noqa: E402
+
+
+def assembly(source, out):
+    """Device assembly of a .hip file, with the library's own flags."""
+    flags = [f for f in hip.FLAGS if f not in ("-shared", "-fPIC")]
+    subprocess.run([hip.HIPCC, *flags, "-I", os.path.join(hip.ROOT, "include"), "-I", hip.CSRC, "--cuda-device-only", "-S",
+                    "-o", str(out), str(source)], check=True, capture_output=True, text=True)
+    return open(out).read()
+
+
+def instructions(text, kernel):
+    """(instruction lines of a kernel, whether each came from inline assembly)."""
+    body = text[text.index(f"\n{kernel}:"):]
+    body = body[:body.index("s_endpgm")]
+    lines, inline = [], False
+    for line in body.splitlines():
+        if "#ASMSTART" in line or "#ASMEND" in line:
+            inline = "#ASMSTART" in line
+            continue
+        line = line.split(";")[0].strip()
+        if line and not line.startswith(".") and not line.endswith(":"):
+            lines.append((line, inline))
+    return lines
+
+
+PROBE = """
+#include "common.h"
+#include "{header}"
+using namespace w4a4;
+typedef const __attribute__((address_space(1))) void global;
+typedef __attribute__((address_space(3))) void shared;
+extern "C" __global__ void probe(const uint8_t *p, uint8_t *y, int on) {{
+    __shared__ uint8_t smem[4096];
+    const uint32_t base = (uint32_t)(uintptr_t)(shared *)smem;
+    __builtin_amdgcn_global_load_lds((global *)(p + 4 * threadIdx.x), (shared *)(smem + 1024), 4, 0, 0);
+    {load};
+    __builtin_amdgcn_global_load_lds((global *)(p + 256 + 4 * threadIdx.x), (shared *)(smem + 1024), 4, 0, 0);
+    __builtin_amdgcn_s_waitcnt(0);
+    y[threadIdx.x] = smem[threadIdx.x] + smem[1024 + threadIdx.x];
+}}
+"""
+
+
+@pytest.mark.parametrize("header,load", [("k_mx4.h", "mx4_load16(p + 16 * threadIdx.x, base)"),
+                                         ("k_mx4.h", "mx4_load16(p + 16 * threadIdx.x, base, on)"),
+                                         ("k_dense.h", "dma16s(p, 16 * threadIdx.x, base)")])
+def test_direct_loads_say_that_they_write_m0(tmp_path, header, load):
+    """Between two of the compiler's own direct loads to one LDS address, one of
+    ours to another: the compiler must set M0 again after it."""
+    source = tmp_path / "probe.hip"
+    source.write_text(PROBE.format(header=header, load=load))
+    code = instructions(assembly(source, tmp_path / "probe.s"), "probe")
+    ours = [i for i, (line, inline) in enumerate(code) if inline and "load_lds" in line]
+    later = [i for i, (line, inline) in enumerate(code) if not inline and "load_lds" in line and i > ours[-1]]
+    assert len(ours) == 1 and len(later) == 1
+    between = [line for line, inline in code[ours[0] + 1:later[0]] if not inline]
+    assert any(re.match(r"s_\w+ m0,", line) for line in between), between
