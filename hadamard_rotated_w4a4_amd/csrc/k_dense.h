@@ -217,7 +217,8 @@ __device__ __forceinline__ T lds_read(const uint8_t *p) {
 // through M0).  The base is wave-uniform (SGPRs) and voff a per-lane 32-bit
 // byte offset, so no 64-bit vector address arithmetic is needed per load.
 __device__ __forceinline__ void dma16s(const uint8_t *sbase, uint32_t voff, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(sbase), "s"(lds) : "memory", "m0");
+    uint32_t m0;  // written
+    asm volatile("s_mov_b32 m0, %3\n\tglobal_load_lds_dwordx4 %1, %2" : "={m0}"(m0) : "v"(voff), "s"(sbase), "s"(lds) : "memory");
 }
 
 // A wave-uniform pointer, placed in SGPRs.  (The builtin returns a signed

@@ -157,14 +157,17 @@ struct Mx4Cfg {
 // One global-to-LDS load of 16 bytes per lane: the 16 bytes at lane l's p land
 // at LDS byte address lds + 16 l (lds is uniform).
 __device__ __forceinline__ void mx4_load16(const uint8_t *p, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(lds) : "memory", "m0");
+    uint32_t m0;  // written
+    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %1, off" : "={m0}"(m0) : "v"(p), "s"(lds) : "memory");
 }
 // The same, if on (uniform); see Mx4Cfg::STRAIGHT.
 __device__ __forceinline__ void mx4_load16(const uint8_t *p, uint32_t lds, int on) {
+    uint32_t m0;
     asm volatile(
-        "s_cmp_eq_u32 %2, 0\n\ts_cbranch_scc1 1f\n\ts_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off\n1:" ::"v"(p),
-        "s"(lds), "s"(__builtin_amdgcn_readfirstlane(on))
-        : "memory", "m0", "scc");
+        "s_cmp_eq_u32 %3, 0\n\ts_cbranch_scc1 1f\n\ts_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %1, off\n1:"
+        : "={m0}"(m0)
+        : "v"(p), "s"(lds), "s"(__builtin_amdgcn_readfirstlane(on))
+        : "memory", "scc");
 }
 // Until at most A (which = 0), B (which = 1) or no vector loads are in flight.
 template <int A, int B>
