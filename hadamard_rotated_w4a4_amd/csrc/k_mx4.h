@@ -486,6 +486,13 @@ __global__ __launch_bounds__(C::NT) void gemm_mx4_stream_kernel(Mx4Args a) {
                                                           (int64_t)(t0 + t) * MX4_BLOCKS);
         }
     };
+    // Until the chunk's scales are there and with them its codes, whose loads are
+    // older and return in order.  The compiler counts the loads behind them (the
+    // weights' at the start, which stay in flight).
+    auto wait_rows = [&] {
+#pragma unroll
+        for (int j = 0; j < HELD; j++) asm volatile("" ::"v"(held[j]) : "memory");
+    };
     auto store_scales = [&](int t0, int cnt) {
         uint32_t *scl = reinterpret_cast<uint32_t *>(smem + cnt * ROWS * MX4_ROW_BYTES);
 #pragma unroll
@@ -507,7 +514,7 @@ __global__ __launch_bounds__(C::NT) void gemm_mx4_stream_kernel(Mx4Args a) {
     const int first = min(CHUNK, stages);
     stage_codes(0, first);
     load_scales(0, first);
-    asm volatile("" ::: "memory");  // in this order: the waits for the rows leave the weights in flight
+    asm volatile("" ::: "memory");  // in this order: the wait for the rows leaves the weights in flight
 #pragma unroll
     for (int d = 0; d < DEPTH; d++) load(wave + WAVES * d, ring[d]);
 
@@ -517,16 +524,16 @@ __global__ __launch_bounds__(C::NT) void gemm_mx4_stream_kernel(Mx4Args a) {
 #pragma unroll
         for (int v = 0; v < 16; v++) acc[i][v] = 0.0f;
     const int sw = mx4_swizzle(ar);
+    wait_rows();
     for (int t0 = 0; t0 < stages; t0 += CHUNK) {
         const int cnt = min(CHUNK, stages - t0);
         if (t0) {
             __syncthreads();  // every wave is done with the last chunk
             stage_codes(t0, cnt);
             load_scales(t0, cnt);
+            wait_rows();
         }
         store_scales(t0, cnt);
-        if (t0) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        else asm volatile("s_waitcnt vmcnt(%0)" ::"n"(3 * DEPTH) : "memory");
         __syncthreads();
         const uint8_t *scl = smem + cnt * ROWS * MX4_ROW_BYTES;
         for (int t = t0 + wave; t < t0 + cnt; t += WAVES * DEPTH) {

@@ -66,3 +66,30 @@ def test_direct_loads_say_that_they_write_m0(tmp_path, header, load):
     assert len(ours) == 1 and len(later) == 1
     between = [line for line, inline in code[ours[0] + 1:later[0]] if not inline]
     assert any(re.match(r"s_\w+ m0,", line) for line in between), between
+
+
+@pytest.fixture(scope="module")
+def product(tmp_path_factory):
+    """Assembly of the MXFP4 product's kernels."""
+    return assembly(os.path.join(hip.CSRC, "mx4.hip"), tmp_path_factory.mktemp("code") / "mx4.s")
+
+
+def kernels(text, name):
+    return sorted(set(re.findall(rf"^(_ZN4w4a4\d+{name}\w*):", text, re.M)))
+
+
+def test_streams_wait_for_their_rows_by_a_load_that_follows_them(product):
+    """A stream's first barrier needs the rows' codes in LDS, direct loads that the
+    compiler does not count.  It waits for the scales, loaded after the codes
+    (loads return in order): by waits of the compiler's own, which count what it
+    issued behind them, and by no count of ours."""
+    names = kernels(product, "gemm_mx4_stream_kernel")
+    assert len(names) == 5
+    for name in names:
+        code = instructions(product, name)
+        assert not [line for line, inline in code if inline and "s_waitcnt" in line], name
+        first = next(i for i, (line, _) in enumerate(code) if line == "s_barrier")
+        direct = max(i for i, (line, _) in enumerate(code[:first]) if "load_lds" in line)
+        behind = [line for line, _ in code[direct + 1:first] if re.match(r"(global|buffer|flat)_(load|store)", line)]
+        waits = [int(re.search(r"vmcnt\((\d+)\)", line).group(1)) for line, _ in code[direct + 1:first] if "vmcnt" in line]
+        assert waits and min(waits) < len(behind), f"{name}: {len(behind)} loads behind the codes, waits {waits}"
