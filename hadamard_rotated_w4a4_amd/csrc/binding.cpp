@@ -112,13 +112,28 @@ c10::Device one_device(std::initializer_list<const at::Tensor *> ts) {
     return first->device();
 }
 
+// Makes a device current for its own lifetime, also where that ends by an exception.
+class Current {
+  public:
+    explicit Current(c10::Device device) : before(c10::hip::current_device()), other(before != device.index()) {
+        if (other) c10::hip::set_device(device.index());
+    }
+    ~Current() {
+        if (other) (void)c10::hip::MaybeSetDevice(before);  // it was current: no failure to report
+    }
+    Current(const Current &) = delete;
+    Current &operator=(const Current &) = delete;
+
+  private:
+    const c10::DeviceIndex before;
+    const bool other;
+};
+
 // Calls f(stream) with the device current, on its current stream.
 template <class F>
 void call(const char *name, c10::Device device, F f) {
-    const auto before = c10::hip::current_device();
-    if (before != device.index()) c10::hip::set_device(device.index());
+    const Current current(device);
     const w4a4_status st = f((void *)c10::hip::getCurrentHIPStream(device.index()).stream());
-    if (before != device.index()) c10::hip::set_device(before);
     if (st == W4A4_OK) return;
     const std::string detail = st == W4A4_ERR_HIP ? w4a4_last_hip_error() : "";
     refuse(std::string(name) + ": " + w4a4_status_string(st) + (detail.empty() ? "" : " (" + detail + ")"));
