@@ -1,11 +1,13 @@
 """Build libw4a4.so (hipcc, gfx950) and the native binding _native.so (g++,
-host code only) in-tree.
+host code only; needs PyTorch's headers) in-tree.
 
     python -m hadamard_rotated_w4a4_amd.build
 """
 from __future__ import annotations
 
+import importlib.util
 import os
+import shutil
 import subprocess
 import sys
 import sysconfig
@@ -17,6 +19,7 @@ LIB = os.path.join(PKG, "libw4a4.so")
 CEILINGS_LIB = os.path.join(PKG, "libw4a4_ceilings.so")  # measured ceilings for the benchmark
 NATIVE = os.path.join(PKG, "_native.so")  # the binding's native part
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+CXX = os.environ.get("CXX", "g++")  # the native binding's host compiler
 
 SOURCES = [os.path.join(CSRC, f) for f in ("w4a4.hip", "rows.hip", "mx4.hip")]
 HEADERS = [os.path.join(CSRC, h) for h in ("abi.h", "common.h", "k_prep.h", "k_rotq.h", "k_route.h", "k_dense.h", "k_smallm.h", "k_grouped.h", "k_w16.h",
@@ -43,25 +46,47 @@ FLAGS = [
 
 def build(verbose: bool = False) -> str:
     """Compile the HIP sources into libw4a4.so and the ceiling probes into
-    libw4a4_ceilings.so, then the native binding (always recompiles)."""
+    libw4a4_ceilings.so, then the native binding (always recompiles).  The C
+    libraries need hipcc only: without PyTorch and its headers they are built
+    and the binding is left out, with a note."""
     _compile(LIB, SOURCES, verbose)
     _compile(CEILINGS_LIB, [os.path.join(CSRC, "ceilings.hip")], verbose)
-    _compile_native(verbose)
+    home = _pytorch()
+    if home is None:
+        print("PyTorch's headers not found: libw4a4.so is built, the Python binding's _native.so is not", flush=True)
+    else:
+        _compile_native(home, verbose)
     return LIB
 
 
-def _compile_native(verbose: bool) -> None:
-    """csrc/binding.cpp against PyTorch's headers and libw4a4.so beside it."""
-    import torch
-    home = os.path.dirname(torch.__file__)
+def _pytorch():
+    """The folder of the PyTorch package with its headers, or None."""
+    spec = importlib.util.find_spec("torch")
+    home = os.path.dirname(spec.origin) if spec and spec.origin else None
+    header = home and os.path.join(home, "include", "torch", "csrc", "autograd", "python_variable.h")
+    return home if header and os.path.exists(header) else None
+
+
+def _rocm_include() -> str:
+    """The HIP headers of the ROCm that HIPCC belongs to."""
+    path = shutil.which(HIPCC) or HIPCC
+    for hipcc in (path, os.path.realpath(path)):  # <rocm>/bin/hipcc, itself or behind a link
+        include = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(hipcc))), "include")
+        if os.path.exists(os.path.join(include, "hip", "hip_runtime.h")):
+            return include
+    raise RuntimeError(f"no HIP headers beside {HIPCC}")
+
+
+def _compile_native(home: str, verbose: bool) -> None:
+    """csrc/binding.cpp against the headers of PyTorch at `home` and libw4a4.so."""
     includes = [os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
-                sysconfig.get_paths()["include"], "/opt/rocm/include", os.path.join(ROOT, "include")]
+                sysconfig.get_paths()["include"], _rocm_include(), os.path.join(ROOT, "include")]
     libs = os.path.join(home, "lib")
     tmp = NATIVE + ".tmp"
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
-           *(f"-isystem{i}" for i in includes), "-o", tmp, os.path.join(CSRC, "binding.cpp"), f"-L{PKG}", "-l:" + os.path.basename(LIB), f"-L{libs}", "-ltorch_python",
-           "-ltorch", "-ltorch_cpu", "-ltorch_hip", "-lc10", "-lc10_hip", f"-Wl,-rpath,$ORIGIN:{libs}"]
-    _run(cmd, "g++", verbose)
+    cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           *(f"-isystem{i}" for i in includes), "-o", tmp, os.path.join(CSRC, "binding.cpp"), f"-L{PKG}", "-l:" + os.path.basename(LIB),
+           f"-L{libs}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_hip", "-lc10", "-lc10_hip", f"-Wl,-rpath,$ORIGIN:{libs}"]
+    _run(cmd, CXX, verbose)
     os.replace(tmp, NATIVE)
 
 
