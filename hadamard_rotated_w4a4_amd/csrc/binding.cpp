@@ -58,9 +58,16 @@ int64_t integer(PyObject *o) {
     if (v == -1 && PyErr_Occurred()) throw PythonError{};
     return v;
 }
-int64_t width(int64_t k) {
-    if (k < 0 || k % 32) refuse("k = " + str(k) + " is not a multiple of 32");
+// The library's own bounds, here so that the sizes computed from k and n fit 64 bits.
+int64_t width(int64_t k, const char *more = "") {
+    if (k < 0 || k % 32) refuse(more + ("k = " + str(k) + " is not a multiple of 32"));
+    if (k > int64_t{1} << 24) refuse("k = " + str(k) + ", at most 2^24");
     return k;
+}
+int64_t columns(int64_t n) {
+    if (n < 0) refuse("n = " + str(n) + " is negative");
+    if (n > int64_t{1} << 26) refuse("n = " + str(n) + ", at most 2^26");
+    return n;
 }
 // The k of an optional argument, x's width by default.
 int64_t width_of(PyObject *k, const at::Tensor &x) { return width(k == Py_None ? x.size(1) : integer(k)); }
@@ -320,8 +327,7 @@ PyObject *glu_quantize(PyObject *const *a) {
 // codes, scales, n, k, out -> out
 PyObject *repack_mx4(PyObject *const *a) {
     const at::Tensor &codes = required(a[0], "codes"), &scales = required(a[1], "scales");
-    const int64_t n = integer(a[2]), k = width(integer(a[3]));
-    if (n < 0) refuse("n = " + str(n) + " is negative");
+    const int64_t n = columns(integer(a[2])), k = width(integer(a[3]));
     need_codes(format(W4A4_ACT_MX4, n, k), codes, scales);
     at::Tensor out = tensor(a[4], "out");
     const int64_t size = (int64_t)w4a4_mx4_packed_bytes(n, k);
@@ -337,9 +343,7 @@ PyObject *repack_mx4(PyObject *const *a) {
 // packed, codes, scales, n, k, y, workspace, dtype -> y
 PyObject *gemm_mx4(PyObject *const *a) {
     const at::Tensor &packed = required(a[0], "packed"), &codes = matrix(a[1], "codes"), &scales = required(a[2], "scales");
-    const int64_t n = integer(a[3]), k = integer(a[4]), m = codes.size(0);
-    if (k < 0 || k % 32) refuse("codes must be rows of whole blocks: k = " + str(k) + " is not a multiple of 32");
-    if (n < 0) refuse("n = " + str(n) + " is negative");
+    const int64_t m = codes.size(0), k = width(integer(a[4]), "codes must be rows of whole blocks: "), n = columns(integer(a[3]));
     need(packed, "packed", at::kByte, m && n ? (int64_t)w4a4_mx4_packed_bytes(n, k) : 0);
     need_codes(format(W4A4_ACT_MX4, m, k), codes, scales);
     at::Tensor y = tensor(a[5], "y"), workspace = tensor(a[6], "workspace");

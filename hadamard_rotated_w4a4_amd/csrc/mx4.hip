@@ -14,7 +14,7 @@ using namespace w4a4;
 extern "C" {
 
 size_t w4a4_mx4_packed_bytes(int64_t n, int64_t k) {
-    if (n < 0 || k < 0 || k % QK) return 0;
+    if (n < 0 || k < 0 || k % QK || !within_bounds(0, n, k)) return 0;
     return (size_t)mx4_packed_bytes(n, k);
 }
 

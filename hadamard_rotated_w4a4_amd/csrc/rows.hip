@@ -22,6 +22,10 @@ namespace {
 inline bool known(w4a4_dtype t) { return t == W4A4_DTYPE_F32 || t == W4A4_DTYPE_F16 || t == W4A4_DTYPE_BF16; }
 inline int64_t size_of(w4a4_dtype t) { return t == W4A4_DTYPE_F32 ? 4 : 2; }
 inline bool known_format(int f) { return f >= FMT_INT4 && f <= FMT_MX4_H32; }
+// what the size queries take: beyond it no call does, and a size may not fit 64 bits
+inline bool sizes_valid(int f, int64_t m, int64_t k) {
+    return known_format(f) && m >= 0 && m <= kMaxN && k >= 0 && k <= kMaxK && k % QK == 0;
+}
 inline bool is_mx4(int f) { return f == FMT_MX4 || f == FMT_MX4_H32; }
 
 // The quantised outputs of a producer: sizes known to be >= 0 and in bounds,
@@ -42,21 +46,22 @@ w4a4_status check_outputs(int fmt, const RowsOut &o, size_t act_bytes) {
 extern "C" {
 
 size_t w4a4_mx4_scale_stride(int64_t k) {
-    if (k < 0 || k % QK) return 0;
+    if (k < 0 || k % QK || k > kMaxK) return 0;
     return (size_t)mx4_stride(k);
 }
 
 size_t w4a4_act_format_code_bytes(w4a4_act_format fmt, int64_t m, int64_t k) {
-    if (!known_format(fmt) || m < 0 || k < 0 || k % QK) return 0;
+    if (!sizes_valid(fmt, m, k)) return 0;
     return (size_t)(fmt == W4A4_ACT_INT8 ? m * k : m * (k / 2));
 }
 
 size_t w4a4_act_format_scale_bytes(w4a4_act_format fmt, int64_t m, int64_t k) {
-    if (!known_format(fmt) || m < 0 || k < 0 || k % QK) return 0;
+    if (!sizes_valid(fmt, m, k)) return 0;
     return (size_t)(is_mx4(fmt) ? m * mx4_stride(k) : m * (k / QK) * 4);
 }
 
 size_t w4a4_act_format_operand_bytes(w4a4_act_format fmt, int64_t m, int64_t k) {
+    if (!sizes_valid(fmt, m, k)) return 0;
     switch (fmt) {
     case W4A4_ACT_INT4: return w4a4_act_operand_bytes(m, k);
     case W4A4_ACT_INT4_SMALL: return w4a4_small_act_operand_bytes(m, k);
