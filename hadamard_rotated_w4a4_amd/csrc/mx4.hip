@@ -88,9 +88,11 @@ void launch_tile(const Mx4Args &a, hipStream_t s) {
     gemm_mx4_tile_kernel<C><<<(unsigned)tiles, C::NT, 0, s>>>(a);
 }
 
-// What the plan knows of a shape: its size, how many workgroups a CU holds
-// (their LDS rings decide), and the measured time of one stage (128 of K), in
-// us, of a workgroup on an otherwise idle chip and of a full round.
+// What the plan knows of a shape: its size, how many workgroups a CU holds (the
+// LDS rings decide, but for 160 x 128: two of its rings fit, and its registers
+// leave 4 waves a SIMD where two workgroups of 10 waves need 5), and the measured
+// time of one stage (128 of K), in us, of a workgroup on an otherwise idle chip
+// and of a full round.
 struct TileShape {
     int64_t bm, bn, per_cu;
     double alone, full;

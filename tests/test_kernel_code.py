@@ -93,3 +93,21 @@ def test_streams_wait_for_their_rows_by_a_load_that_follows_them(product):
         behind = [line for line, _ in code[direct + 1:first] if re.match(r"(global|buffer|flat)_(load|store)", line)]
         waits = [int(re.search(r"vmcnt\((\d+)\)", line).group(1)) for line, _ in code[direct + 1:first] if "vmcnt" in line]
         assert waits and min(waits) < len(behind), f"{name}: {len(behind)} loads behind the codes, waits {waits}"
+
+
+def test_the_plan_counts_the_workgroups_that_a_cu_holds(product):
+    """kShapes' workgroups per CU against the kernels' LDS and registers (160 KB of
+    LDS; 512 VGPRs a SIMD in groups of 8 to at most 8 waves, four SIMDs)."""
+    host = open(os.path.join(hip.CSRC, "mx4.hip")).read()
+    configs = dict(re.findall(r"using (T\w+) = Mx4Cfg<([\d, ]+)>;", host))
+    per_cu = dict(re.findall(r"shape<(T\w+)>\((\d+),", host))
+    assert len(configs) == 6 and per_cu.keys() == configs.keys()
+    for shape, args in configs.items():
+        numbers = [int(n) for n in args.split(",")]
+        kernel = "gemm_mx4_tile_kernelINS_6Mx4CfgI" + "".join(f"Li{n}E" for n in numbers) + "EE"
+        meta = next(part for part in product.split("  - .agpr_count:")[1:] if kernel in part)
+        lds, vgprs, scratch = (int(re.search(rf"\.{name}: +(\d+)", meta).group(1)) for name in
+                               ("group_segment_fixed_size", "vgpr_count", "private_segment_fixed_size"))
+        waves = numbers[0] * numbers[1]
+        slots = min(8, 512 // ((vgprs + 7) // 8 * 8)) * 4
+        assert scratch == 0 and min(160 * 1024 // lds, slots // waves) == int(per_cu[shape]), (shape, lds, vgprs, waves)
