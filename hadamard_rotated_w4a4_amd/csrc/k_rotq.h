@@ -110,6 +110,14 @@ __device__ __forceinline__ void fwht32_quad(float v[8], int L) {
         v[i] = __fadd_rn(quad_f32<QP_XOR2>(v[i]), __uint_as_float(__float_as_uint(v[i]) ^ flip2));
 }
 
+// The larger of two values; with KEEP_NAN a NaN if either is (one instruction all
+// the same, v_maximum3_f32 in place of v_max3_f32).
+template <bool KEEP_NAN>
+__device__ __forceinline__ float larger(float a, float b) {
+    if constexpr (KEEP_NAN) return __builtin_elementwise_maximum(a, b);
+    else return fmaxf(a, b);
+}
+
 // The values of one (row, block), held by a quad of lanes (lane L of the quad:
 // elements 8L .. 8L + 7 in v), quantised: the butterflies (unless ROTATE is
 // false), the absmax, the scale s and this lane's 8 codes.  KEEP_NAN: a NaN among
@@ -117,11 +125,6 @@ __device__ __forceinline__ void fwht32_quad(float v[8], int L) {
 // read back as numbers; else the absmax ignores NaN.  Every lane of the quad must
 // take part (the butterflies and the absmax exchange values through quad
 // permutes).
-template <bool KEEP_NAN>
-__device__ __forceinline__ float larger(float a, float b) {
-    if constexpr (KEEP_NAN) return __builtin_elementwise_maximum(a, b);  // NaN if either is: v_maximum3_f32
-    else return fmaxf(a, b);
-}
 template <int QMAX, bool ROTATE, bool KEEP_NAN = false>
 __device__ __forceinline__ void quantise_values(float v[8], int L, int q[8], float &s) {
     if constexpr (ROTATE) fwht32_quad(v, L);

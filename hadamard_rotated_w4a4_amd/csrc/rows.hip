@@ -203,8 +203,9 @@ w4a4_status w4a4_rms_norm_quantize(const void *x, w4a4_dtype xdt, int64_t ldx, c
     if (k % QK) return W4A4_ERR_K_NOT_MULTIPLE_OF_32;
     if (m == 0 || k == 0) return W4A4_OK;
     if (!x) return W4A4_ERR_INVALID_VALUE;
-    // in place: the same elements only
-    if ((h == x && (xdt != rdt || ldh != ldx)) || (h && h == residual && ldh != ldr)) return W4A4_ERR_INVALID_VALUE;
+    // in place: the same elements only (one row has no stride)
+    if ((h == x && (xdt != rdt || (m > 1 && ldh != ldx))) || (h && h == residual && m > 1 && ldh != ldr))
+        return W4A4_ERR_INVALID_VALUE;
     const NormArgs a{static_cast<const uint8_t *>(x), static_cast<const uint8_t *>(residual), weight,
                      static_cast<uint8_t *>(h), ldx, ldr, ldh, eps, 1.0 / (double)k, xdt, rdt,
                      RowsOut{static_cast<uint8_t *>(codes), scales, static_cast<uint8_t *>(operand), m, k}};

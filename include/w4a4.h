@@ -575,8 +575,8 @@ w4a4_status w4a4_dequantize_act(w4a4_act_format fmt, const void *codes, const vo
  *   weight    [k] fp32, or NULL for ones; 4-byte aligned.
  *   eps       > 0, finite.
  *   h         out, [m][ldh] of type rdt, or NULL.  May be residual, or x when
- *             the types are equal (same pointer and stride: in place); no
- *             other overlap of outputs with inputs.
+ *             the types are equal (same pointer and, for more than one
+ *             row, stride: in place); no other overlap of outputs with inputs.
  *   codes, scales, operand   out, as fmt has them.
  * Errors: an unknown type -> W4A4_ERR_UNSUPPORTED_DTYPE; an unknown format,
  * negative sizes, a stride below k, bad eps, null pointers with work to do, an
