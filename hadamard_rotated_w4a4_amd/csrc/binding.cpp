@@ -1,8 +1,9 @@
 // Native binding of the quantised-row producers and the MXFP4 product
 // (include/w4a4.h): argument checks, output allocation and the call, for
 // _lib.py.  A decoder step makes dozens of these calls on a few rows, where
-// the kernels take 3 to 6 us each: checks and allocations in Python cost 12 to
-// 14 us a call, here about 3.
+// the kernels take 3 to 6 us each.  Checks and marshalling take 0.3 to 0.4 us a
+// call, new outputs 0.7 to 1.0 more, the launch 2.5 to 2.7; checks and allocations
+// written in Python took 12 to 14 with it.
 //
 // Every function takes positional arguments (None for those left out), raises
 // the exception type given to init() and lets no C++ exception out.

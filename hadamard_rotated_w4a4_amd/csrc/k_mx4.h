@@ -43,7 +43,8 @@ __host__ __device__ inline int64_t mx4_packed_bytes(int64_t n, int64_t k) {
 }
 
 // One thread per (tile, stage, lane).  Bound by memory for weights (5120 x 17408
-// 23 us, 4.1 TB/s) and by a launch's latency for rows (302 x 17408 3.6 us).
+// 19.4 us, 95 MB, 4.9 TB/s) and by a launch's latency for rows (302 x 17408 4.2 us,
+// 512 x 5120 3.6).
 __global__ __launch_bounds__(256) void repack_mx4_kernel(const uint8_t *__restrict__ codes,
                                                          const uint8_t *__restrict__ scales, int64_t n, int64_t k,
                                                          uint8_t *__restrict__ packed) {
@@ -119,13 +120,14 @@ __device__ __forceinline__ void mx4_store(uint8_t *y, int dt, int64_t i, float v
 // its MFMAs, not at the barrier.
 //
 // What bounds it: a 256 x 256 tile's slot holds 1024 matrix-core cycles a SIMD and
-// 770 cycles of LDS reads, and takes about 2600 cycles at 2.4 GHz where a launch
-// fills the chip: random codes draw so much power that the clock falls to 1.9 GHz
-// (512 x 32768 x 5120, one full round: 58 us, 3.0 PFLOP/s; with zero codes 48).
-// About 10 us of that are the start, the first loads and the output's way to
-// memory, which the one round leaves in the open.  Small tiles wait for LDS reads,
-// the loads' writes there and barriers: 302 x 5120 x 17408 spends 30.7 us in 64 x
-// 64 tiles, 18 % of it in matrix instructions, and 3.9 in the rows' records.
+// 770 cycles of LDS reads, and takes 1.04 us where a launch fills the chip, 0.75
+// with zero codes: random codes draw so much power that the clock falls from 2.4 to
+// 1.9 GHz (512 x 32768 x 5120, one full round: 54 us back to back, 3.2 PFLOP/s, 50
+// with the chip idle before it; 41 with zero codes).  About 12 us of that are the
+// start, the first loads and the output's way to memory, which the one round leaves
+// in the open.  Small tiles wait for LDS reads, the loads' writes there and
+// barriers: 302 x 5120 x 17408 spends 30.6 us in 64 x 64 tiles, 18 % of it in
+// matrix instructions, and 4.2 in the rows' records.
 //
 // Tried and slower or no faster: the rows read in place instead of from records
 // (302 x 5120 x 17408 47.7 us against 38.9 with the same tiles: their 64- and
@@ -409,7 +411,7 @@ __global__ __launch_bounds__(C::NT) void gemm_mx4_tile_kernel(Mx4Args a) {
 }
 
 // y = the splits' partial sums added in ascending order (the order is fixed: the
-// same inputs give the same bits).  302 x 5120, three splits: 5.7 us.
+// same inputs give the same bits).  140 x 10240, three splits: 5.7 us, 22.9 MB.
 __global__ __launch_bounds__(256) void mx4_reduce_kernel(Mx4Args a) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= a.m * a.n) return;
@@ -422,9 +424,10 @@ __global__ __launch_bounds__(256) void mx4_reduce_kernel(Mx4Args a) {
 // Few rows: the weights are streamed straight into registers, once per block of
 // ROWS rows.
 //
-// Bound by the weights' way from memory: 16 x 17408 x 5120 10.3 us, 48.9 MB, 4.7
-// TB/s (a copy reaches 5.15); 1 x 1024 x 5120, 32 workgroups and 2.8 MB, 3.8 us of
-// launch and load latency.
+// Bound by the weights' way from memory: 16 x 17408 x 5120 11.2 us, 48.9 MB, 4.4
+// TB/s (9.8 at best; a copy reaches 5.15); 1 x 1024 x 5120, 32 workgroups and 2.8 MB,
+// 3.7 us of launch and load latency.  With fewer column tiles than CUs, or a K of
+// several chunks, less: 16 x 5120 x 17408 11.0 us, 64 x 5120 x 17408 23.3.
 //
 // A workgroup takes one 32-column tile (blockIdx.x) of one block of rows
 // (blockIdx.y) over the whole of K; its waves take the stages round-robin, each

@@ -10,10 +10,12 @@
 // Codes depend on every rounding before them, so each is defined by a fixed
 // sequence of roundings.  Where an exact value is an unordered sum (the row's
 // sum of squares) or a transcendental function (the gated activation), it is
-// evaluated in fp64, to within 2^-40, and rounded once to fp32: the codes do
-// not depend on the launch shape.  fp64 multiply-adds issue at the fp32 rate on
-// this part: the norm's are hidden behind its loads, the gated activation's are
-// two fifths of its instructions.
+// evaluated in fp64 (the sum to about 2^-50, the function to within 2^-40) and
+// rounded once to fp32: a launch shape that takes the sum in another order gives
+// another last place of the root for less than one row in 2^26, and the same codes
+// for all others.  fp64 multiply-adds issue at the fp32 rate on this part: the norm's
+// are hidden behind its loads, the gated activation's are two fifths of its
+// instructions.
 //
 // A block is held by a quad of lanes (lane L: elements 8L .. 8L + 7), as in
 // the quantiser.
@@ -201,7 +203,7 @@ __device__ __forceinline__ void block_of_quad(RowBlocks blocks, int64_t &row, in
 
 // ---------------------------------------------------------------------------
 // Plain rows to MXFP4.  Bound by memory: one pass, every byte once.  17408 x 5120
-// fp32 74 us, 5.4 TB/s; 512 x 5120 fp16 3.6 us, of which a launch that does
+// fp32 73 us, 5.5 TB/s; 512 x 5120 fp16 3.4 us, of which a launch that does
 // nothing takes about 2.
 // ---------------------------------------------------------------------------
 struct PlainArgs {
@@ -223,10 +225,11 @@ __global__ __launch_bounds__(ROWS_THREADS) void quantise_rows_kernel(PlainArgs a
 }
 
 // ---------------------------------------------------------------------------
-// Gated activation: v = fl32(act(g) u), act in fp64.  Bound by vector issue: some
-// 64 instructions an element, 77 % of the issue slots filled.  302 x 17408 fp16
-// to int8 12.4 us (26.9 MB, 2.2 TB/s), 8192 x 768 fp32 to int4 13.2 us (54.3 MB,
-// 4.1 TB/s), 16 x 17408 3.3 us.
+// Gated activation: v = fl32(act(g) u), act in fp64.  Bound by vector issue: 65
+// instructions an element for 302 x 17408 fp16 to int8, 5,174 a SIMD, which at 4
+// cycles of 2.4 GHz are 8.6 of its 11.6 us (27.1 MB, 2.3 TB/s).  8192 x 768 fp32 to
+// int4 13.2 us (54.4 MB, 4.1 TB/s), 16 x 17408 3.2 us.  With operand records 302 x
+// 17408 takes 17.0 us to int8 (40.2 MB, 7,260 instructions) and 13.9 to int4.
 // ---------------------------------------------------------------------------
 constexpr int GLU_SILU = 0, GLU_GELU_TANH = 1;  // w4a4_glu_act
 
@@ -307,11 +310,13 @@ __global__ __launch_bounds__(ROWS_THREADS) void glu_rows_kernel(GluArgs a) {
 // longer row twice, reading h (or the inputs, when h is not written) again.
 // With operand records, the 32 rows of a tile go to workgroups of one XCD
 // (they are dealt round-robin), whose L2 joins their 8-byte pieces of a record
-// to whole lines.
+// to whole lines: 512 x 5120 to int8 with its records writes 13.43 MB, the outputs'
+// own bytes (10.3 us).
 //
 // Few rows are bound by one chain of latencies, load -> sum over the workgroup ->
-// quantise -> store (1 x 5120 3.2 us, 512 x 5120 9.0 us: 24.3 MB in one round of
-// workgroups, 2.7 TB/s), many by memory (2048 x 5120 19.1 us, 5.0 TB/s).
+// quantise -> store (1 x 5120 3.3 us), 512 x 5120 to int8 (9.3 us, 24.2 MB, 2.6 TB/s)
+// by a launch and one burst of reads followed by one of writes, all its workgroups
+// being resident together; many rows by memory (2048 x 5120 20.4 us, 4.7 TB/s).
 // ---------------------------------------------------------------------------
 struct NormArgs {
     const uint8_t *x, *residual;  // residual may be null
@@ -480,7 +485,7 @@ __global__ __launch_bounds__(1024) void norm_rows_kernel(NormArgs a, bool act) {
 // ---------------------------------------------------------------------------
 // Quantised rows read back: y = fl(q s) in type dt (MXFP4 values are exact in
 // fp32 and bf16; a block whose scale byte is 255 reads as NaN).  Bound by memory:
-// 17408 x 5120 MXFP4 to bf16 51 us, 4.5 TB/s; 302 x 17408 int8 to fp16 3.3 us.
+// 17408 x 5120 MXFP4 to bf16 52 us, 4.4 TB/s; 302 x 17408 int8 to fp16 3.5 us.
 // ---------------------------------------------------------------------------
 struct ReadArgs {
     const uint8_t *codes;

@@ -37,9 +37,11 @@ w4a4_status w4a4_repack_mx4(const uint8_t *codes, const uint8_t *scales, int64_t
 namespace {
 
 // The streaming kernels: up to 16, 32 or 64 rows a block, waves, records in
-// flight, LDS share in KB.  Measured: 16 rows, 8 waves for K up to 5120 (17408
-// columns 11.3 us against 11.9 with 16 waves), 16 waves past it (5120 x 8192
-// 6.8 us against 7.4); 32 rows, 16 waves with a CU's whole LDS while every
+// flight, LDS share in KB.  Measured: 16 rows, 8 waves for K up to 5120 and 16 past
+// it, where the two cross at every width tried (weights from memory, us with 8 and
+// 16 waves: 1024 columns 4.3 and 4.4 at K 4096, 4.7 and 4.7 at 5120, 6.2 and 5.4 at
+// 7168; 5120 columns 5.7 and 5.8, 6.7 and 6.6, 9.2 and 8.0; 17408 columns 11.3 and
+// 11.7, 14.0 and 13.7, 18.1 and 17.5); 32 rows, 16 waves with a CU's whole LDS while every
 // column tile has a CU (5120 x 8192 8.2 us against 10.2), else 8 (17408 x 5120
 // 13.7 us against 16.5).
 using Stream16 = Mx4Stream<16, 8, 2, 52>;

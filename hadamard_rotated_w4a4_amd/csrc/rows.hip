@@ -142,9 +142,12 @@ void launch_norm_chunks(const NormArgs &a, int64_t rows, int64_t threads, hipStr
 }
 // A row's pieces of 8 elements over a workgroup's threads, in 1, 2 or 4 pieces
 // each; rows past 32768 walk twice.  Few rows wait for one row's chain of loads,
-// sum and stores: as many threads as a workgroup holds (1 x 5120 3.5 us against
-// 4.2 with half).  With two rows a CU and more, fewer waves with two pieces each
-// do less of what every wave repeats (2048 x 5120 19.1 us against 21.2).
+// sum and stores: as many threads as a workgroup holds (1 x 5120 3.6 us against
+// 4.2 with at most 512).  With two rows a CU and more, rows up to 16384 go to at
+// most 512 threads, so that several workgroups share a CU (to int8, from memory:
+// 2048 x 16384 64 us against 76 with up to 1024, 512 x 16384 22.0 against 23.4).
+// Rows that 1024 threads hold in one piece each do not gain from that: 512 x 5120
+// 10.4 us against 9.5, 2048 x 5120 25.1 against 24.0, 2048 x 2048 the same.
 template <int FMT>
 void launch_norm(const NormArgs &a, hipStream_t s) {
     const int64_t rows = rows_covered(FMT, a.out.act != nullptr, a.out.m);

@@ -564,8 +564,9 @@ w4a4_status w4a4_dequantize_act(w4a4_act_format fmt, const void *codes, const vo
  *   h = rdt(x + residual)        (one fp32 addition, one rounding; rdt(x)
  *                                 without a residual)
  *   s = fp32(1 / sqrt(sum_i h_i^2 / k + eps))   (the sum and the root in
- *                                 fp64, one rounding: s does not depend on
- *                                 the order of the sum)
+ *                                 fp64, one rounding; another order of the
+ *                                 sum changes the last place of s for
+ *                                 less than one row in 2^26)
  *   v_i = fl(fl(h_i * s) * weight_i)            (fp32)
  * and v quantised in format fmt as the calls named above quantise x.  An
  * infinity in h makes s 0: its own block is lost (see the formats), the row's
