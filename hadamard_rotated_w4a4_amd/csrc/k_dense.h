@@ -214,11 +214,16 @@ __device__ __forceinline__ T lds_read(const uint8_t *p) {
 
 // One global-to-LDS load of 16 bytes per lane: lane l's bytes at sbase +
 // voff land at LDS byte address lds + 16 l (lds is wave-uniform, passed
-// through M0).  The base is wave-uniform (SGPRs) and voff a per-lane 32-bit
-// byte offset, so no 64-bit vector address arithmetic is needed per load.
+// through M0; a load that reads M0 needs one wait state after the write, and
+// the compiler sees neither in here).  The base is wave-uniform (SGPRs) and
+// voff a per-lane 32-bit byte offset, so no 64-bit vector address arithmetic
+// is needed per load.
 __device__ __forceinline__ void dma16s(const uint8_t *sbase, uint32_t voff, uint32_t lds) {
     uint32_t m0;  // written
-    asm volatile("s_mov_b32 m0, %3\n\tglobal_load_lds_dwordx4 %1, %2" : "={m0}"(m0) : "v"(voff), "s"(sbase), "s"(lds) : "memory");
+    asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 : "={m0}"(m0)
+                 : "v"(voff), "s"(sbase), "s"(lds)
+                 : "memory");
 }
 
 // A wave-uniform pointer, placed in SGPRs.  (The builtin returns a signed

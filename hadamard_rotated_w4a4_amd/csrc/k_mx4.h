@@ -157,16 +157,17 @@ struct Mx4Cfg {
 };
 
 // One global-to-LDS load of 16 bytes per lane: the 16 bytes at lane l's p land
-// at LDS byte address lds + 16 l (lds is uniform).
+// at LDS byte address lds + 16 l (lds is uniform).  A load that reads M0 needs one
+// wait state after the write (the compiler sees neither in here).
 __device__ __forceinline__ void mx4_load16(const uint8_t *p, uint32_t lds) {
     uint32_t m0;  // written
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %1, off" : "={m0}"(m0) : "v"(p), "s"(lds) : "memory");
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : "={m0}"(m0) : "v"(p), "s"(lds) : "memory");
 }
 // The same, if on (uniform); see Mx4Cfg::STRAIGHT.
 __device__ __forceinline__ void mx4_load16(const uint8_t *p, uint32_t lds, int on) {
     uint32_t m0;
     asm volatile(
-        "s_cmp_eq_u32 %3, 0\n\ts_cbranch_scc1 1f\n\ts_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %1, off\n1:"
+        "s_cmp_eq_u32 %3, 0\n\ts_cbranch_scc1 1f\n\ts_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off\n1:"
         : "={m0}"(m0)
         : "v"(p), "s"(lds), "s"(__builtin_amdgcn_readfirstlane(on))
         : "memory", "scc");

@@ -2,6 +2,7 @@
 of code built here (CPU only: hipcc cross-compiles)."""
 import os
 import re
+import shutil
 import subprocess
 
 import pytest
@@ -9,6 +10,8 @@ import pytest
 pytest.importorskip("torch")
 
 from hadamard_rotated_w4a4_amd import build as hip  # noqa: E402
+
+pytestmark = pytest.mark.skipif(shutil.which(hip.HIPCC) is None, reason=f"no compiler at {hip.HIPCC}")
 
 
 def assembly(source, out):
@@ -34,6 +37,11 @@ def instructions(text, kernel):
     return lines
 
 
+def waits_between(code, i, j):
+    """Wait states between instructions i and j: one an instruction, n + 1 an s_nop n."""
+    return sum(int(line.split()[1]) + 1 if line.startswith("s_nop") else 1 for line, _ in code[i + 1:j])
+
+
 PROBE = """
 #include "common.h"
 #include "{header}"
@@ -57,13 +65,16 @@ extern "C" __global__ void probe(const uint8_t *p, uint8_t *y, int on) {{
                                          ("k_dense.h", "dma16s(p, 16 * threadIdx.x, base)")])
 def test_direct_loads_say_that_they_write_m0(tmp_path, header, load):
     """Between two of the compiler's own direct loads to one LDS address, one of
-    ours to another: the compiler must set M0 again after it."""
+    ours to another: the compiler must set M0 again after it, and ours needs a
+    wait state between its write of M0 and its load."""
     source = tmp_path / "probe.hip"
     source.write_text(PROBE.format(header=header, load=load))
     code = instructions(assembly(source, tmp_path / "probe.s"), "probe")
     ours = [i for i, (line, inline) in enumerate(code) if inline and "load_lds" in line]
     later = [i for i, (line, inline) in enumerate(code) if not inline and "load_lds" in line and i > ours[-1]]
     assert len(ours) == 1 and len(later) == 1
+    write = max(i for i, (line, _) in enumerate(code[:ours[0]]) if line.startswith("s_mov_b32 m0,"))
+    assert code[write][1] and waits_between(code, write, ours[0]) >= 1
     between = [line for line, inline in code[ours[0] + 1:later[0]] if not inline]
     assert any(re.match(r"s_\w+ m0,", line) for line in between), between
 
@@ -111,3 +122,14 @@ def test_the_plan_counts_the_workgroups_that_a_cu_holds(product):
         waves = numbers[0] * numbers[1]
         slots = min(8, 512 // ((vgprs + 7) // 8 * 8)) * 4
         assert scratch == 0 and min(160 * 1024 // lds, slots // waves) == int(per_cu[shape]), (shape, lds, vgprs, waves)
+
+
+def test_every_direct_load_waits_for_its_m0(product):
+    """One wait state between a write of M0 and the load that reads it."""
+    for name in kernels(product, "gemm_mx4_stream_kernel") + kernels(product, "gemm_mx4_tile_kernel"):
+        code = instructions(product, name)
+        loads = [i for i, (line, _) in enumerate(code) if "load_lds" in line]
+        assert loads, name
+        for i in loads:
+            write = max(j for j, (line, _) in enumerate(code[:i]) if re.match(r"s_\w+ m0,", line))
+            assert waits_between(code, write, i) >= 1, (name, code[write:i + 1])
