@@ -169,6 +169,7 @@ size_t w4a4_gemm_mx4_workspace_bytes(int64_t m, int64_t n, int64_t k) {
 }
 
 size_t w4a4_gemm_mx4_plan(int64_t m, int64_t n, int64_t k, char *text, size_t bytes) {
+    if (!text) bytes = 0;
     if (bytes) text[0] = 0;
     if (m <= 0 || n <= 0 || k <= 0 || k % QK || !within_bounds(m, n, k)) return 0;
     int len;

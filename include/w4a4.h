@@ -631,7 +631,7 @@ w4a4_status w4a4_glu_quantize(const void *gate, const void *up, w4a4_dtype dt, i
  *
  * w4a4_gemm_mx4_plan: the kernels that w4a4_gemm_mx4 launches for these sizes,
  * for tests and measurements, as a line of text in `text` (at most bytes - 1
- * characters and a zero; may be NULL when bytes is 0): "stream RxW" (weights
+ * characters and a zero; may be NULL, for the length only): "stream RxW" (weights
  * streamed for blocks of R rows, W waves a workgroup), "tile MxN", "tile MxN
  * split S" (S splits of K, then their sum) or "tile MxN + PxQ" (whole rounds of
  * one shape, the remaining columns in another).  Returns the text's length; 0

@@ -3,6 +3,7 @@ test_gpu_mx4, reach each kernel shape whole, with K splits, ahead of another
 shape and as the remaining columns of one.  The CPU test holds the list against
 the plans that a sweep of sizes gives, so a refit of the plan's constants shows
 here which sizes have to join."""
+import ctypes
 import math
 import random
 import re
@@ -69,7 +70,9 @@ def test_plan_query():
         rows = (ops.mx4_packed_bytes(m, k) + 255) // 256 * 256 if need else 0
         splits = int(text.split()[-1]) if "split" in text else 0
         assert need == rows + (splits * m * n * 4 + 255) // 256 * 256
-    assert L.w4a4_gemm_mx4_plan(1, 1, 32, None, 0) == len("stream 16x8")
+    assert L.w4a4_gemm_mx4_plan(1, 1, 32, None, 0) == len("stream 16x8") == L.w4a4_gemm_mx4_plan(1, 1, 32, None, 9)
+    short = ctypes.create_string_buffer(7)
+    assert L.w4a4_gemm_mx4_plan(1, 1, 32, short, 7) == len("stream 16x8") and short.value == b"stream"
 
 
 @pytest.mark.gpu
