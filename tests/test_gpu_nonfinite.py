@@ -168,6 +168,34 @@ def test_an_overflow_reaches_the_product_of_the_operand(ops, m):
         assert not np.isfinite(y[hit]).any() and np.array_equal(y[~hit], want[~hit])
 
 
+@pytest.mark.parametrize("m", [5, 40])
+def test_an_overflow_reaches_the_products_of_codes_and_scales(ops, m):
+    """As above for the products that read the public codes and scales, dense and
+    per routed row."""
+    say(f"glu_quantize -> products of codes and scales, m={m}")
+    n, k, experts = 64, 256, 3
+    rng = np.random.default_rng(m + 1)
+    g, u = (dev(rng.standard_normal((m, k)).astype(np.float32)) for _ in range(2))
+    packed = [ops.prepare_weights(dev((rng.standard_normal((n, k)) * 0.02).astype(np.float32))) for _ in range(experts)]
+    ids = dev(rng.integers(0, experts, (m, 1)).astype(np.int32))
+
+    def products():
+        c4, s4 = ops.glu_quantize(g, u, ops.ACT_INT4)
+        c8, s8 = ops.glu_quantize(g, u, ops.ACT_INT8)
+        out = [ops.gemm(packed[0], c4, s4, n, k), ops.gemm_noalloc(packed[0], c4, s4, n, k), ops.gemm_a8(packed[0], c8, s8, n, k),
+               ops.gemm_id(torch.cat(packed), experts, c4, s4, 1, ids, n, k).reshape(m, n)]
+        return [y.cpu().numpy() for y in out]
+
+    clean = products()
+    g[2, 37], u[2, 37] = float("inf"), 1.0
+    g[4, 200] = float("nan")
+    hit = np.zeros(m, bool)
+    hit[[2, 4]] = True
+    for i, (y, want) in enumerate(zip(products(), clean)):
+        assert not np.isfinite(y[hit]).any(), i
+        assert np.array_equal(y[~hit], want[~hit]), i
+
+
 @pytest.mark.parametrize("call,top,rotate", [("rotate_quantize_act", 7, True), ("rotate_quantize_act8", 127, True), ("quantize_act", 7, False)])
 def test_quantisers_of_a_matrix_keep_their_codes(ops, call, top, rotate):
     """The quantisers of a matrix in memory: a product that is NaN (an infinite
