@@ -95,6 +95,12 @@ def lib() -> ctypes.CDLL:
             "w4a4_gemm_mx4_workspace_bytes": ([I64, I64, I64], SZ),
             "w4a4_gemm_mx4_plan": ([I64, I64, I64, ctypes.c_char_p, SZ], SZ),
             "w4a4_gemm_mx4": ([P, P, P, P, ST, I64, I64, I64, I64, P, SZ, P], ST),
+            "w4a4_kv_cache_code_bytes": ([I64, I64, I64, I64], SZ),
+            "w4a4_kv_cache_scale_bytes": ([I64, I64, I64, I64], SZ),
+            "w4a4_append_kv": ([ST, P, P, P, I64, P, ST, P, P, ctypes.c_double, P, P, P, P], ST),
+            "w4a4_read_kv": ([P, P, ST, P, P, P], ST),
+            "w4a4_attention_kv_workspace_bytes": ([I64, I64, I64, I64, I64, I64], SZ),
+            "w4a4_attention_kv": ([P, ST, I64, P, ST, P, I64, ctypes.c_double, ST, I64, P, P, P, SZ, P], ST),
         }
         for name, (args, res) in sigs.items():
             fn = getattr(L, name)
@@ -756,3 +762,59 @@ def gemm_mx4(packed: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, n:
     The workspace is allocated there unless given (uint8, at least
     gemm_mx4_workspace_bytes)."""
     return (_native_module or _native()).gemm_mx4(packed, codes, scales, n, k, y, workspace, dtype)
+
+
+# --------------------------------------------------------------------------
+# The paged key/value cache in 8 bits, and attention over it
+# --------------------------------------------------------------------------
+
+def new_kv_cache(pages: int, page: int, heads: int, dim: int, device) -> tuple[torch.Tensor, torch.Tensor]:
+    """An empty pool of `pages` pages of `page` tokens for `heads` key/value heads
+    of width `dim`: codes uint8 [pages, heads, page/32, 2, 32 dim], scales uint8
+    [pages, heads, page/32, 2] (include/w4a4.h has the layout)."""
+    if pages and not lib().w4a4_kv_cache_code_bytes(pages, page, heads, dim):
+        raise W4A4Error(f"no cache of {pages} pages of {page} tokens, {heads} heads of {dim}")
+    return (torch.zeros((pages, heads, page // 32, 2, 32 * dim), dtype=torch.uint8, device=device),
+            torch.zeros((pages, heads, page // 32, 2), dtype=torch.uint8, device=device))
+
+
+def append_kv(k: torch.Tensor, v: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, pages: torch.Tensor,
+              starts: torch.Tensor, lens: torch.Tensor, q: torch.Tensor | None = None, rope: torch.Tensor | None = None,
+              positions: torch.Tensor | None = None, axes: torch.Tensor | None = None, interleaved: bool = False,
+              q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None, eps: float = 1e-6,
+              q_out: torch.Tensor | None = None, dtype: torch.dtype = torch.bfloat16) -> torch.Tensor | None:
+    """New tokens' k and v ([rows, heads, dim], any strides along rows and heads)
+    into the cache, sequence b's rows starts[b] .. starts[b + 1] - 1 as its last
+    tokens of lens[b] (pages int32 [seqs, n], starts int32 [seqs + 1], lens int32
+    [seqs]).  RMS norm of every q and k head where there is a weight (fp32 [dim]),
+    then rotary positions by the table rope (fp32 [positions, width]: cosines, then
+    sines), at the token's number or at positions (int32 [rows], or [axes, rows]
+    with axes, uint8 [width / 2], the axis of each pair).  Returns the queries in
+    `dtype` (or q_out's type), None without q."""
+    return (_native_module or _native()).append_kv(k, v, codes, scales, pages, starts, lens, q, rope, positions, axes,
+                                                   interleaved, q_weight, k_weight, eps, q_out, dtype)
+
+
+def read_kv(codes: torch.Tensor, scales: torch.Tensor, pages: torch.Tensor, starts: torch.Tensor, lens: torch.Tensor,
+            rows: int, dtype: torch.dtype = torch.bfloat16, k: torch.Tensor | None = None,
+            v: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+    """The last tokens of every sequence read back (starts, lens as in append_kv):
+    (k, v), both [rows, heads, dim] of `dtype`."""
+    return (_native_module or _native()).read_kv(codes, scales, pages, starts, lens, rows, dtype, k, v)
+
+
+def attention_kv_workspace_bytes(rows: int, seqs: int, q_heads: int, heads: int, dim: int, tokens: int) -> int:
+    """tokens: pages of a sequence (pages.size(1)) times their length."""
+    return int(lib().w4a4_attention_kv_workspace_bytes(rows, seqs, q_heads, heads, dim, tokens))
+
+
+def attention_kv(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, pages: torch.Tensor, starts: torch.Tensor,
+                 lens: torch.Tensor, scale: float | None = None, causal: bool = True, window: int = 0,
+                 out: torch.Tensor | None = None, lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                 dtype: torch.dtype | None = None) -> torch.Tensor:
+    """Attention of q (fp16 or bf16 [rows, q_heads, dim]) over the cache, the rows
+    being each sequence's last tokens (starts, lens as in append_kv); scale 1 /
+    sqrt(dim) unless given.  Returns [rows, q_heads, dim] of `dtype` (fp16 or bf16;
+    out's type, or q's); lse (fp32 [rows, q_heads]) is written where given."""
+    return (_native_module or _native()).attention_kv(q, codes, scales, pages, starts, lens, scale, causal, window, out, lse,
+                                                      workspace, dtype)

@@ -21,9 +21,9 @@ NATIVE = os.path.join(PKG, "_native.so")  # the binding's native part
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 CXX = os.environ.get("CXX", "g++")  # the native binding's host compiler
 
-SOURCES = [os.path.join(CSRC, f) for f in ("w4a4.hip", "rows.hip", "mx4.hip")]
+SOURCES = [os.path.join(CSRC, f) for f in ("w4a4.hip", "rows.hip", "mx4.hip", "kv.hip")]
 HEADERS = [os.path.join(CSRC, h) for h in ("abi.h", "common.h", "k_prep.h", "k_rotq.h", "k_route.h", "k_dense.h", "k_smallm.h", "k_grouped.h", "k_w16.h",
-                                            "k_rows.h", "k_mx4.h")] + [
+                                            "k_rows.h", "k_mx4.h", "k_kv.h", "k_attend.h")] + [
     os.path.join(ROOT, "include", "w4a4.h")]
 
 FLAGS = [

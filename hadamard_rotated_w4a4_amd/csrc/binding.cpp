@@ -1,5 +1,5 @@
-// Native binding of the quantised-row producers and the MXFP4 product
-// (include/w4a4.h): argument checks, output allocation and the call, for
+// Native binding of the quantised-row producers, the MXFP4 product and the
+// key/value cache (include/w4a4.h): argument checks, output allocation and the call, for
 // _lib.py.  A decoder step makes dozens of these calls on a few rows, where
 // the kernels take 3 to 6 us each.  Checks and marshalling take 0.3 to 0.4 us a
 // call, new outputs 0.7 to 1.0 more, the launch 2.5 to 2.7; checks and allocations
@@ -370,6 +370,181 @@ PyObject *gemm_mx4(PyObject *const *a) {
     return give(a[5], y);
 }
 
+// --------------------------------------------------- the key/value cache
+
+// codes [pages][heads][page / 32][2][32 dim] and scales [pages][heads][page / 32][2].
+w4a4_kv_cache cache_of(const at::Tensor &codes, const at::Tensor &scales) {
+    need(codes, "codes", at::kByte, 0);
+    need(scales, "scales", at::kByte, 0);
+    if (codes.dim() != 5 || codes.size(3) != 2 || codes.size(4) % 32 || codes.size(1) < 1 || codes.size(2) < 1)
+        refuse("codes: expected [pages, heads, page / 32, 2, 32 dim]");
+    if (scales.dim() != 4 || scales.size(0) != codes.size(0) || scales.size(1) != codes.size(1) || scales.size(2) != codes.size(2) ||
+        scales.size(3) != 2)
+        refuse("scales: expected [pages, heads, page / 32, 2] as the codes have them");
+    const int64_t dim = codes.size(4) / 32;
+    if (dim != 64 && dim != 128 && dim != 256) refuse("heads of " + str(dim) + ", expected 64, 128 or 256");
+    return w4a4_kv_cache{ptr(codes), (uint8_t *)ptr(scales), codes.size(0), codes.size(2) * 32, codes.size(1), dim};
+}
+w4a4_kv_batch batch_of(const at::Tensor &pages, const at::Tensor &starts, const at::Tensor &lens, int64_t rows) {
+    if (pages.scalar_type() != at::kInt) refuse(std::string("pages: dtype ") + c10::toString(pages.scalar_type()) + ", expected Int");
+    const int64_t seqs = pages.size(0), per = pages.size(1);
+    if ((seqs > 0 && per > 1 && pages.stride(1) != 1) || (seqs > 1 && pages.stride(0) < per))
+        refuse("pages: strides, expected unit column stride and rows that do not overlap");
+    need(starts, "starts", at::kInt, 4 * (seqs + 1));
+    need(lens, "lens", at::kInt, 4 * seqs);
+    return w4a4_kv_batch{(const int32_t *)ptr(pages), seqs > 1 ? pages.stride(0) : per, per, (const int32_t *)ptr(starts),
+                         (const int32_t *)ptr(lens), seqs, rows};
+}
+// t is [rows][heads][dim] with unit stride along dim.
+w4a4_head_rows head_rows(const at::Tensor &t, const char *name, int64_t rows, int64_t heads, int64_t dim) {
+    if (!t.defined()) return w4a4_head_rows{nullptr, 0, 0};
+    if (t.dim() != 3 || (rows >= 0 && t.size(0) != rows) || (heads >= 0 && t.size(1) != heads) || t.size(2) != dim)
+        refuse(std::string(name) + ": shape, expected [" + (rows < 0 ? "rows" : str(rows)) + ", " + (heads < 0 ? "heads" : str(heads)) +
+               ", " + str(dim) + "]");
+    if (t.numel() && t.stride(2) != 1) refuse(std::string(name) + ": expected unit stride along a head");
+    return w4a4_head_rows{ptr(t), t.stride(0), t.stride(1)};
+}
+at::ScalarType type_of(PyObject *o) {
+    if (!THPDtype_Check(o)) refuse("dtype: expected a torch.dtype");
+    return reinterpret_cast<THPDtype *>(o)->scalar_type;
+}
+w4a4_dtype half_type(at::ScalarType t, const char *name) {
+    if (t != at::kHalf && t != at::kBFloat16)
+        refuse(std::string(name) + ": dtype " + c10::toString(t) + ", expected float16 or bfloat16");
+    return row_type(t, name);
+}
+
+// k, v, codes, scales, pages, starts, lens, q, rope, positions, axes, interleaved, q_weight, k_weight, eps, q_out, dtype
+// -> q_out or None
+PyObject *append_kv(PyObject *const *a) {
+    const at::Tensor &k = required(a[0], "k"), &v = required(a[1], "v"), &codes = required(a[2], "codes"), &scales = required(a[3], "scales"),
+                     &pages = matrix(a[4], "pages"), &starts = required(a[5], "starts"), &lens = required(a[6], "lens"),
+                     &q = tensor(a[7], "q"), &table = tensor(a[8], "rope"), &positions = tensor(a[9], "positions"),
+                     &axes = tensor(a[10], "axes"), &q_weight = tensor(a[12], "q_weight"), &k_weight = tensor(a[13], "k_weight");
+    at::Tensor q_out = tensor(a[15], "q_out");
+    const w4a4_kv_cache cache = cache_of(codes, scales);
+    if (k.dim() != 3) refuse("k: expected [rows, heads, dim]");
+    const int64_t rows = k.size(0);
+    const w4a4_dtype dt = row_type(k.scalar_type(), "k");
+    const w4a4_head_rows kr = head_rows(k, "k", rows, cache.heads, cache.dim), vr = head_rows(v, "v", rows, cache.heads, cache.dim);
+    if (v.scalar_type() != k.scalar_type() || (q.defined() && q.scalar_type() != k.scalar_type())) refuse("q, k and v: expected one dtype");
+    const w4a4_head_rows qr = head_rows(q, "q", rows, -1, cache.dim);
+    const int64_t q_heads = q.defined() ? q.size(1) : 0;
+    if (!q.defined() && q_out.defined()) refuse("q_out without q");
+    at::ScalarType otype = at::kBFloat16;
+    if (q.defined()) otype = q_out.defined() ? q_out.scalar_type() : type_of(a[16]);
+    const w4a4_dtype odt = half_type(otype, "q_out");
+    head_rows(q_out, "q_out", rows, q_heads, cache.dim);
+    need(q_weight, "q_weight", at::kFloat, 4 * cache.dim);
+    need(k_weight, "k_weight", at::kFloat, 4 * cache.dim);
+    const double eps = PyFloat_AsDouble(a[14]);
+    if (eps == -1.0 && PyErr_Occurred()) throw PythonError{};
+    if ((q_weight.defined() || k_weight.defined()) && (!(eps > 0.0) || !std::isfinite(eps)))
+        refuse("eps = " + std::to_string(eps) + ", expected a positive number");
+    const int interleaved = PyObject_IsTrue(a[11]);
+    if (interleaved < 0) throw PythonError{};
+    w4a4_rope rope{};
+    if (table.defined()) {
+        need(table, "rope", at::kFloat, 0);
+        if (table.dim() != 2 || table.size(1) < 16 || table.size(1) % 16 || table.size(1) > cache.dim)
+            refuse("rope: expected [positions, width], width a multiple of 16 up to " + str(cache.dim));
+        const int64_t half = table.size(1) / 2;
+        rope = w4a4_rope{(const float *)ptr(table), table.size(0), table.size(1), nullptr, 0, nullptr, 1, interleaved};
+        if (positions.defined()) {
+            need(positions, "positions", at::kInt, 0);
+            if (positions.dim() < 1 || positions.dim() > 2 || positions.size(-1) != rows || (positions.dim() == 2 && positions.size(0) < 1))
+                refuse("positions: expected [" + str(rows) + "] or [axes, " + str(rows) + "]");
+            rope.positions = (const int32_t *)ptr(positions), rope.ld = rows;
+            rope.n_axes = positions.dim() == 2 ? positions.size(0) : 1;
+            if (rope.n_axes > 1 && !axes.defined()) refuse("positions of several axes need axes");
+        }
+        if (axes.defined()) {
+            if (!positions.defined()) refuse("axes without positions");
+            need(axes, "axes", at::kByte, half);
+            rope.axes = (const uint8_t *)ptr(axes);
+        }
+    } else if (positions.defined() || axes.defined()) {
+        refuse("positions and axes need rope");
+    }
+    const w4a4_kv_batch batch = batch_of(pages, starts, lens, rows);
+    const c10::Device device = one_device({&k, &v, &codes, &scales, &pages, &starts, &lens, &q, &table, &positions, &axes, &q_weight, &k_weight, &q_out});
+    if (q.defined() && !q_out.defined()) q_out = make({rows, q_heads, cache.dim}, otype, device);
+    const w4a4_head_rows out = head_rows(q_out, "q_out", rows, q_heads, cache.dim);
+    call("w4a4_append_kv", device, [&](void *s) {
+        return w4a4_append_kv(dt, &kr, &vr, &qr, q_heads, &out, odt, (const float *)ptr(q_weight), (const float *)ptr(k_weight), eps,
+                              table.defined() ? &rope : nullptr, &cache, &batch, s);
+    });
+    return q_out.defined() ? give(a[15], q_out) : none();
+}
+
+// codes, scales, pages, starts, lens, rows, dtype, k, v -> (k, v)
+PyObject *read_kv(PyObject *const *a) {
+    const at::Tensor &codes = required(a[0], "codes"), &scales = required(a[1], "scales"), &pages = matrix(a[2], "pages"),
+                     &starts = required(a[3], "starts"), &lens = required(a[4], "lens");
+    at::Tensor k = tensor(a[7], "k"), v = tensor(a[8], "v");
+    const w4a4_kv_cache cache = cache_of(codes, scales);
+    const int64_t rows = integer(a[5]);
+    if (rows < 0) refuse("rows = " + str(rows) + " is negative");
+    if (rows > int64_t{1} << 22) refuse("rows = " + str(rows) + ", too many");
+    at::ScalarType type = k.defined() ? k.scalar_type() : v.defined() ? v.scalar_type() : type_of(a[6]);
+    const w4a4_dtype dt = row_type(type, "k");
+    if ((k.defined() && k.scalar_type() != type) || (v.defined() && v.scalar_type() != type)) refuse("k and v: expected one dtype");
+    head_rows(k, "k", rows, cache.heads, cache.dim);
+    head_rows(v, "v", rows, cache.heads, cache.dim);
+    const w4a4_kv_batch batch = batch_of(pages, starts, lens, rows);
+    const c10::Device device = one_device({&codes, &scales, &pages, &starts, &lens, &k, &v});
+    if (!k.defined()) k = make({rows, cache.heads, cache.dim}, type, device);
+    if (!v.defined()) v = make({rows, cache.heads, cache.dim}, type, device);
+    const w4a4_head_rows kr = head_rows(k, "k", rows, cache.heads, cache.dim), vr = head_rows(v, "v", rows, cache.heads, cache.dim);
+    call("w4a4_read_kv", device, [&](void *s) { return w4a4_read_kv(&cache, &batch, dt, &kr, &vr, s); });
+    return pack({give(a[7], k), give(a[8], v)});
+}
+
+// q, codes, scales, pages, starts, lens, scale, causal, window, out, lse, workspace, dtype -> out
+PyObject *attention_kv(PyObject *const *a) {
+    const at::Tensor &q = required(a[0], "q"), &codes = required(a[1], "codes"), &scales = required(a[2], "scales"), &pages = matrix(a[3], "pages"),
+                     &starts = required(a[4], "starts"), &lens = required(a[5], "lens"), &lse = tensor(a[10], "lse");
+    at::Tensor out = tensor(a[9], "out"), workspace = tensor(a[11], "workspace");
+    const w4a4_kv_cache cache = cache_of(codes, scales);
+    if (q.dim() != 3) refuse("q: expected [rows, heads, dim]");
+    const int64_t rows = q.size(0), q_heads = q.size(1);
+    const w4a4_dtype dt = half_type(q.scalar_type(), "q");
+    const w4a4_head_rows qr = head_rows(q, "q", rows, q_heads, cache.dim);
+    if (q_heads < 1 || q_heads % cache.heads) refuse(str(q_heads) + " query heads over " + str(cache.heads) + " of the cache");
+    const at::ScalarType otype = out.defined() ? out.scalar_type() : a[12] == Py_None ? q.scalar_type() : type_of(a[12]);
+    const w4a4_dtype odt = half_type(otype, "out");
+    head_rows(out, "out", rows, q_heads, cache.dim);
+    double scale = 1.0 / std::sqrt((double)cache.dim);
+    if (a[6] != Py_None) {
+        scale = PyFloat_AsDouble(a[6]);
+        if (scale == -1.0 && PyErr_Occurred()) throw PythonError{};
+    }
+    if (!(scale > 0.0) || !std::isfinite((float)scale)) refuse("scale = " + std::to_string(scale) + ", expected a positive number");
+    const int causal = PyObject_IsTrue(a[7]);
+    if (causal < 0) throw PythonError{};
+    const int64_t window = integer(a[8]);
+    if (window < 0) refuse("window = " + str(window) + " is negative");
+    const w4a4_kv_batch batch = batch_of(pages, starts, lens, rows);
+    if (lse.defined()) {
+        if (lse.scalar_type() != at::kFloat) refuse("lse: expected float32");
+        if (lse.dim() != 2) refuse("lse: expected [rows, heads]");
+        need_rows(lse, "lse", rows, q_heads);
+    }
+    const int64_t tokens = batch.pages_per_seq * cache.page;
+    const int64_t size = (int64_t)w4a4_attention_kv_workspace_bytes(rows, batch.seqs, q_heads, cache.heads, cache.dim, tokens);
+    need(workspace, "workspace", at::kByte, size);
+    const c10::Device device = one_device({&q, &codes, &scales, &pages, &starts, &lens, &out, &lse, &workspace});
+    if (!out.defined()) out = make({rows, q_heads, cache.dim}, otype, device);
+    if (!workspace.defined() && size) workspace = make({size}, at::kByte, device);
+    const w4a4_head_rows orow = head_rows(out, "out", rows, q_heads, cache.dim);
+    const int64_t ld = lse.defined() ? std::max(lse.stride(0), q_heads) : 0;
+    call("w4a4_attention_kv", device, [&](void *s) {
+        return w4a4_attention_kv(&qr, dt, q_heads, &orow, odt, (float *)ptr(lse), ld, scale, causal, window, &cache, &batch,
+                                 ptr(workspace), bytes(workspace), s);
+    });
+    return give(a[9], out);
+}
+
 // ----------------------------------------------------------------- module
 
 template <PyObject *(*F)(PyObject *const *), Py_ssize_t N>
@@ -408,6 +583,9 @@ PyMethodDef kMethods[] = {method<quantize_mx4, 5>("quantize_mx4"),
                           method<glu_quantize, 8>("glu_quantize"),
                           method<repack_mx4, 5>("repack_mx4"),
                           method<gemm_mx4, 8>("gemm_mx4"),
+                          method<append_kv, 17>("append_kv"),
+                          method<read_kv, 9>("read_kv"),
+                          method<attention_kv, 13>("attention_kv"),
                           {"init", init, METH_O, nullptr},
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};

@@ -1,0 +1,473 @@
+// Attention over the paged 8-bit key/value cache (k_kv.h).
+//
+//   s_rj = scale sum_d q_rd k_jd,  p_rj = e^(s_rj - m_r),  o_r = sum_j p_rj v_j / sum_j p_rj
+//
+// over the tokens j that row r sees, in one pass: running maximum m and sum in
+// fp32, 16 products in 16 bits an fp32 accumulator.  Keys become the queries' type
+// (fp16 or bf16; an E4M3 code is exact in both) and values fp16 by the conversion
+// instruction, two a lane.  The keys' scale goes into the factor of the exponent.
+// The values' is applied by their conversion relative to the largest one so far, 2^E,
+// so that they stay within fp16, and 2^E at the end.  p is rounded to fp16 (11 bits,
+// as the output's own type or better), and summed as rounded, so that a row's weights
+// add up to one.
+//
+// m is raised only where a tile's maximum passes it by over RAISE: accumulators are
+// rescaled seldom.  Weights carry a factor 2^LIFT: at most 2^(LIFT + RAISE) < 65504,
+// and full precision down to 2^-(14 + LIFT) of the nominal maximum.
+#pragma once
+
+#include "common.h"
+#include "k_kv.h"
+
+namespace w4a4 {
+
+typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+typedef __bf16 v2b __attribute__((ext_vector_type(2)));
+typedef __bf16 v8b __attribute__((ext_vector_type(8)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+
+constexpr float ATT_RAISE = 8.0f, ATT_LIFT = 6.0f;  // powers of two
+
+struct AttendArgs {
+    const uint8_t *q;
+    uint8_t *out;
+    float *lse;
+    int64_t q_row, q_head, o_row, o_head, lse_row;  // in elements
+    float scale_log2;                               // of the scores, times log2(e)
+    int32_t heads, group;                           // query heads; of them for one key/value head
+    int32_t causal, window, odt;
+    KvPool pool;
+    KvBatch batch;
+    // partial results: [slots][rows of a tile][D] sums, then [slots][rows][2] maxima and sums
+    float *part, *part_ml;
+    int32_t workers;     // workgroups that share all tiles' tokens evenly; 0: one workgroup a tile and head
+    int32_t tile_bound;  // at least the tiles of the batch
+};
+
+// Two dwords of codes (8 values) as a 16-bit operand, times the power of two s.
+template <bool BF16>
+__device__ __forceinline__ v4u widen_e4m3(uint32_t lo, uint32_t hi, float s) {
+    if constexpr (BF16) {
+        const v2b a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, 0), b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, 1);
+        const v2b c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, s, 0), d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, s, 1);
+        return v4u{__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), __builtin_bit_cast(uint32_t, c),
+                   __builtin_bit_cast(uint32_t, d)};
+    } else {
+        const v2h a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, s, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, s, 1);
+        const v2h c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, s, 0), d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, s, 1);
+        return v4u{__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), __builtin_bit_cast(uint32_t, c),
+                   __builtin_bit_cast(uint32_t, d)};
+    }
+}
+template <bool BF16>
+__device__ __forceinline__ v4f mfma_16x16x32(v4u a, v4u b, v4f c) {
+    if constexpr (BF16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8b, a), __builtin_bit_cast(v8b, b), c, 0, 0, 0);
+    else return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
+}
+
+// Two fp32 values as fp16, to nearest even.
+__device__ __forceinline__ uint32_t f16_pair(float a, float b) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{a, b}), v2h));
+}
+// c + the sum of two fp16 values.
+__device__ __forceinline__ float add_pair(uint32_t x, float c) {
+    return __builtin_amdgcn_fdot2(__builtin_bit_cast(v2h, x), v2h{(_Float16)1.0f, (_Float16)1.0f}, c, false);
+}
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(min(max(e, -126), 127) + 127) << 23); }
+
+// x over the lanes l, l ^ 16, l ^ 32 and l ^ 48.
+template <class F>
+__device__ __forceinline__ float over_groups(float x, F f) {
+    x = f(x, __shfl_xor(x, 16));
+    return f(x, __shfl_xor(x, 32));
+}
+
+// The tokens that rows [r0, r1) of a sequence's head group see: [lo, hi), in
+// tokens; hi <= lo: none.
+struct Span {
+    int lo, hi;
+};
+__device__ __forceinline__ Span span_of(const AttendArgs &a, const KvSeq &s, int r0, int r1) {
+    const int first = s.first() + r0 / a.group, last = s.first() + (r1 - 1) / a.group;
+    const int64_t low = a.window ? (int64_t)first - a.window + 1 : 0;
+    return Span{(int)(low > 0 ? low : 0), a.causal ? min(s.len, last + 1) : s.len};
+}
+
+// Four channels of a row's result: sums y on maximum m (a power of two, above
+// LIFT), weights that sum to `total`.  A row that sees nothing has total 0.
+__device__ __forceinline__ void attend_store(const AttendArgs &a, int row0, int r, int head, int d, v4f y, float m, float total) {
+    const int i = r / a.group, h = head * a.group + (r - i * a.group);
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+    uint32_t w[2];
+#pragma unroll
+    for (int x = 0; x < 2; x++) {
+        const float lo = y[2 * x] * inv, hi = y[2 * x + 1] * inv;
+        w[x] = a.odt == ROW_F16 ? f16_bits(lo) | (uint32_t)f16_bits(hi) << 16 : bf16_bits(lo) | (uint32_t)bf16_bits(hi) << 16;
+    }
+    typedef v2u v2u_any __attribute__((aligned(2)));
+    *reinterpret_cast<v2u_any *>(a.out + ((int64_t)(row0 + i) * a.o_row + (int64_t)h * a.o_head + d) * 2) = v2u{w[0], w[1]};
+    if (a.lse && d == 0)
+        a.lse[(int64_t)(row0 + i) * a.lse_row + h] =
+            total == 0.0f ? -INFINITY : (m - ATT_LIFT + __builtin_amdgcn_logf(total)) * 0.693147180559945309f;
+}
+
+// Tiles of R rows of a sequence, for one head.
+template <int R>
+__device__ __forceinline__ int tiles_of(const AttendArgs &a, const KvSeq &s) {
+    return (int)(((int64_t)s.n * a.group + R - 1) / R);
+}
+
+// ---------------------------------------------------------------------------
+// Few rows: a wave streams the cache from memory into its registers
+// ---------------------------------------------------------------------------
+
+constexpr int STREAM_WAVES = 4, STREAM_PAIR = 2 * KV_BLOCK;  // a step of a wave: two blocks
+constexpr int STREAM_LEAST = 8;                              // steps of a worker, at least
+
+template <int R>
+__device__ __forceinline__ int steps_of(const AttendArgs &a, const KvSeq &s, int tile) {
+    const Span x = span_of(a, s, tile * R, (int)min((int64_t)(tile + 1) * R, (int64_t)s.n * a.group));
+    return x.hi <= x.lo ? 1 : (x.hi + STREAM_PAIR - 1) / STREAM_PAIR - x.lo / STREAM_PAIR;  // a tile without tokens writes zeros
+}
+template <int R>
+__device__ __forceinline__ int64_t steps_of(const AttendArgs &a, const KvSeq &s) {
+    int64_t n = 0;
+    for (int t = 0; t < tiles_of<R>(a, s); t++) n += steps_of<R>(a, s, t);
+    return n;
+}
+template <int R>
+__device__ __forceinline__ int64_t all_steps(const AttendArgs &a, int page_tokens, int lane) {
+    int64_t mine = 0;
+    for (int b = lane; b < a.batch.seqs; b += 64) mine += steps_of<R>(a, kv_seq(a.batch, page_tokens, b));
+    return wave_pick(wave_scan(mine, lane), 63) * a.pool.heads;
+}
+// Workers in use, and where worker w begins among all steps.
+__device__ __forceinline__ int64_t workers_used(int64_t steps, int workers) {
+    const int64_t most = (steps + STREAM_LEAST - 1) / STREAM_LEAST;
+    return most < workers ? most : workers;
+}
+
+// R = 16 NR rows (one head group's) of one sequence against its tokens, 64 a step:
+// S^T = K Q^T by 16 x 16 x 32 products, whose rows are chosen such that lane group
+// g holds the tokens of block g / 2 and half g % 2 as the value pieces have them.
+template <int D, bool BF16, int NR>
+__global__ __launch_bounds__(64 * STREAM_WAVES) void attend_stream_kernel(AttendArgs a) {
+    constexpr int R = 16 * NR, J = D / 64, C = D / 32, PITCH = D + 4;
+    __shared__ __align__(16) float sums[STREAM_WAVES * R * PITCH];
+    __shared__ float mls[STREAM_WAVES][R][2];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid / 64);
+    const int t16 = lane & 15, g = lane >> 4, page_tokens = a.pool.per_page * KV_BLOCK, heads = a.pool.heads;
+
+    // where this workgroup begins, and how many steps it has
+    int b, head, tile, step;
+    int64_t left;
+    if (a.workers) {
+        const int64_t all = all_steps<R>(a, page_tokens, lane), used = workers_used(all, a.workers);
+        const int64_t w = blockIdx.x;
+        if (w >= used) return;
+        int64_t at = all * w / used;
+        left = all * (w + 1) / used - at;
+        b = kv_find(a.batch.seqs, at, lane, [&](int i) { return steps_of<R>(a, kv_seq(a.batch, page_tokens, i)) * heads; });
+        if (b < 0) return;
+        const KvSeq s = kv_seq(a.batch, page_tokens, b);
+        const int64_t of_head = steps_of<R>(a, s);
+        head = (int)(at / of_head);
+        at -= head * of_head;
+        for (tile = 0; at >= steps_of<R>(a, s, tile); tile++) at -= steps_of<R>(a, s, tile);
+        step = (int)at;
+    } else {
+        int32_t id = (int32_t)(blockIdx.x / heads);
+        head = (int)(blockIdx.x % heads), step = 0, left = int64_t{1} << 40;
+        b = kv_find(a.batch.seqs, id, lane, [&](int i) { return tiles_of<R>(a, kv_seq(a.batch, page_tokens, i)); });
+        if (b < 0) return;
+        tile = id;
+    }
+
+    for (;;) {
+        const KvSeq s = kv_seq(a.batch, page_tokens, b);
+        const int rows = (int)min((int64_t)R, (int64_t)s.n * a.group - (int64_t)tile * R);
+        const Span span = span_of(a, s, tile * R, tile * R + rows);
+        const int steps = steps_of<R>(a, s, tile), stop = (int)min((int64_t)steps, step + left);
+        const int pair0 = span.lo / STREAM_PAIR;
+
+        // the queries, and what each row sees
+        v4u q[NR][J][2];
+        int row_lo[NR], row_hi[NR];
+#pragma unroll
+        for (int n = 0; n < NR; n++) {
+            const int r = tile * R + 16 * n + t16;
+            const bool live = 16 * n + t16 < rows;
+            const int i = live ? r / a.group : 0, h = live ? r - i * a.group : 0;
+            const uint8_t *p = a.q + ((int64_t)(s.row + i) * a.q_row + (int64_t)(head * a.group + h) * a.q_head) * 2;
+#pragma unroll
+            for (int j = 0; j < J; j++)
+#pragma unroll
+                for (int k = 0; k < 2; k++)
+                    q[n][j][k] = live ? *reinterpret_cast<const v4u_any *>(p + (64 * j + 16 * g + 8 * k) * 2) : v4u{0, 0, 0, 0};
+            const Span x = span_of(a, s, live ? r : tile * R, (live ? r : tile * R) + 1);
+            row_lo[n] = x.lo, row_hi[n] = live ? x.hi : 0;
+        }
+        // tokens in here are seen by every live row
+        const int every_lo = span_of(a, s, tile * R + rows - 1, tile * R + rows).lo;
+        const int every_hi = span_of(a, s, tile * R, tile * R + 1).hi;
+
+        float m[NR], l[NR];
+        v4f o[NR][C][2];
+        int E = -1000;
+#pragma unroll
+        for (int n = 0; n < NR; n++) {
+            m[n] = -INFINITY, l[n] = 0.0f;
+#pragma unroll
+            for (int c = 0; c < C; c++) o[n][c][0] = o[n][c][1] = v4f{0, 0, 0, 0};
+        }
+
+        // lane 2 k + x: block x of this wave's step k of the next 32
+        int held_block = 0, held_scale = 0;
+        int k = 32;
+        const int begin = step + wave;
+        for (int u = span.hi <= span.lo ? stop : begin; u < stop; u += STREAM_WAVES, k++) {
+            if (k == 32) {
+                k = 0;
+                const int blk = 2 * (pair0 + u + (lane >> 1) * STREAM_WAVES) + (lane & 1);
+                held_block = (int64_t)blk * KV_BLOCK < s.len ? kv_block(a.pool, a.batch, b, head, blk) : -1;
+                held_scale = held_block >= 0 ? reinterpret_cast<const uint16_t *>(a.pool.scales)[held_block] : 0;
+            }
+            const int b0 = wave_pick(held_block, 2 * k), b1 = wave_pick(held_block, 2 * k + 1);
+            const int s0 = wave_pick(held_scale, 2 * k), s1 = wave_pick(held_scale, 2 * k + 1);
+            const uint8_t *p0 = a.pool.codes + (int64_t)max(b0, 0) * (64 * D), *p1 = a.pool.codes + (int64_t)max(b1, 0) * (64 * D);
+            const uint8_t *kp = (t16 & 8 ? p1 : p0) + (g >> 1) * 1024 + (g & 1) * 512 + (t16 & 7) * 16;
+            const uint8_t *vp = (g & 2 ? p1 : p0) + 32 * D + (g & 1) * 512 + t16 * 16;
+            v4u kr[4][J], vr[C][2];
+#pragma unroll
+            for (int x = 0; x < 4; x++)
+#pragma unroll
+                for (int j = 0; j < J; j++) kr[x][j] = *reinterpret_cast<const v4u *>(kp + j * 2048 + x * 128);
+#pragma unroll
+            for (int c = 0; c < C; c++)
+#pragma unroll
+                for (int x = 0; x < 2; x++) vr[c][x] = *reinterpret_cast<const v4u *>(vp + c * 1024 + x * 256);
+
+            const int mine = g & 2 ? s1 : s0, token = (pair0 + u) * STREAM_PAIR + (g & 2 ? 32 : 0) + (g & 1) * 4;
+            const bool have = (g & 2 ? b1 : b0) >= 0;
+            // the score's factor; never 0, for -infinity times 0 is no mask
+            const float f = fmaxf(ldexpf(a.scale_log2, (mine & 255) - 127), 1.17549435e-38f);
+
+            // subtile x = 2 i + q holds tokens 16 i + 8 q + 4 h + r
+            v4f st[NR][4];
+#pragma unroll
+            for (int x = 0; x < 4; x++) {
+#pragma unroll
+                for (int n = 0; n < NR; n++) st[n][x] = v4f{0, 0, 0, 0};
+#pragma unroll
+                for (int j = 0; j < J; j++) {
+                    const v4u k0 = widen_e4m3<BF16>(kr[x][j][0], kr[x][j][1], 1.0f), k1 = widen_e4m3<BF16>(kr[x][j][2], kr[x][j][3], 1.0f);
+#pragma unroll
+                    for (int n = 0; n < NR; n++) {
+                        st[n][x] = mfma_16x16x32<BF16>(k0, q[n][j][0], st[n][x]);
+                        st[n][x] = mfma_16x16x32<BF16>(k1, q[n][j][1], st[n][x]);
+                    }
+                }
+            }
+            const int tokens0 = (pair0 + u) * STREAM_PAIR;
+            const bool whole = b0 >= 0 && b1 >= 0 && tokens0 + STREAM_PAIR <= s.len;
+            if (!whole || tokens0 < every_lo || tokens0 + STREAM_PAIR > every_hi) {
+#pragma unroll
+                for (int n = 0; n < NR; n++)
+#pragma unroll
+                    for (int x = 0; x < 4; x++)
+#pragma unroll
+                        for (int r = 0; r < 4; r++) {
+                            const int t = token + 8 * x + r;
+                            if (!have || t < row_lo[n] || t >= row_hi[n]) st[n][x][r] = -INFINITY;
+                        }
+            }
+            if (!whole) {  // nothing but zeros where there is no token
+                const int t0 = tokens0 + (g & 2 ? 32 : 0), in = have ? min(max(s.len - t0, 0), KV_BLOCK) : 0;
+#pragma unroll
+                for (int x = 0; x < 4; x++) {
+                    const uint32_t mask = kv_token_bytes(x >> 1, x & 1, g & 1, 0, in);
+#pragma unroll
+                    for (int c = 0; c < C; c++) vr[c][0][x] &= mask, vr[c][1][x] &= mask;
+                }
+            }
+
+            float top[NR];
+            bool raise = false;
+#pragma unroll
+            for (int n = 0; n < NR; n++) {
+                float t = st[n][0][0];
+#pragma unroll
+                for (int x = 0; x < 4; x++)
+#pragma unroll
+                    for (int r = 0; r < 4; r++) t = fmaxf(t, st[n][x][r]);
+                top[n] = over_groups(t * f, [](float x, float y) { return fmaxf(x, y); });
+                raise |= top[n] > m[n] + ATT_RAISE;
+            }
+            const int e0 = b0 >= 0 ? (s0 >> 8) - 127 : -1000, e1 = b1 >= 0 ? (s1 >> 8) - 127 : -1000;
+            const int e = max(e0, e1);
+            if (__ballot(raise) != 0 || e > E) {
+                const float down = e > E ? power_of_two(E - e) : 1.0f;
+#pragma unroll
+                for (int n = 0; n < NR; n++) {
+                    const bool up = top[n] > m[n] + ATT_RAISE;
+                    const float alpha = up ? __builtin_amdgcn_exp2f(m[n] - top[n]) : 1.0f, beta = alpha * down;
+                    if (up) m[n] = top[n];
+                    l[n] *= alpha;
+#pragma unroll
+                    for (int c = 0; c < C; c++)
+#pragma unroll
+                        for (int x = 0; x < 2; x++)
+#pragma unroll
+                            for (int r = 0; r < 4; r++) o[n][c][x][r] *= beta;
+                }
+                E = max(E, e);
+            }
+            uint32_t p[NR][4][2];
+#pragma unroll
+            for (int n = 0; n < NR; n++) {
+                const float base = (m[n] > -INFINITY ? m[n] : 0.0f) - ATT_LIFT;
+#pragma unroll
+                for (int x = 0; x < 4; x++)
+#pragma unroll
+                    for (int r = 0; r < 2; r++) {
+                        p[n][x][r] = f16_pair(__builtin_amdgcn_exp2f(__builtin_fmaf(st[n][x][2 * r], f, -base)),
+                                              __builtin_amdgcn_exp2f(__builtin_fmaf(st[n][x][2 * r + 1], f, -base)));
+                        l[n] = add_pair(p[n][x][r], l[n]);
+                    }
+            }
+            const float unit = power_of_two((have ? (mine >> 8) - 127 : -1000) - E);
+#pragma unroll
+            for (int c = 0; c < C; c++)
+#pragma unroll
+                for (int x = 0; x < 2; x++)
+#pragma unroll
+                    for (int i = 0; i < 2; i++) {
+                        const v4u v = widen_e4m3<false>(vr[c][x][i], vr[c][x][2 + i], unit);
+#pragma unroll
+                        for (int n = 0; n < NR; n++)
+                            o[n][c][x] = mfma_16x16x32<false>(
+                                v, v4u{p[n][2 * i][0], p[n][2 * i][1], p[n][2 * i + 1][0], p[n][2 * i + 1][1]}, o[n][c][x]);
+                    }
+        }
+
+        // the waves' sums, on the largest of their maxima
+        const bool done = step == 0 && stop == steps;
+#pragma unroll
+        for (int n = 0; n < NR; n++) {
+            l[n] = over_groups(l[n], [](float x, float y) { return x + y; });
+            if (g == 0) mls[wave][16 * n + t16][0] = m[n], mls[wave][16 * n + t16][1] = l[n];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < NR; n++) {
+            float M = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < STREAM_WAVES; w++) M = fmaxf(M, mls[w][16 * n + t16][0]);
+            const float alpha = m[n] > -INFINITY ? __builtin_amdgcn_exp2f(m[n] - M) : 0.0f;
+            if (16 * n + t16 < rows) {
+#pragma unroll
+                for (int c = 0; c < C; c++)
+#pragma unroll
+                    for (int x = 0; x < 2; x++) {
+                        v4f y = o[n][c][x];
+#pragma unroll
+                        for (int r = 0; r < 4; r++) y[r] = ldexpf(y[r] * alpha, E);
+                        *reinterpret_cast<v4f *>(sums + (wave * R + 16 * n + t16) * PITCH + 32 * c + 16 * x + 4 * g) = y;
+                    }
+            }
+        }
+        __syncthreads();
+        const int64_t slot = 2 * (int64_t)blockIdx.x + (step == 0 ? 1 : 0);  // of a tile begun here, or before
+        for (int at = tid; at < rows * (D / 4); at += 64 * STREAM_WAVES) {
+            const int r = at / (D / 4), d = at % (D / 4) * 4;
+            float M = -INFINITY, total = 0.0f;
+#pragma unroll
+            for (int w = 0; w < STREAM_WAVES; w++) M = fmaxf(M, mls[w][r][0]);
+#pragma unroll
+            for (int w = 0; w < STREAM_WAVES; w++)
+                total += mls[w][r][0] > -INFINITY ? __builtin_amdgcn_exp2f(mls[w][r][0] - M) * mls[w][r][1] : mls[w][r][1];
+            v4f y = {0, 0, 0, 0};
+#pragma unroll
+            for (int w = 0; w < STREAM_WAVES; w++) y += *reinterpret_cast<const v4f *>(sums + (w * R + r) * PITCH + d);
+            if (!done) {
+                *reinterpret_cast<v4f *>(a.part + (slot * R + r) * D + d) = y;
+                if (d == 0) a.part_ml[(slot * R + r) * 2] = M, a.part_ml[(slot * R + r) * 2 + 1] = total;
+                continue;
+            }
+            attend_store(a, s.row, tile * R + r, head, d, y, M, total);
+        }
+        left -= stop - step;
+        if (left <= 0 || !a.workers) return;
+        // the next tile, head, sequence
+        step = 0;
+        if (++tile == tiles_of<R>(a, s)) {
+            tile = 0;
+            if (++head == heads) {
+                head = 0;
+                do b++;
+                while (b < a.batch.seqs && kv_seq(a.batch, page_tokens, b).n == 0);
+                if (b >= a.batch.seqs) return;
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// One row of a tile whose tokens several workers had: their sums joined, always
+// in the workers' order.
+template <int D, int R>
+__global__ __launch_bounds__(64 * STREAM_WAVES) void attend_join_kernel(AttendArgs a) {
+    __shared__ __align__(16) float sums[STREAM_WAVES][D];
+    __shared__ float weights[STREAM_WAVES];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid / 64);
+    const int page_tokens = a.pool.per_page * KV_BLOCK, heads = a.pool.heads, row = (int)blockIdx.y;
+    int32_t tile = (int32_t)(blockIdx.x / heads);
+    const int head = (int)(blockIdx.x % heads);
+    const int b = kv_find(a.batch.seqs, tile, lane, [&](int i) { return tiles_of<R>(a, kv_seq(a.batch, page_tokens, i)); });
+    if (b < 0) return;
+    const KvSeq s = kv_seq(a.batch, page_tokens, b);
+    if (row >= (int64_t)s.n * a.group - (int64_t)tile * R) return;
+    int64_t before = 0, own = 0, all = 0;  // steps of the sequences before, of this one, of all: for one head
+    for (int i = lane; i < a.batch.seqs; i += 64) {
+        const int64_t n = steps_of<R>(a, kv_seq(a.batch, page_tokens, i));
+        all += n;
+        if (i < b) before += n;
+        if (i == b) own += n;
+    }
+    all = wave_pick(wave_scan(all, lane), 63) * heads;
+    before = wave_pick(wave_scan(before, lane), 63) * heads;
+    own = wave_pick(wave_scan(own, lane), 63);
+    int64_t begin = before + head * own;
+    for (int t = 0; t < tile; t++) begin += steps_of<R>(a, s, t);
+    const int64_t end = begin + steps_of<R>(a, s, tile), used = workers_used(all, a.workers);
+    const int w0 = (int)(((begin + 1) * used - 1) / all), w1 = (int)((end * used - 1) / all);
+    if (w0 == w1) return;  // written by its only worker
+
+    auto slot = [&](int w) { return (int64_t)(2 * w + (w == w0 ? 1 : 0)) * R + row; };
+    float m = -INFINITY;
+    for (int w = w0 + lane; w <= w1; w += 64) m = fmaxf(m, a.part_ml[slot(w) * 2]);
+#pragma unroll
+    for (int x = 1; x < 64; x *= 2) m = fmaxf(m, __shfl_xor(m, x));
+    float y[D / 64] = {}, total = 0.0f;
+#pragma unroll 4
+    for (int w = w0 + wave; w <= w1; w += STREAM_WAVES) {
+        const float mw = a.part_ml[slot(w) * 2], f = mw > -INFINITY ? __builtin_amdgcn_exp2f(mw - m) : 1.0f;
+        total += f * a.part_ml[slot(w) * 2 + 1];
+#pragma unroll
+        for (int i = 0; i < D / 64; i++) y[i] += f * a.part[slot(w) * D + 64 * i + lane];
+    }
+#pragma unroll
+    for (int i = 0; i < D / 64; i++) sums[wave][64 * i + lane] = y[i];
+    if (lane == 0) weights[wave] = total;
+    __syncthreads();
+    if (tid >= D / 4) return;
+    v4f z = {0, 0, 0, 0};
+    total = 0.0f;
+#pragma unroll
+    for (int w = 0; w < STREAM_WAVES; w++) z += reinterpret_cast<const v4f *>(sums[w])[tid], total += weights[w];
+    attend_store(a, s.row, tile * R + row, head, tid * 4, z, m, total);
+}
+
+}  // namespace w4a4

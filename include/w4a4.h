@@ -55,8 +55,8 @@ typedef enum {
 } w4a4_status;
 
 /* W4A4_DTYPE_BF16 is taken by the calls from w4a4_quantize_mx4 on (the
- * quantised-row producers, the read-back and the MXFP4 product); the others
- * return W4A4_ERR_UNSUPPORTED_DTYPE for it. */
+ * quantised-row producers, the read-back, the MXFP4 product and the key/value
+ * cache); the others return W4A4_ERR_UNSUPPORTED_DTYPE for it. */
 typedef enum { W4A4_DTYPE_F32 = 0, W4A4_DTYPE_F16 = 1, W4A4_DTYPE_BF16 = 2 } w4a4_dtype;
 
 /* Human-readable name of a status.  Host only; never NULL. */
@@ -646,6 +646,148 @@ size_t w4a4_gemm_mx4_plan(int64_t m, int64_t n, int64_t k, char *text, size_t by
 w4a4_status w4a4_gemm_mx4(const void *packed_w, const uint8_t *codes, const uint8_t *scales, void *y, w4a4_dtype ydt,
                           int64_t m, int64_t n, int64_t k, int64_t ldy, void *workspace, size_t workspace_bytes,
                           void *stream);
+
+/*
+ * The paged key/value cache in 8 bits, what writes it and what reads it.
+ *
+ * A page holds `page` tokens (a multiple of 32) of one sequence for each of
+ * `heads` key/value heads of width `dim` (64, 128 or 256).  Per page, head and
+ * block of 32 tokens: 32 dim bytes of key codes, then 32 dim of value codes, OCP
+ * E4M3, and two E8M0 scale bytes, the keys' and the values'; a code c stands for
+ * c 2^(byte - 127).
+ *   codes   [pages][heads][page / 32][2][32 dim] bytes, 16-byte aligned.  Keys:
+ *           channel 32 c + 16 h + j of token t of the block at byte 1024 c +
+ *           512 h + 16 t + j.  Values: channel 32 c + d of token 16 i + 8 q + 4 h + r
+ *           at byte 1024 c + 512 h + 16 d + 8 q + 4 i + r.
+ *   scales  [pages][heads][page / 32][2] bytes, 2-byte aligned.
+ * Where a sequence's tokens lie is the caller's to say, per call:
+ *   pages   [seqs][ld] int32, the first pages_per_seq of a row: page i of
+ *           sequence b holds its tokens i page ... i page + page - 1.  An entry
+ *           outside [0, cache pages) is no page: what would be written there is
+ *           dropped, attention passes over it, and it reads back as zeros.
+ *   starts  [seqs + 1] int32, ascending: sequence b has rows starts[b] ...
+ *           starts[b + 1] - 1 of the call (new tokens, queries, rows read back).
+ *   lens    [seqs] int32: sequence b's tokens with these rows; its last row is
+ *           token lens[b] - 1, at most pages_per_seq page tokens.  Rows before
+ *           token 0 (more rows than tokens) have no token.
+ * These arrays are read on the device; no entry makes a call read or write
+ * outside its buffers.  Rows outside every sequence are left as they were.
+ * Bounds: rows at most 2097120, seqs at most 65536, query heads at most 8192, pages
+ * * heads * (page / 32) and pages_per_seq * page below 2^31.
+ */
+typedef struct {
+    void *codes;
+    uint8_t *scales;
+    int64_t pages, page, heads, dim;
+} w4a4_kv_cache;
+typedef struct {
+    const int32_t *pages;
+    int64_t ld, pages_per_seq;
+    const int32_t *starts, *lens;
+    int64_t seqs, rows;
+} w4a4_kv_batch;
+
+/* Rows of heads: channel i of head h of row r at data[r row_stride + h
+ * head_stride + i] (strides in elements; element-aligned).  Inputs may have any
+ * strides >= 0; an output's rows and heads may not overlap. */
+typedef struct {
+    void *data;
+    int64_t row_stride, head_stride;
+} w4a4_head_rows;
+
+/* Rotary positions of the leading `width` channels of a head (a multiple of 16, at
+ * most dim): pair i of width / 2 is turned by the angle whose cosine and sine are
+ * table[p][i] and table[p][width / 2 + i], p the row's position.
+ *   table        [table_rows][width] fp32, 4-byte aligned.
+ *   positions    NULL: a row's position is its token's number in the sequence.
+ *                Else [n_axes][ld] int32, one position a row and axis.
+ *   axes         NULL (n_axes 1), or [width / 2] bytes: the axis whose position
+ *                turns pair i (time, height and width of an image's tokens, say).
+ *   interleaved  0: pair i is channels i and width / 2 + i; else 2 i and 2 i + 1.
+ * A position outside the table, or an axis outside the positions, turns by NaN. */
+typedef struct {
+    const float *table;
+    int64_t table_rows, width;
+    const int32_t *positions;
+    int64_t ld;
+    const uint8_t *axes;
+    int64_t n_axes;
+    int interleaved;
+} w4a4_rope;
+
+/* Bytes of the two buffers of a cache (0 for invalid sizes).  Host only, pure. */
+size_t w4a4_kv_cache_code_bytes(int64_t pages, int64_t page, int64_t heads, int64_t dim);
+size_t w4a4_kv_cache_scale_bytes(int64_t pages, int64_t page, int64_t heads, int64_t dim);
+
+/*
+ * New tokens' keys and values into the cache, and their queries for attention, in
+ * one launch.  Per head row x (k and q, fp32 throughout, one rounding an
+ * operation): x = fl(fl(x * s) * weight) with s = fp32(1 / sqrt(sum x^2 / dim +
+ * eps)) (sum and root in fp64) where there is a weight; then each pair (a, b) of
+ * rope becomes (fl(fl(a cos) - fl(b sin)), fl(fl(b cos) + fl(a sin))).  q is rounded
+ * to q_out's type.  k and v are rounded to the block's grid: e is the least integer
+ * >= -127 for which the largest magnitude of the call's rows in the block (one head,
+ * keys and values each) is at most 448 * 2^e, or the block's present e where that is
+ * larger and the block holds tokens before the sequence's first row.  Codes are x *
+ * 2^-e to the nearest E4M3 value, ties to even.  Where e grows, the codes of the
+ * tokens before are rounded to the new grid.  A token whose key or value row holds a
+ * NaN or an infinity, for one head, gets NaN key codes and zero value codes and does
+ * not count for e: a query row that sees it has no finite output, and others do not
+ * notice.  Codes behind a sequence's last token are left as they were.
+ *   dt        type of q, k and v (fp32, fp16 or bf16).
+ *   k, v      [rows][heads][dim].
+ *   q, q_out  [rows][q_heads][dim] or both data NULL; q_out's type, odt, fp16 or
+ *             bf16.  q_out may be q (same strides, odt == dt).
+ *   q_weight, k_weight  [dim] fp32 or NULL; 4-byte aligned.
+ *   eps       > 0, finite (read only where there is a weight).
+ *   rope      NULL: no rotation.
+ * Two sequences of a call may not write one block.
+ * Errors: an unknown type, or odt fp32 -> W4A4_ERR_UNSUPPORTED_DTYPE; sizes past
+ * the bounds, a dim or page as above, a bad stride, width, eps or table, null
+ * pointers with work to do -> W4A4_ERR_INVALID_VALUE; misalignment ->
+ * W4A4_ERR_MISALIGNED.
+ */
+w4a4_status w4a4_append_kv(w4a4_dtype dt, const w4a4_head_rows *k, const w4a4_head_rows *v, const w4a4_head_rows *q,
+                           int64_t q_heads, const w4a4_head_rows *q_out, w4a4_dtype odt, const float *q_weight,
+                           const float *k_weight, double eps, const w4a4_rope *rope, const w4a4_kv_cache *cache,
+                           const w4a4_kv_batch *batch, void *stream);
+
+/*
+ * The tokens of a batch's rows read back: k and v, [rows][heads][dim] of type dt,
+ * value fl(code * 2^(byte - 127)) rounded to dt (exact in bf16 and fp32).
+ */
+w4a4_status w4a4_read_kv(const w4a4_kv_cache *cache, const w4a4_kv_batch *batch, w4a4_dtype dt, const w4a4_head_rows *k,
+                         const w4a4_head_rows *v, void *stream);
+
+/*
+ * Attention of a batch's rows over the cache.  Query head h reads key/value head
+ * h / (q_heads / heads).  A row that is token p of its sequence sees the tokens j <
+ * lens[b] that have a page, with j <= p if causal, and j > p - window if window > 0:
+ *   s_j = scale sum_i q_i k_ji,  out = sum_j e^(s_j) v_j / sum_j e^(s_j)
+ * and lse = log sum_j e^(s_j).  A row that sees nothing, or only scores of minus
+ * infinity, gets zeros and lse minus infinity.  Products are summed in fp32, weights
+ * rounded to fp16.  Tokens that a row does not see do not reach it, whatever they hold
+ * (value codes are taken to hold no NaN, and w4a4_append_kv writes none).
+ *   q     [rows][q_heads][dim] of type dt, fp16 or bf16.
+ *   out   [rows][q_heads][dim] of type odt, fp16 or bf16; may be q (odt == dt, same
+ *         strides).
+ *   lse   [rows][ld_lse] fp32, ld_lse >= q_heads, or NULL.
+ *   scale > 0, finite.  window >= 0.
+ *   workspace  w4a4_attention_kv_workspace_bytes(rows, seqs, q_heads, heads, dim,
+ *         pages_per_seq * page) bytes, 256-byte aligned (may be NULL when that is 0);
+ *         contents on entry are ignored, calls that share one must not overlap,
+ *         replays of captured calls among them.
+ * The result of a row does not depend on the other sequences of the call but for
+ * the order of its fp32 sums, which is fixed for a call's sizes and lens.
+ * Errors: dt or odt neither fp16 nor bf16 -> W4A4_ERR_UNSUPPORTED_DTYPE; the others
+ * as w4a4_append_kv, with W4A4_ERR_WORKSPACE_TOO_SMALL.
+ */
+size_t w4a4_attention_kv_workspace_bytes(int64_t rows, int64_t seqs, int64_t q_heads, int64_t heads, int64_t dim,
+                                         int64_t tokens);
+w4a4_status w4a4_attention_kv(const w4a4_head_rows *q, w4a4_dtype dt, int64_t q_heads, const w4a4_head_rows *out,
+                              w4a4_dtype odt, float *lse, int64_t ld_lse, double scale, int causal, int64_t window,
+                              const w4a4_kv_cache *cache, const w4a4_kv_batch *batch, void *workspace,
+                              size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }
