@@ -41,6 +41,7 @@ struct AttendArgs {
     KvBatch batch;
     // partial results: [slots][rows of a tile][D] sums, then [slots][rows][2] maxima and sums
     float *part, *part_ml;
+    int32_t splits;      // workgroups that share a tile's tokens (many rows)
     int32_t workers;     // workgroups that share all tiles' tokens evenly; 0: one workgroup a tile and head
     int32_t tile_bound;  // at least the tiles of the batch
 };
@@ -77,12 +78,23 @@ __device__ __forceinline__ float add_pair(uint32_t x, float c) {
 }
 __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(min(max(e, -126), 127) + 127) << 23); }
 
-// x over the lanes l, l ^ 16, l ^ 32 and l ^ 48.
+// x over the lanes l and l ^ 32; over l, l ^ 16, l ^ 32 and l ^ 48.
+template <class F>
+__device__ __forceinline__ float over_halves(float x, F f) {
+    const auto y = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return f(__uint_as_float(y[0]), __uint_as_float(y[1]));
+}
 template <class F>
 __device__ __forceinline__ float over_groups(float x, F f) {
-    x = f(x, __shfl_xor(x, 16));
-    return f(x, __shfl_xor(x, 32));
+    const auto y = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return over_halves(f(__uint_as_float(y[0]), __uint_as_float(y[1])), f);
 }
+struct Larger {
+    __device__ __forceinline__ float operator()(float x, float y) const { return fmaxf(x, y); }
+};
+struct Sum {
+    __device__ __forceinline__ float operator()(float x, float y) const { return x + y; }
+};
 
 // The tokens that rows [r0, r1) of a sequence's head group see: [lo, hi), in
 // tokens; hi <= lo: none.
@@ -302,7 +314,7 @@ __global__ __launch_bounds__(64 * STREAM_WAVES) void attend_stream_kernel(Attend
                 for (int x = 0; x < 4; x++)
 #pragma unroll
                     for (int r = 0; r < 4; r++) t = fmaxf(t, st[n][x][r]);
-                top[n] = over_groups(t * f, [](float x, float y) { return fmaxf(x, y); });
+                top[n] = over_groups(t * f, Larger{});
                 raise |= top[n] > m[n] + ATT_RAISE;
             }
             const int e0 = b0 >= 0 ? (s0 >> 8) - 127 : -1000, e1 = b1 >= 0 ? (s1 >> 8) - 127 : -1000;
@@ -356,7 +368,7 @@ __global__ __launch_bounds__(64 * STREAM_WAVES) void attend_stream_kernel(Attend
         const bool done = step == 0 && stop == steps;
 #pragma unroll
         for (int n = 0; n < NR; n++) {
-            l[n] = over_groups(l[n], [](float x, float y) { return x + y; });
+            l[n] = over_groups(l[n], Sum{});
             if (g == 0) mls[wave][16 * n + t16][0] = m[n], mls[wave][16 * n + t16][1] = l[n];
         }
         __syncthreads();
@@ -468,6 +480,279 @@ __global__ __launch_bounds__(64 * STREAM_WAVES) void attend_join_kernel(AttendAr
 #pragma unroll
     for (int w = 0; w < STREAM_WAVES; w++) z += reinterpret_cast<const v4f *>(sums[w])[tid], total += weights[w];
     attend_store(a, s.row, tile * R + row, head, tid * 4, z, m, total);
+}
+
+
+// ---------------------------------------------------------------------------
+// Many rows: a workgroup's waves share the cache's blocks through LDS
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ v16f mfma_32x32x16_f16(v4u a, v4u b, v16f c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
+}
+template <bool BF16>
+__device__ __forceinline__ v16f mfma_32x32x16(v4u a, v4u b, v16f c) {
+    if constexpr (BF16)
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8b, a), __builtin_bit_cast(v8b, b), c, 0, 0, 0);
+    else return mfma_32x32x16_f16(a, b, c);
+}
+
+// 16 bytes a lane from p to LDS byte address lds + 16 lane (uniform), without
+// passing registers; counted by vmcnt, unseen by the compiler.
+__device__ __forceinline__ void att_load16(const uint8_t *p, uint32_t lds) {
+    uint32_t m0;  // written; the load that reads it needs one wait state
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : "={m0}"(m0) : "v"(p), "s"(lds) : "memory");
+}
+
+// RW waves of 32 rows each, times TW that take turns at a stage's blocks.
+template <int D_, int RW_>
+struct AttTile {
+    static constexpr int D = D_, RW = RW_, WAVES = 8, TW = WAVES / RW, ROWS = 32 * RW, THREADS = 64 * WAVES;
+    static constexpr int BLOCK_BYTES = 64 * D;
+    static constexpr int SB = D == 256 ? (TW > 2 ? TW : 2) : (TW > 4 ? TW : 4);  // blocks of a stage
+    static constexpr int RING = SB * BLOCK_BYTES > 49152 ? 2 : 3;                // stages in LDS
+    static constexpr int LOADS = SB * BLOCK_BYTES / 1024 / WAVES;                // of a wave and stage
+    static constexpr int RING_BYTES = RING * SB * BLOCK_BYTES;
+    static constexpr int JOIN_BYTES = TW > 1 ? 4 * 32 * D * 4 + 4 * 64 * 8 + 64 : 0;  // half the waves' sums, maxima and exponents
+    static constexpr int LDS = RING_BYTES > JOIN_BYTES ? RING_BYTES : JOIN_BYTES;
+    static_assert(SB % TW == 0 && 64 % SB == 0 && LOADS >= 1 && LOADS * WAVES * 1024 == SB * BLOCK_BYTES && LDS <= 163840, "");
+};
+
+template <int N>
+__device__ __forceinline__ void att_wait() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
+
+template <class C, bool BF16>
+__global__ __launch_bounds__(C::THREADS) void attend_tile_kernel(AttendArgs a) {
+    constexpr int D = C::D, N = D / 32;
+    __shared__ __align__(1024) uint8_t smem[C::LDS];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid / 64);
+    const int rw = wave % C::RW, tw = wave / C::RW, col = lane & 31, h = lane >> 5;
+    const int page_tokens = a.pool.per_page * KV_BLOCK, heads = a.pool.heads;
+
+    // splits and heads first, so that workgroups of one XCD share keys and values;
+    // the last tiles, which see most, first
+    const int split = (int)(blockIdx.x % a.splits), task = (int)(blockIdx.x / a.splits), head = task % heads;
+    const int order = a.tile_bound - 1 - task / heads;
+    int32_t tile = order;
+    const int b = kv_find(a.batch.seqs, tile, lane, [&](int i) { return tiles_of<C::ROWS>(a, kv_seq(a.batch, page_tokens, i)); });
+    if (b < 0) return;
+    const KvSeq s = kv_seq(a.batch, page_tokens, b);
+    const int all_rows = (int)((int64_t)s.n * a.group), row0 = tile * C::ROWS, rows = min(C::ROWS, all_rows - row0);
+    const Span span = span_of(a, s, row0, row0 + rows);
+    const int first_block = span.lo / KV_BLOCK, blocks_all = span.hi <= span.lo ? 0 : (span.hi - 1) / KV_BLOCK + 1 - first_block;
+    const int stages_all = (blocks_all + C::SB - 1) / C::SB;
+    const int begin = (int)((int64_t)stages_all * split / a.splits), stages = (int)((int64_t)stages_all * (split + 1) / a.splits) - begin;
+    const int block0 = first_block + begin * C::SB, blocks = min(stages * C::SB, blocks_all - begin * C::SB);
+
+    // this wave's rows
+    const int wrow0 = row0 + 32 * rw, wrows = min(max(rows - 32 * rw, 0), 32);
+    const bool live = col < wrows;
+    const int r = live ? wrow0 + col : row0, qi = r / a.group;
+    v4u q[N][2];
+    {
+        const uint8_t *p = a.q + ((int64_t)(s.row + qi) * a.q_row + (int64_t)(head * a.group + r - qi * a.group) * a.q_head) * 2;
+#pragma unroll
+        for (int c = 0; c < N; c++)
+#pragma unroll
+            for (int i = 0; i < 2; i++) q[c][i] = *reinterpret_cast<const v4u_any *>(p + (32 * c + 16 * h + 8 * i) * 2);
+    }
+    const Span mine = span_of(a, s, r, r + 1);
+    const int row_lo = mine.lo, row_hi = live ? mine.hi : 0;
+    const Span wspan = wrows ? span_of(a, s, wrow0, wrow0 + wrows) : Span{0, 0};
+    const int every_lo = wrows ? span_of(a, s, wrow0 + wrows - 1, wrow0 + wrows).lo : 0;
+    const int every_hi = wrows ? span_of(a, s, wrow0, wrow0 + 1).hi : 0;
+
+    // lane i: block i of the next 64 of this workgroup's; scales -1 where it is none
+    int held_block = 0, held_scale = -1, before_scale = -1, held_chunk = -1;
+    auto fetch = [&](int chunk) {
+        const int rel = chunk * 64 + lane, blk = block0 + rel;
+        before_scale = held_scale, held_chunk = chunk;
+        const int at = rel < blocks ? kv_block(a.pool, a.batch, b, head, blk) : -1;
+        held_block = max(at, 0);
+        held_scale = at >= 0 ? reinterpret_cast<const uint16_t *>(a.pool.scales)[at] : -1;
+    };
+    const uint32_t ring = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)smem;
+    auto load = [&](int stage) {
+        if (stage * C::SB / 64 != held_chunk) fetch(stage * C::SB / 64);
+        const uint32_t to = ring + (uint32_t)(stage % C::RING) * (C::SB * C::BLOCK_BYTES);
+#pragma unroll
+        for (int i = 0; i < C::LOADS; i++) {
+            const int unit = wave + i * C::WAVES, j = unit / (D / 16);
+            const int at = wave_pick(held_block, (stage * C::SB + j) & 63);
+            att_load16(a.pool.codes + (int64_t)at * C::BLOCK_BYTES + unit % (D / 16) * 1024 + lane * 16,
+                       __builtin_amdgcn_readfirstlane(to + unit * 1024));
+        }
+    };
+
+    float m = -INFINITY, l = 0.0f;
+    int E = -1000;
+    v16f o[N];
+#pragma unroll
+    for (int c = 0; c < N; c++) o[c] = v16f{};
+
+#pragma unroll
+    for (int i = 0; i < C::RING - 1; i++)
+        if (i < stages) load(i);
+    for (int st = 0; st < stages; st++) {
+        if (C::RING > 2 && st + 1 < stages) att_wait<(C::RING - 2) * C::LOADS>();
+        else att_wait<0>();
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");  // no read of the stage moves up
+        if (st + C::RING - 1 < stages) load(st + C::RING - 1);
+        const uint8_t *stage = smem + st % C::RING * (C::SB * C::BLOCK_BYTES);
+#pragma unroll 1
+        for (int j = tw; j < C::SB; j += C::TW) {
+            const int rel = st * C::SB + j, token0 = (block0 + rel) * KV_BLOCK;
+            const int scale = wave_pick(rel / 64 == held_chunk ? held_scale : before_scale, rel & 63);
+            if (scale < 0 || token0 + KV_BLOCK <= wspan.lo || token0 >= wspan.hi) continue;
+            const uint8_t *p = stage + j * C::BLOCK_BYTES + lane * 16;
+            v16f t = {};
+#pragma unroll
+            for (int c = 0; c < N; c++) {
+                const v4u x = *reinterpret_cast<const v4u *>(p + c * 1024);
+                t = mfma_32x32x16<BF16>(widen_e4m3<BF16>(x[0], x[1], 1.0f), q[c][0], t);
+                t = mfma_32x32x16<BF16>(widen_e4m3<BF16>(x[2], x[3], 1.0f), q[c][1], t);
+            }
+            const float f = fmaxf(ldexpf(a.scale_log2, (scale & 255) - 127), 1.17549435e-38f);  // never 0: -infinity stays
+            if (token0 < every_lo || token0 + KV_BLOCK > every_hi) {
+#pragma unroll
+                for (int v = 0; v < 16; v++) {
+                    const int at = token0 + mfma32_row(v, lane);
+                    if (at < row_lo || at >= row_hi) t[v] = -INFINITY;
+                }
+            }
+            float top = t[0];
+#pragma unroll
+            for (int v = 1; v < 16; v++) top = fmaxf(top, t[v]);
+            top = over_halves(top * f, Larger{});
+            const bool up = top > m + ATT_RAISE;
+            const int e = (scale >> 8) - 127;
+            if (__ballot(up) != 0 || e > E) {
+                const float alpha = up ? __builtin_amdgcn_exp2f(m - top) : 1.0f, beta = alpha * (e > E ? power_of_two(E - e) : 1.0f);
+                if (up) m = top;
+                l *= alpha, E = max(E, e);
+#pragma unroll
+                for (int c = 0; c < N; c++)
+#pragma unroll
+                    for (int v = 0; v < 16; v++) o[c][v] *= beta;
+            }
+            const float base = (m > -INFINITY ? m : 0.0f) - ATT_LIFT;
+            v4u w[2];
+#pragma unroll
+            for (int v = 0; v < 8; v++) {
+                const uint32_t x = f16_pair(__builtin_amdgcn_exp2f(__builtin_fmaf(t[2 * v], f, -base)),
+                                            __builtin_amdgcn_exp2f(__builtin_fmaf(t[2 * v + 1], f, -base)));
+                w[v / 4][v % 4] = x;
+                l = add_pair(x, l);
+            }
+            const float unit = power_of_two(e - E);
+            const bool tail = token0 + KV_BLOCK > s.len;  // nothing but zeros where there is no token
+            uint32_t mask[4];
+            if (tail) {
+#pragma unroll
+                for (int x = 0; x < 4; x++) mask[x] = kv_token_bytes(x >> 1, x & 1, h, 0, s.len - token0);
+            }
+#pragma unroll
+            for (int c = 0; c < N; c++) {
+                v4u x = *reinterpret_cast<const v4u *>(p + 32 * D + c * 1024);
+                if (tail) {
+#pragma unroll
+                    for (int y = 0; y < 4; y++) x[y] &= mask[y];
+                }
+                o[c] = mfma_32x32x16_f16(widen_e4m3<false>(x[0], x[2], unit), w[0], o[c]);
+                o[c] = mfma_32x32x16_f16(widen_e4m3<false>(x[1], x[3], unit), w[1], o[c]);
+            }
+        }
+    }
+
+    // the waves of the same rows, two by two
+    l = over_halves(l, Sum{});
+    if constexpr (C::TW > 1) {
+        v4f *sums = reinterpret_cast<v4f *>(smem);  // [wave][N][4][64 lanes]
+        v2f *mls = reinterpret_cast<v2f *>(smem + 4 * 32 * D * 4);
+        int *es = reinterpret_cast<int *>(smem + 4 * 32 * D * 4 + 4 * 64 * 8);
+#pragma unroll
+        for (int half = C::TW / 2; half > 0; half /= 2) {
+            __syncthreads();
+            if (tw >= half && tw < 2 * half) {
+                const int at = wave - half * C::RW;
+                mls[at * 64 + lane] = v2f{m, l};
+                if (lane == 0) es[at] = E;
+#pragma unroll
+                for (int c = 0; c < N; c++)
+#pragma unroll
+                    for (int x = 0; x < 4; x++)
+                        sums[((at * N + c) * 4 + x) * 64 + lane] = v4f{o[c][4 * x], o[c][4 * x + 1], o[c][4 * x + 2], o[c][4 * x + 3]};
+            }
+            __syncthreads();
+            if (tw < half) {
+                const v2f ml = mls[wave * 64 + lane];
+                const int e = __builtin_amdgcn_readfirstlane(es[wave]), eb = max(e, E);
+                const float mb = fmaxf(m, ml.x);
+                const float own = m > -INFINITY ? __builtin_amdgcn_exp2f(m - mb) : 1.0f, other = ml.x > -INFINITY ? __builtin_amdgcn_exp2f(ml.x - mb) : 1.0f;
+                const float fo = own * power_of_two(E - eb), fe = other * power_of_two(e - eb);
+                l = l * own + ml.y * other, m = mb, E = eb;
+#pragma unroll
+                for (int c = 0; c < N; c++)
+#pragma unroll
+                    for (int x = 0; x < 4; x++) {
+                        const v4f y = sums[((wave * N + c) * 4 + x) * 64 + lane];
+#pragma unroll
+                        for (int i = 0; i < 4; i++) o[c][4 * x + i] = o[c][4 * x + i] * fo + y[i] * fe;
+                    }
+            }
+        }
+        if (tw) return;
+    }
+    if (!live) return;
+    const int64_t slot = ((int64_t)(order * heads + head) * a.splits + split) * C::ROWS + 32 * rw + col;
+    if (a.splits > 1 && h == 0) a.part_ml[slot * 2] = m, a.part_ml[slot * 2 + 1] = l;
+    if (a.splits > 1 && E == -1000) return;  // no block: never read
+#pragma unroll
+    for (int c = 0; c < N; c++)
+#pragma unroll
+        for (int x = 0; x < 4; x++) {
+            v4f y;
+#pragma unroll
+            for (int i = 0; i < 4; i++) y[i] = ldexpf(o[c][4 * x + i], E);
+            const int d = 32 * c + 8 * x + 4 * h;
+            if (a.splits > 1) *reinterpret_cast<v4f *>(a.part + slot * D + d) = y;
+            else attend_store(a, s.row, r, head, d, y, m, l);
+        }
+}
+
+// The rows of a tile that `splits` workgroups had the tokens of, a wave a row.
+template <int D, int ROWS>
+__global__ __launch_bounds__(256) void attend_splits_kernel(AttendArgs a) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int page_tokens = a.pool.per_page * KV_BLOCK, heads = a.pool.heads, row = (int)blockIdx.y * 4 + wave;
+    const int order = (int)(blockIdx.x / heads), head = (int)(blockIdx.x % heads);
+    int32_t tile = order;
+    const int b = kv_find(a.batch.seqs, tile, lane, [&](int i) { return tiles_of<ROWS>(a, kv_seq(a.batch, page_tokens, i)); });
+    if (b < 0) return;
+    const KvSeq s = kv_seq(a.batch, page_tokens, b);
+    if (row >= (int64_t)s.n * a.group - (int64_t)tile * ROWS) return;
+    const int64_t slot0 = (int64_t)(order * heads + head) * a.splits * ROWS + row;
+    const v2f own = lane < a.splits ? *reinterpret_cast<const v2f *>(a.part_ml + (slot0 + (int64_t)lane * ROWS) * 2) : v2f{-INFINITY, 0.0f};
+    float m = own.x;
+#pragma unroll
+    for (int x = 1; x < 64; x *= 2) m = fmaxf(m, __shfl_xor(m, x));
+    const float f = own.x > -INFINITY ? __builtin_amdgcn_exp2f(own.x - m) : 1.0f;
+    float total = f * own.y;
+#pragma unroll
+    for (int x = 1; x < 64; x *= 2) total += __shfl_xor(total, x);
+    const uint64_t some = __ballot(own.x > -INFINITY || own.y != 0.0f);  // a split without tokens wrote no sums
+    const int d = lane * 4;
+    v4f y = {0, 0, 0, 0};
+#pragma unroll 4
+    for (int i = 0; i < a.splits; i++) {
+        const float fi = __uint_as_float(wave_pick((int32_t)__float_as_uint(f), i));
+        const v4f x = d < D ? *reinterpret_cast<const v4f *>(a.part + (slot0 + (int64_t)i * ROWS) * D + d) : v4f{0, 0, 0, 0};
+        y = some >> i & 1 ? y + fi * x : y;
+    }
+    if (d < D) attend_store(a, s.row, tile * ROWS + row, head, d, y, m, total);
 }
 
 }  // namespace w4a4

@@ -74,26 +74,73 @@ void with_dim(int64_t dim, F f) {
 // How attention runs for these sizes.
 struct Plan {
     int rows;         // of a tile
+    int waves;        // of a tile's rows, in a workgroup of many rows; 0: few rows, streamed
     int64_t tiles;    // of all sequences, at most
-    int64_t workers;  // 0: a workgroup a tile and head
+    int64_t workers;  // few rows: 0, a workgroup a tile and head, or the workgroups that share all
+    int64_t splits;   // many rows: workgroups that share a tile's tokens
+    int64_t slots(int64_t heads) const { return waves ? (splits > 1 ? tiles * heads * splits : 0) : 2 * workers; }
 };
+int64_t tile_bound(int64_t rows, int64_t seqs, int64_t group, int64_t tile) {
+    return std::min(rows * group / tile + std::min(rows, seqs), rows * ((group + tile - 1) / tile));
+}
+// A workgroup's time for 32 tokens and the 32 rows of each of its waves (us, two
+// waves a SIMD), by the width of a head.
+double block_us(int64_t dim) { return 0.2 + 0.8 * (double)dim / 256; }
+
 Plan plan_of(int64_t rows, int64_t seqs, int64_t q_heads, int64_t heads, int64_t dim, int64_t tokens) {
-    Plan p;
     const int64_t group = q_heads / heads;
-    p.rows = rows * group <= 16 * seqs ? 16 : 32;
-    p.tiles = std::min(rows * group / p.rows + std::min(rows, seqs), rows * ((group + p.rows - 1) / p.rows));
-    const int64_t steps = (tokens + STREAM_PAIR - 1) / STREAM_PAIR, tasks = p.tiles * heads;
-    p.workers = steps <= STREAM_LEAST || tasks >= 4096 ? 0 : std::min<int64_t>(512, tasks * (steps / STREAM_LEAST + 1));
+    Plan p{};
+    if (rows * group <= 32 * seqs) {
+        p.rows = rows * group <= 16 * seqs ? 16 : 32, p.splits = 1;
+        p.tiles = tile_bound(rows, seqs, group, p.rows);
+        const int64_t steps = (tokens + STREAM_PAIR - 1) / STREAM_PAIR, tasks = p.tiles * heads;
+        p.workers = steps <= STREAM_LEAST || tasks >= 4096 ? 0 : std::min<int64_t>(512, tasks * (steps / STREAM_LEAST + 1));
+        return p;
+    }
+    // The waves of a workgroup over rows or over tokens, and tiles whole or split: what
+    // the rounds of 256 workgroups would take, by a workgroup's blocks, its start and
+    // end, and the partial sums written and read.
+    double best = 1e30;
+    const double blocks = (double)((tokens + KV_BLOCK - 1) / KV_BLOCK);
+    for (int waves = 8; waves >= 2; waves /= 2) {
+        const int64_t tiles = tile_bound(rows, seqs, group, 32 * waves), tasks = tiles * heads;
+        for (int64_t splits = 1; splits <= 32; splits++) {
+            if (splits > 1 && (tasks * splits > 1024 || blocks < 4 * (double)splits)) break;
+            const double turns = 8 / waves, rounds = (double)((tasks * splits + 255) / 256);
+            double us = rounds * (4 + std::ceil(blocks / (double)splits / turns) * block_us(dim) + (waves < 8 ? 2 : 0));
+            if (splits > 1) us += 4 + (double)(tasks * splits * 32 * waves * dim * 8) / 4e6;
+            if (us < best) best = us, p = Plan{32 * waves, waves, tiles, 0, splits};
+        }
+    }
     return p;
 }
-size_t part_bytes(const Plan &p, int64_t dim) { return (size_t)(2 * p.workers * p.rows * dim * 4); }
-size_t ml_bytes(const Plan &p) { return (size_t)(2 * p.workers * p.rows * 8); }
+size_t part_bytes(const Plan &p, int64_t heads, int64_t dim) { return (size_t)(p.slots(heads) * p.rows * dim * 4); }
+size_t ml_bytes(const Plan &p, int64_t heads) { return (size_t)(p.slots(heads) * p.rows * 8); }
+size_t workspace_of(const Plan &p, int64_t heads, int64_t dim) {
+    return p.slots(heads) ? up256_bytes(part_bytes(p, heads, dim)) + up256_bytes(ml_bytes(p, heads)) : 0;
+}
 
 template <int D, bool BF16, int NR>
-void launch_attend(const AttendArgs &a, const Plan &p, hipStream_t s) {
+void launch_stream(const AttendArgs &a, const Plan &p, hipStream_t s) {
     const unsigned tasks = (unsigned)(p.tiles * a.pool.heads);
     attend_stream_kernel<D, BF16, NR><<<p.workers ? (unsigned)p.workers : tasks, 64 * STREAM_WAVES, 0, s>>>(a);
     if (p.workers) attend_join_kernel<D, 16 * NR><<<dim3(tasks, 16 * NR), 64 * STREAM_WAVES, 0, s>>>(a);
+}
+template <int D, bool BF16, int RW>
+void launch_tile(const AttendArgs &a, const Plan &p, hipStream_t s) {
+    using C = AttTile<D, RW>;
+    const unsigned tasks = (unsigned)(p.tiles * a.pool.heads);
+    attend_tile_kernel<C, BF16><<<tasks * (unsigned)p.splits, C::THREADS, 0, s>>>(a);
+    if (p.splits > 1) attend_splits_kernel<D, C::ROWS><<<dim3(tasks, C::ROWS / 4), 256, 0, s>>>(a);
+}
+template <int D, bool BF16>
+void launch_attend(const AttendArgs &a, const Plan &p, hipStream_t s) {
+    switch (p.waves) {
+    case 0: return p.rows == 16 ? launch_stream<D, BF16, 1>(a, p, s) : launch_stream<D, BF16, 2>(a, p, s);
+    case 2: return launch_tile<D, BF16, 2>(a, p, s);
+    case 4: return launch_tile<D, BF16, 4>(a, p, s);
+    default: return launch_tile<D, BF16, 8>(a, p, s);
+    }
 }
 
 }  // namespace
@@ -183,8 +230,7 @@ size_t w4a4_attention_kv_workspace_bytes(int64_t rows, int64_t seqs, int64_t q_h
         q_heads > kMaxHeads || q_heads % heads || tokens < 0 || tokens > kMax31)
         return 0;
     if (rows == 0 || seqs == 0) return 0;
-    const Plan p = plan_of(rows, seqs, q_heads, heads, dim, tokens);
-    return p.workers ? up256_bytes(part_bytes(p, dim)) + up256_bytes(ml_bytes(p)) : 0;
+    return workspace_of(plan_of(rows, seqs, q_heads, heads, dim, tokens), heads, dim);
 }
 
 w4a4_status w4a4_attention_kv(const w4a4_head_rows *q, w4a4_dtype dt, int64_t q_heads, const w4a4_head_rows *out,
@@ -201,11 +247,16 @@ w4a4_status w4a4_attention_kv(const w4a4_head_rows *q, w4a4_dtype dt, int64_t q_
     if (q->data && q->data == out->data &&
         (odt != dt || (rows > 1 && q->row_stride != out->row_stride) || (q_heads > 1 && q->head_stride != out->head_stride)))
         return W4A4_ERR_INVALID_VALUE;
-    const Plan p = plan_of(std::max<int64_t>(rows, 1), std::max<int64_t>(batch->seqs, 1), q_heads, cache->heads, dim, batch->pages_per_seq * cache->page);
-    if (p.tiles > kMax31 / cache->heads || !grid_fits(p.tiles * cache->heads * 64 * STREAM_WAVES)) return W4A4_ERR_INVALID_VALUE;
+    const int64_t tokens = batch->pages_per_seq * cache->page, heads = cache->heads;
+    Plan p = plan_of(std::max<int64_t>(rows, 1), std::max<int64_t>(batch->seqs, 1), q_heads, heads, dim, tokens);
+    if (p.tiles > kMax31 / heads || !grid_fits(p.tiles * heads * p.splits * 512)) return W4A4_ERR_INVALID_VALUE;
     if (no_work(batch)) return W4A4_OK;
     if (!q->data || !out->data) return W4A4_ERR_INVALID_VALUE;
-    const size_t need = w4a4_attention_kv_workspace_bytes(rows, batch->seqs, q_heads, cache->heads, dim, batch->pages_per_seq * cache->page);
+    const size_t need = workspace_of(p, heads, dim);
+    if (window) {  // a tile's rows see fewer tokens; the workspace is as the sizes alone have it
+        const Plan less = plan_of(rows, batch->seqs, q_heads, heads, dim, std::min(tokens, window + 2 * KV_BLOCK));
+        if (workspace_of(less, heads, dim) <= need) p = less;
+    }
     if (need && !workspace) return W4A4_ERR_INVALID_VALUE;
     const w4a4_status st = check_batch(cache, batch);
     if (st != W4A4_OK) return st;
@@ -219,13 +270,13 @@ w4a4_status w4a4_attention_kv(const w4a4_head_rows *q, w4a4_dtype dt, int64_t q_
     a.heads = (int32_t)q_heads, a.group = (int32_t)(q_heads / cache->heads), a.causal = causal != 0;
     a.window = (int32_t)std::min<int64_t>(window, kMax31), a.odt = odt;
     a.pool = pool_of(cache), a.batch = batch_of(batch);
-    a.part = static_cast<float *>(workspace), a.workers = (int32_t)p.workers, a.tile_bound = (int32_t)p.tiles;
-    if (need) a.part_ml = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + up256_bytes(part_bytes(p, dim)));
+    a.part = static_cast<float *>(workspace), a.tile_bound = (int32_t)p.tiles;
+    a.workers = (int32_t)p.workers, a.splits = (int32_t)p.splits;
+    if (p.slots(heads)) a.part_ml = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + up256_bytes(part_bytes(p, heads, dim)));
     hipStream_t s = as_stream(stream);
     with_dim(dim, [&](auto d) {
         constexpr int D = decltype(d)::value;
-        if (dt == W4A4_DTYPE_BF16) p.rows == 16 ? launch_attend<D, true, 1>(a, p, s) : launch_attend<D, true, 2>(a, p, s);
-        else p.rows == 16 ? launch_attend<D, false, 1>(a, p, s) : launch_attend<D, false, 2>(a, p, s);
+        dt == W4A4_DTYPE_BF16 ? launch_attend<D, true>(a, p, s) : launch_attend<D, false>(a, p, s);
     });
     return hip_status("attend_kernel");
 }
