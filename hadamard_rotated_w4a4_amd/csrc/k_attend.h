@@ -497,11 +497,11 @@ __device__ __forceinline__ v16f mfma_32x32x16(v4u a, v4u b, v16f c) {
     else return mfma_32x32x16_f16(a, b, c);
 }
 
-// 16 bytes a lane from p to LDS byte address lds + 16 lane (uniform), without
-// passing registers; counted by vmcnt, unseen by the compiler.
-__device__ __forceinline__ void att_load16(const uint8_t *p, uint32_t lds) {
+// 16 bytes a lane from p + at (p uniform) to LDS byte address lds + 16 lane
+// (uniform), without passing registers; counted by vmcnt, unseen by the compiler.
+__device__ __forceinline__ void att_load16(const uint8_t *p, uint32_t at, uint32_t lds) {
     uint32_t m0;  // written; the load that reads it needs one wait state
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : "={m0}"(m0) : "v"(p), "s"(lds) : "memory");
+    asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" : "={m0}"(m0) : "v"(at), "s"(p), "s"(lds) : "memory");
 }
 
 // RW waves of 32 rows each, times TW that take turns at a stage's blocks.
@@ -521,6 +521,22 @@ struct AttTile {
 template <int N>
 __device__ __forceinline__ void att_wait() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
+
+// The order of N pieces' reads, conversions and products: two reads ahead, and
+// each product's conversions while the one before runs.
+template <int N>
+__device__ __forceinline__ void att_interleave() {
+    constexpr int READ = 0x100, VALU = 0x2, MFMA = 0x8, AHEAD = 2;
+    __builtin_amdgcn_sched_group_barrier(READ, AHEAD, 0);
+#pragma unroll
+    for (int c = 0; c < N; c++) {
+        __builtin_amdgcn_sched_group_barrier(VALU, 4, 0);
+        __builtin_amdgcn_sched_group_barrier(MFMA, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(VALU, 4, 0);
+        if (c + AHEAD < N) __builtin_amdgcn_sched_group_barrier(READ, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(MFMA, 1, 0);
+    }
 }
 
 template <class C, bool BF16>
@@ -558,6 +574,9 @@ __global__ __launch_bounds__(C::THREADS) void attend_tile_kernel(AttendArgs a) {
 #pragma unroll
             for (int i = 0; i < 2; i++) q[c][i] = *reinterpret_cast<const v4u_any *>(p + (32 * c + 16 * h + 8 * i) * 2);
     }
+    // here once, or the compiler waits for them in the loop, and for the loads that it does not see
+#pragma unroll
+    for (int c = 0; c < N; c++) asm volatile("" : "+v"(q[c][0]), "+v"(q[c][1]));
     const Span mine = span_of(a, s, r, r + 1);
     const int row_lo = mine.lo, row_hi = live ? mine.hi : 0;
     const Span wspan = wrows ? span_of(a, s, wrow0, wrow0 + wrows) : Span{0, 0};
@@ -581,8 +600,7 @@ __global__ __launch_bounds__(C::THREADS) void attend_tile_kernel(AttendArgs a) {
         for (int i = 0; i < C::LOADS; i++) {
             const int unit = wave + i * C::WAVES, j = unit / (D / 16);
             const int at = wave_pick(held_block, (stage * C::SB + j) & 63);
-            att_load16(a.pool.codes + (int64_t)at * C::BLOCK_BYTES + unit % (D / 16) * 1024 + lane * 16,
-                       __builtin_amdgcn_readfirstlane(to + unit * 1024));
+            att_load16(a.pool.codes + (int64_t)at * C::BLOCK_BYTES + unit % (D / 16) * 1024, lane * 16, to + unit * 1024);
         }
     };
 
@@ -601,7 +619,20 @@ __global__ __launch_bounds__(C::THREADS) void attend_tile_kernel(AttendArgs a) {
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");  // no read of the stage moves up
         if (st + C::RING - 1 < stages) load(st + C::RING - 1);
-        const uint8_t *stage = smem + st % C::RING * (C::SB * C::BLOCK_BYTES);
+        uint8_t *stage = smem + st % C::RING * (C::SB * C::BLOCK_BYTES);
+        // no value but zero where there is no token: once a sequence, in its last stage
+        if ((block0 + (st + 1) * C::SB) * KV_BLOCK > s.len) {
+            for (int u = tid; u < C::SB * 2 * D; u += C::THREADS) {
+                const int j = u / (2 * D), x = u % (2 * D), in = s.len - (block0 + st * C::SB + j) * KV_BLOCK;
+                if (in >= KV_BLOCK) continue;
+                v4u *piece = reinterpret_cast<v4u *>(stage + j * C::BLOCK_BYTES + 32 * D) + x;
+                v4u y = *piece;
+#pragma unroll
+                for (int i = 0; i < 4; i++) y[i] &= kv_token_bytes(i >> 1, i & 1, x / 32 % 2, 0, in);
+                *piece = y;
+            }
+            __syncthreads();
+        }
 #pragma unroll 1
         for (int j = tw; j < C::SB; j += C::TW) {
             const int rel = st * C::SB + j, token0 = (block0 + rel) * KV_BLOCK;
@@ -609,12 +640,15 @@ __global__ __launch_bounds__(C::THREADS) void attend_tile_kernel(AttendArgs a) {
             if (scale < 0 || token0 + KV_BLOCK <= wspan.lo || token0 >= wspan.hi) continue;
             const uint8_t *p = stage + j * C::BLOCK_BYTES + lane * 16;
             v16f t = {};
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int c = 0; c < N; c++) {
                 const v4u x = *reinterpret_cast<const v4u *>(p + c * 1024);
                 t = mfma_32x32x16<BF16>(widen_e4m3<BF16>(x[0], x[1], 1.0f), q[c][0], t);
                 t = mfma_32x32x16<BF16>(widen_e4m3<BF16>(x[2], x[3], 1.0f), q[c][1], t);
             }
+            att_interleave<N>();
+            __builtin_amdgcn_sched_barrier(0);
             const float f = fmaxf(ldexpf(a.scale_log2, (scale & 255) - 127), 1.17549435e-38f);  // never 0: -infinity stays
             if (token0 < every_lo || token0 + KV_BLOCK > every_hi) {
 #pragma unroll
@@ -648,22 +682,15 @@ __global__ __launch_bounds__(C::THREADS) void attend_tile_kernel(AttendArgs a) {
                 l = add_pair(x, l);
             }
             const float unit = power_of_two(e - E);
-            const bool tail = token0 + KV_BLOCK > s.len;  // nothing but zeros where there is no token
-            uint32_t mask[4];
-            if (tail) {
-#pragma unroll
-                for (int x = 0; x < 4; x++) mask[x] = kv_token_bytes(x >> 1, x & 1, h, 0, s.len - token0);
-            }
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int c = 0; c < N; c++) {
-                v4u x = *reinterpret_cast<const v4u *>(p + 32 * D + c * 1024);
-                if (tail) {
-#pragma unroll
-                    for (int y = 0; y < 4; y++) x[y] &= mask[y];
-                }
+                const v4u x = *reinterpret_cast<const v4u *>(p + 32 * D + c * 1024);
                 o[c] = mfma_32x32x16_f16(widen_e4m3<false>(x[0], x[2], unit), w[0], o[c]);
                 o[c] = mfma_32x32x16_f16(widen_e4m3<false>(x[1], x[3], unit), w[1], o[c]);
             }
+            att_interleave<N>();
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
 
