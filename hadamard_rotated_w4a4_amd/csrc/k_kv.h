@@ -152,7 +152,7 @@ struct AppendArgs {
     int32_t rope_rows, half, n_axes, interleaved;
     uint8_t *q_out;
     int64_t o_row, o_head;
-    int32_t dt, odt, q_heads;
+    int32_t dt, odt, q_heads, q_passes;
     int32_t kv_groups;  // workgroups of keys and values, before those of queries
     KvPool pool;
     KvBatch batch;
@@ -160,58 +160,74 @@ struct AppendArgs {
 
 // The cosines and sines that turn channels d .. d + 7 of a head of a row at
 // token `index` of its sequence: pair d + i (halves) or d / 2 + i, i < 4
-// (interleaved).  Positions outside the table give NaN.
-__device__ __forceinline__ void rope_turn(const AppendArgs &a, int row, int index, int d, float c[8], float s[8]) {
-    const int pair = a.interleaved ? d / 2 : d >= a.half ? d - a.half : d, n = a.interleaved ? 4 : 8;
-    const float bad = __uint_as_float(0x7FC00000u);
+// (interleaved).  Positions outside the table give NaN; channels that are not
+// turned nothing.
+struct Turn {
+    v4u c[2], s[2];
+};
+typedef v4u v4u_word __attribute__((aligned(4)));
+__device__ __forceinline__ void rope_turn(const AppendArgs &a, int row, int index, int d, Turn &t) {
+    if (d >= 2 * a.half) return;
+    const int pair = a.interleaved ? d / 2 : d >= a.half ? d - a.half : d;
+    constexpr uint32_t bad = 0x7FC00000u;
     if (!a.axes) {
         const int at = a.positions ? a.positions[row] : index;
-        if ((uint32_t)at < (uint32_t)a.rope_rows) {
-            const float *p = a.rope + (int64_t)at * 2 * a.half + pair;
+        const bool in = (uint32_t)at < (uint32_t)a.rope_rows;
+        const float *p = a.rope + (in ? (int64_t)at * 2 * a.half : 0) + pair;
 #pragma unroll
-            for (int i = 0; i < 8; i++)
-                if (i < n) c[i] = p[i], s[i] = p[a.half + i];
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; i++) c[i] = s[i] = bad;
+        for (int i = 0; i < 2; i++) {
+            if (i && a.interleaved) break;
+            t.c[i] = in ? reinterpret_cast<const v4u_word *>(p)[i] : v4u{bad, bad, bad, bad};
+            t.s[i] = in ? reinterpret_cast<const v4u_word *>(p + a.half)[i] : v4u{bad, bad, bad, bad};
         }
         return;
     }
 #pragma unroll
     for (int i = 0; i < 8; i++) {
-        if (i >= n) break;
+        if (i >= 4 && a.interleaved) break;
         const int axis = a.axes[pair + i];
         const int at = axis < a.n_axes ? a.positions[axis * a.ld_positions + row] : -1;
         const bool in = (uint32_t)at < (uint32_t)a.rope_rows;
         const float *p = a.rope + (in ? (int64_t)at * 2 * a.half : 0) + pair + i;
-        c[i] = in ? p[0] : bad, s[i] = in ? p[a.half] : bad;
+        t.c[i / 4][i % 4] = in ? __float_as_uint(p[0]) : bad, t.s[i / 4][i % 4] = in ? __float_as_uint(p[a.half]) : bad;
     }
 }
 
-// A head's row, held by D / 8 consecutive lanes of a wave (lane: channels d ..
-// d + 7): its RMS norm when there is a weight, as in w4a4_rms_norm_quantize
-// (fp64 sum and root, one rounding), then its leading 2 half channels turned in
-// pairs, one fp32 operation at a time.  Lanes without a row pass live = false.
-template <int D>
-__device__ __forceinline__ void head_row(const AppendArgs &a, const uint8_t *src, const float *weight, int row, int index,
-                                         int d, bool live, float v[8]) {
-    const int size = row_size(a.dt);
-    const bool turned = d < 2 * a.half, paired = turned && !a.interleaved;
-    const int mate = d < a.half ? d + a.half : d - a.half;  // where a pair's other channels lie, halves apart
-    Raw8 mine = {}, other = {};
-    float c[8], s[8], x[8], y[8], w[8], u[8];
-    if (live) {
-        mine = load_raw8(src + (int64_t)d * size, a.dt);
-        if (paired) other = load_raw8(src + (int64_t)mate * size, a.dt);
-        if (turned) rope_turn(a, row, index, d, c, s);
-        if (weight) {
+// A head's row as loaded: D / 8 consecutive lanes of a wave hold it, a lane
+// channels d .. d + 7 and, halves apart, the other channels of its pairs.
+// Loading and computing are apart, so that every load of a thread is in flight
+// before it waits for the first.
+struct HeadRaw {
+    Raw8 mine, mate;
+};
+__device__ __forceinline__ int mate_of(const AppendArgs &a, int d) {
+    return a.interleaved || d >= 2 * a.half ? -1 : d < a.half ? d + a.half : d - a.half;
+}
+__device__ __forceinline__ void load_head(const AppendArgs &a, const uint8_t *src, int d, HeadRaw &x) {
+    const int size = row_size(a.dt), mate = mate_of(a, d);
+    x.mine = load_raw8(src + (int64_t)d * size, a.dt);
+    if (mate >= 0) x.mate = load_raw8(src + (int64_t)mate * size, a.dt);
+}
+struct HeadWeight {
+    float mine[8], mate[8];
+};
+__device__ __forceinline__ void load_weight(const AppendArgs &a, const float *weight, int d, HeadWeight &w) {
+    if (!weight) return;
+    const int mate = mate_of(a, d);
 #pragma unroll
-            for (int i = 0; i < 8; i++) w[i] = weight[d + i], u[i] = paired ? weight[mate + i] : 0.0f;
-        }
-    }
-    to_f32(mine, a.dt, x);
-    to_f32(other, a.dt, y);
-    if (weight) {
+    for (int i = 0; i < 8; i++) w.mine[i] = weight[d + i], w.mate[i] = mate >= 0 ? weight[mate + i] : 0.0f;
+}
+
+// The row's RMS norm when there is a weight, as in w4a4_rms_norm_quantize (fp64
+// sum and root, one rounding), then its leading 2 half channels turned in pairs,
+// one fp32 operation at a time.  Every lane of the wave takes part.
+template <int D>
+__device__ __forceinline__ void head_row(const AppendArgs &a, const HeadRaw &raw, bool weighted, const HeadWeight &w, const Turn &t,
+                                         int d, float v[8]) {
+    float x[8], y[8];
+    to_f32(raw.mine, a.dt, x);
+    to_f32(raw.mate, a.dt, y);
+    if (weighted) {
         double sum = 0.0;
 #pragma unroll
         for (int i = 0; i < 8; i++) sum = fma((double)x[i], (double)x[i], sum);
@@ -219,24 +235,26 @@ __device__ __forceinline__ void head_row(const AppendArgs &a, const uint8_t *src
         for (int m = 1; m < D / 8; m *= 2) sum += __shfl_xor(sum, m);
         const float root = (float)(1.0 / sqrt(sum / D + a.eps));
 #pragma unroll
-        for (int i = 0; i < 8; i++) x[i] = x[i] * root * w[i], y[i] = y[i] * root * u[i];
+        for (int i = 0; i < 8; i++) x[i] = x[i] * root * w.mine[i], y[i] = y[i] * root * w.mate[i];
     }
-    if (!turned) {
+    auto c = [&](int i) { return __uint_as_float(t.c[i / 4][i % 4]); };
+    auto s = [&](int i) { return __uint_as_float(t.s[i / 4][i % 4]); };
+    if (d >= 2 * a.half) {
 #pragma unroll
         for (int i = 0; i < 8; i++) v[i] = x[i];
     } else if (a.interleaved) {
 #pragma unroll
         for (int i = 0; i < 4; i++) {
             const float p = x[2 * i], r = x[2 * i + 1];
-            v[2 * i] = p * c[i] - r * s[i];
-            v[2 * i + 1] = r * c[i] + p * s[i];
+            v[2 * i] = p * c(i) - r * s(i);
+            v[2 * i + 1] = r * c(i) + p * s(i);
         }
     } else if (d < a.half) {
 #pragma unroll
-        for (int i = 0; i < 8; i++) v[i] = x[i] * c[i] - y[i] * s[i];
+        for (int i = 0; i < 8; i++) v[i] = x[i] * c(i) - y[i] * s(i);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; i++) v[i] = x[i] * c[i] + y[i] * s[i];
+        for (int i = 0; i < 8; i++) v[i] = x[i] * c(i) + y[i] * s(i);
     }
 }
 
@@ -270,14 +288,29 @@ __device__ __forceinline__ void append_block(const AppendArgs &a, int id, uint8_
     if (b < 0) return;
     const KvSeq s = kv_seq(a.batch, page_tokens, b);
     const int blk = kv_first_block(s) + slot, t0 = blk * KV_BLOCK;
+    const int kept = max(s.first() - t0, 0), lo = kept, hi = min(s.len - t0, KV_BLOCK);  // new tokens lo .. hi - 1
+
+    const int d = tid % LANES * 8, r0 = tid / LANES, size = row_size(a.dt);
+    HeadRaw raw[PASSES] = {};
+    Raw8 vraw[PASSES] = {};
+    Turn turn[PASSES] = {};
+    HeadWeight weight = {};
+#pragma unroll
+    for (int p = 0; p < PASSES; p++) {
+        const int t = r0 + p * ROWS, index = t0 + t;
+        if (t < lo || t >= hi) continue;
+        const int64_t row = s.row + (index - s.first());
+        load_head(a, a.k + (row * a.k_row + head * a.k_head) * size, d, raw[p]);
+        vraw[p] = load_raw8(a.v + (row * a.v_row + head * a.v_head + d) * size, a.dt);
+        rope_turn(a, (int)row, index, d, turn[p]);
+    }
+    load_weight(a, a.k_weight, d, weight);
     const int at = kv_block(a.pool, a.batch, b, head, blk);
     if (at < 0) return;
-    const int kept = max(s.first() - t0, 0), lo = kept, hi = min(s.len - t0, KV_BLOCK);  // new tokens lo .. hi - 1
     uint8_t *codes = a.pool.codes + (int64_t)at * (64 * D);
     uint16_t *scale = reinterpret_cast<uint16_t *>(a.pool.scales) + at;
     int was = kept ? *scale : 0;
 
-    const int d = tid % LANES * 8, r0 = tid / LANES;
     float k[PASSES][8], v[PASSES][8];
     bool lost[PASSES];
     uint32_t ktop = 0, vtop = 0;
@@ -287,14 +320,8 @@ __device__ __forceinline__ void append_block(const AppendArgs &a, int id, uint8_
         const bool live = t >= lo && t < hi;
         lost[p] = false;
         if (p * ROWS >= hi || (p + 1) * ROWS <= lo) continue;  // uniform
-        const int index = t0 + t;
-        const int64_t row = s.row + (index - s.first());
-        const int size = row_size(a.dt);
-        const uint8_t *ks = a.k + (row * a.k_row + head * a.k_head) * size;
-        Raw8 raw = {};
-        if (live) raw = load_raw8(a.v + (row * a.v_row + head * a.v_head + d) * size, a.dt);
-        head_row<D>(a, ks, a.k_weight, (int)row, index, d, live, k[p]);
-        to_f32(raw, a.dt, v[p]);
+        head_row<D>(a, raw[p], a.k_weight != nullptr, weight, turn[p], d, k[p]);
+        to_f32(vraw[p], a.dt, v[p]);
         uint32_t kt = 0, vt = 0;
 #pragma unroll
         for (int i = 0; i < 8; i++) {
@@ -380,26 +407,48 @@ __device__ __forceinline__ void append_block(const AppendArgs &a, int id, uint8_
     }
 }
 
-// The queries of a row: D / 8 lanes a head, a wave's heads from one row.
+// The queries of a row: D / 8 lanes a head, a wave's heads from one row, so that
+// cosines, sines and weights are loaded once for a.q_passes steps of 64 / LANES
+// heads.
 template <int D>
 __device__ __forceinline__ void append_queries(const AppendArgs &a, int id) {
-    constexpr int LANES = D / 8, HEADS = 64 / LANES;
-    const int lane = threadIdx.x & 63, groups = (a.q_heads + HEADS - 1) / HEADS;
+    constexpr int LANES = D / 8, HEADS = 64 / LANES, AHEAD = 4;
+    const int lane = threadIdx.x & 63, per = HEADS * a.q_passes, groups = (a.q_heads + per - 1) / per;
     const int64_t task = (int64_t)id * (KV_THREADS / 64) + threadIdx.x / 64;
-    const int row = __builtin_amdgcn_readfirstlane((int)(task / groups)), head = (int)(task % groups) * HEADS + lane / LANES;
+    const int row = __builtin_amdgcn_readfirstlane((int)(task / groups)), head0 = (int)(task % groups) * per + lane / LANES;
     if (row >= a.batch.tokens) return;
-    int index = 0;
+    const int d = lane % LANES * 8, size = row_size(a.dt), end = min(a.q_heads, head0 - lane / LANES + per);
+    const uint8_t *src = a.q + (int64_t)row * a.q_row * size;
+    HeadRaw raw[AHEAD] = {};
+    auto load = [&](int h, HeadRaw &x) {
+        if (h < end) load_head(a, src + h * a.q_head * size, d, x);
+    };
+#pragma unroll
+    for (int i = 0; i < AHEAD; i++) load(head0 + i * HEADS, raw[i]);
+    HeadWeight weight = {};
+    load_weight(a, a.q_weight, d, weight);
     const int b = seq_of_row(a.batch, row, lane);
     if (b < 0) return;
-    if (a.rope && !a.positions) {
-        const KvSeq s = kv_seq(a.batch, a.pool.per_page * KV_BLOCK, b);
-        index = s.first() + (row - s.row);
+    Turn turn = {};
+    if (a.half) {
+        int index = 0;
+        if (!a.positions) {
+            const KvSeq s = kv_seq(a.batch, a.pool.per_page * KV_BLOCK, b);
+            index = s.first() + (row - s.row);
+        }
+        rope_turn(a, row, index, d, turn);
     }
-    const bool live = head < a.q_heads;
-    const int d = lane % LANES * 8;
-    float x[8];
-    head_row<D>(a, a.q + ((int64_t)row * a.q_row + head * a.q_head) * row_size(a.dt), a.q_weight, row, index, d, live, x);
-    if (live) store_row8(a.q_out + ((int64_t)row * a.o_row + head * a.o_head + d) * 2, a.odt, x);
+    uint8_t *dst = a.q_out + ((int64_t)row * a.o_row + d) * 2;
+    for (int h = head0; h - lane / LANES < end; h += AHEAD * HEADS) {
+#pragma unroll
+        for (int i = 0; i < AHEAD; i++) {
+            const int at = h + i * HEADS;
+            float x[8];
+            head_row<D>(a, raw[i], a.q_weight != nullptr, weight, turn, d, x);
+            if (at < end) store_row8(dst + (int64_t)at * a.o_head * 2, a.odt, x);
+            load(at + AHEAD * HEADS, raw[i]);
+        }
+    }
 }
 
 template <int D>

@@ -200,7 +200,11 @@ w4a4_status w4a4_append_kv(w4a4_dtype dt, const w4a4_head_rows *k, const w4a4_he
         a.interleaved = rope->interleaved != 0;
     }
     a.pool = pool_of(cache), a.batch = batch_of(batch), a.kv_groups = (int32_t)blocks;
-    const int64_t heads_a_wave = 64 / (dim / 8), tasks = queries ? rows * ((q_heads + heads_a_wave - 1) / heads_a_wave) : 0;
+    // heads of a wave: steps of 512 / dim, as many as leave every CU 8 waves
+    const int64_t step = 512 / dim, steps = queries ? (q_heads + step - 1) / step : 0;
+    const int64_t passes = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(steps, 8), rows * steps / 2048));
+    const int64_t tasks = rows * ((steps + passes - 1) / passes);
+    a.q_passes = (int32_t)passes;
     const unsigned grid = (unsigned)(blocks + (tasks + 3) / 4);
     with_dim(dim, [&](auto d) { append_kernel<decltype(d)::value><<<grid, KV_THREADS, 0, as_stream(stream)>>>(a); });
     return hip_status("append_kernel");
