@@ -153,7 +153,7 @@ template <int R>
 __device__ __forceinline__ int64_t all_steps(const AttendArgs &a, int page_tokens, int lane) {
     int64_t mine = 0;
     for (int b = lane; b < a.batch.seqs; b += 64) mine += steps_of<R>(a, kv_seq(a.batch, page_tokens, b));
-    return wave_pick(wave_scan(mine, lane), 63) * a.pool.heads;
+    return wave_pick(wave_scan(mine), 63) * a.pool.heads;
 }
 // Workers in use, and where worker w begins among all steps.
 __device__ __forceinline__ int64_t workers_used(int64_t steps, int workers) {
@@ -448,9 +448,9 @@ __global__ __launch_bounds__(64 * STREAM_WAVES) void attend_join_kernel(AttendAr
         if (i < b) before += n;
         if (i == b) own += n;
     }
-    all = wave_pick(wave_scan(all, lane), 63) * heads;
-    before = wave_pick(wave_scan(before, lane), 63) * heads;
-    own = wave_pick(wave_scan(own, lane), 63);
+    all = wave_pick(wave_scan(all), 63) * heads;
+    before = wave_pick(wave_scan(before), 63) * heads;
+    own = wave_pick(wave_scan(own), 63);
     int64_t begin = before + head * own;
     for (int t = 0; t < tile; t++) begin += steps_of<R>(a, s, t);
     const int64_t end = begin + steps_of<R>(a, s, tile), used = workers_used(all, a.workers);

@@ -30,7 +30,9 @@
 namespace w4a4 {
 
 constexpr int KV_BLOCK = 32;     // tokens of a block
-constexpr int KV_THREADS = 256;  // of a workgroup of the kernels here
+// Threads of a workgroup of the kernels here: 32 tokens of a head's rows, 8 channels
+// a thread, in one or two steps.
+__host__ __device__ constexpr int kv_threads(int dim) { return dim == 256 ? 512 : 256; }
 
 typedef float v2f __attribute__((ext_vector_type(2)));
 typedef uint32_t v2u __attribute__((ext_vector_type(2)));
@@ -63,15 +65,66 @@ __device__ __forceinline__ int kv_block(const KvPool &p, const KvBatch &s, int b
     return (uint32_t)page < (uint32_t)p.pages ? (page * p.heads + head) * p.per_page + (blk - slot * p.per_page) : -1;
 }
 
+// x of another lane by a DPP pattern (no LDS round trip, as __shfl has); 0 where
+// the pattern has no lane, or ROWS leaves a row of 16 out.
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ int32_t dpp_of(int32_t x) {
+    return __builtin_amdgcn_update_dpp(0, x, CTRL, ROWS, 0xF, true);
+}
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ int64_t dpp_of(int64_t x) {
+    return (int64_t)((uint64_t)(uint32_t)dpp_of<CTRL, ROWS>((int32_t)(x >> 32)) << 32 | (uint32_t)dpp_of<CTRL, ROWS>((int32_t)x));
+}
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ double dpp_of(double x) {
+    return __builtin_bit_cast(double, dpp_of<CTRL, ROWS>(__builtin_bit_cast(int64_t, x)));
+}
+constexpr int DPP_SHR1 = 0x111, DPP_SHR2 = 0x112, DPP_SHR4 = 0x114, DPP_SHR8 = 0x118, DPP_BCAST15 = 0x142, DPP_BCAST31 = 0x143,
+              DPP_XOR1 = 0xB1, DPP_XOR2 = 0x4E, DPP_MIRROR8 = 0x141, DPP_MIRROR16 = 0x140;
 // Inclusive sum over the wave's lanes.
 template <class T>
-__device__ __forceinline__ T wave_scan(T x, int lane) {
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        const T y = __shfl_up(x, d);
-        if (lane >= d) x += y;
+__device__ __forceinline__ T wave_scan(T x) {
+    x += dpp_of<DPP_SHR1>(x);
+    x += dpp_of<DPP_SHR2>(x);
+    x += dpp_of<DPP_SHR4>(x);
+    x += dpp_of<DPP_SHR8>(x);
+    x += dpp_of<DPP_BCAST15, 0xA>(x);
+    return x + dpp_of<DPP_BCAST31, 0xC>(x);
+}
+// x over the lanes l and l ^ 16, or l ^ 32: f of both.
+template <class F>
+__device__ __forceinline__ uint32_t swap16(uint32_t x, F f) {
+    const auto y = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    return f(y[0], y[1]);
+}
+template <class F>
+__device__ __forceinline__ uint32_t swap32(uint32_t x, F f) {
+    const auto y = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    return f(y[0], y[1]);
+}
+// The sum over a row's LANES lanes (8, 16 or 32), the same in each.
+template <int LANES>
+__device__ __forceinline__ double lanes_sum(double x) {
+    x += dpp_of<DPP_XOR1>(x);
+    x += dpp_of<DPP_XOR2>(x);
+    x += dpp_of<DPP_MIRROR8>(x);  // a quad's lanes hold the same: as good as l ^ 4
+    if constexpr (LANES > 8) x += dpp_of<DPP_MIRROR16>(x);
+    if constexpr (LANES > 16) {
+        const uint64_t u = __builtin_bit_cast(uint64_t, x);
+        const auto lo = __builtin_amdgcn_permlane16_swap((uint32_t)u, (uint32_t)u, false, false);
+        const auto hi = __builtin_amdgcn_permlane16_swap((uint32_t)(u >> 32), (uint32_t)(u >> 32), false, false);
+        x = __builtin_bit_cast(double, (uint64_t)hi[0] << 32 | lo[0]) + __builtin_bit_cast(double, (uint64_t)hi[1] << 32 | lo[1]);
     }
     return x;
+}
+// The largest of the wave's lanes, in each.
+__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
+    auto larger = [](uint32_t a, uint32_t b) { return max(a, b); };
+    x = max(x, (uint32_t)dpp_of<DPP_XOR1>((int32_t)x));
+    x = max(x, (uint32_t)dpp_of<DPP_XOR2>((int32_t)x));
+    x = max(x, (uint32_t)dpp_of<DPP_MIRROR8>((int32_t)x));
+    x = max(x, (uint32_t)dpp_of<DPP_MIRROR16>((int32_t)x));
+    return swap32(swap16(x, larger), larger);
 }
 __device__ __forceinline__ int32_t wave_pick(int32_t x, int lane) { return __builtin_amdgcn_readlane(x, lane); }
 __device__ __forceinline__ int64_t wave_pick(int64_t x, int lane) {
@@ -86,7 +139,7 @@ template <class T, class F>
 __device__ __forceinline__ int kv_find(int seqs, T &id, int lane, F weight) {
     for (int base = 0; base < seqs; base += 64) {
         const T w = base + lane < seqs ? weight(base + lane) : 0;
-        const T sum = wave_scan(w, lane), total = wave_pick(sum, 63);
+        const T sum = wave_scan(w), total = wave_pick(sum, 63);
         if (id < total) {
             const int at = __builtin_ctzll(__ballot(sum > id));
             id -= wave_pick(sum, at) - wave_pick(w, at);
@@ -193,69 +246,51 @@ __device__ __forceinline__ void rope_turn(const AppendArgs &a, int row, int inde
     }
 }
 
-// A head's row as loaded: D / 8 consecutive lanes of a wave hold it, a lane
-// channels d .. d + 7 and, halves apart, the other channels of its pairs.
-// Loading and computing are apart, so that every load of a thread is in flight
-// before it waits for the first.
-struct HeadRaw {
-    Raw8 mine, mate;
-};
-__device__ __forceinline__ int mate_of(const AppendArgs &a, int d) {
-    return a.interleaved || d >= 2 * a.half ? -1 : d < a.half ? d + a.half : d - a.half;
-}
-__device__ __forceinline__ void load_head(const AppendArgs &a, const uint8_t *src, int d, HeadRaw &x) {
-    const int size = row_size(a.dt), mate = mate_of(a, d);
-    x.mine = load_raw8(src + (int64_t)d * size, a.dt);
-    if (mate >= 0) x.mate = load_raw8(src + (int64_t)mate * size, a.dt);
-}
-struct HeadWeight {
-    float mine[8], mate[8];
-};
-__device__ __forceinline__ void load_weight(const AppendArgs &a, const float *weight, int d, HeadWeight &w) {
-    if (!weight) return;
-    const int mate = mate_of(a, d);
-#pragma unroll
-    for (int i = 0; i < 8; i++) w.mine[i] = weight[d + i], w.mate[i] = mate >= 0 ? weight[mate + i] : 0.0f;
-}
-
-// The row's RMS norm when there is a weight, as in w4a4_rms_norm_quantize (fp64
+// A head's row is held by D / 8 consecutive lanes of a wave, a lane channels d ..
+// d + 7.  Its RMS norm when there is a weight, as in w4a4_rms_norm_quantize (fp64
 // sum and root, one rounding), then its leading 2 half channels turned in pairs,
-// one fp32 operation at a time.  Every lane of the wave takes part.
+// one fp32 operation at a time; the other channels of a lane's pairs, halves
+// apart, come from the lane that holds them.  Every lane of the wave takes part.
 template <int D>
-__device__ __forceinline__ void head_row(const AppendArgs &a, const HeadRaw &raw, bool weighted, const HeadWeight &w, const Turn &t,
+__device__ __forceinline__ void head_row(const AppendArgs &a, const Raw8 &raw, const float *weight, const float w[8], const Turn &t,
                                          int d, float v[8]) {
-    float x[8], y[8];
-    to_f32(raw.mine, a.dt, x);
-    to_f32(raw.mate, a.dt, y);
-    if (weighted) {
+    to_f32(raw, a.dt, v);
+    if (weight) {
         double sum = 0.0;
 #pragma unroll
-        for (int i = 0; i < 8; i++) sum = fma((double)x[i], (double)x[i], sum);
+        for (int i = 0; i < 8; i++) sum = fma((double)v[i], (double)v[i], sum);
+        const float root = (float)rsqrt64(fma(lanes_sum<D / 8>(sum), 1.0 / D, a.eps));
 #pragma unroll
-        for (int m = 1; m < D / 8; m *= 2) sum += __shfl_xor(sum, m);
-        const float root = (float)(1.0 / sqrt(sum / D + a.eps));
-#pragma unroll
-        for (int i = 0; i < 8; i++) x[i] = x[i] * root * w.mine[i], y[i] = y[i] * root * w.mate[i];
+        for (int i = 0; i < 8; i++) v[i] = v[i] * root * w[i];
     }
+    if (!a.half) return;
     auto c = [&](int i) { return __uint_as_float(t.c[i / 4][i % 4]); };
     auto s = [&](int i) { return __uint_as_float(t.s[i / 4][i % 4]); };
-    if (d >= 2 * a.half) {
-#pragma unroll
-        for (int i = 0; i < 8; i++) v[i] = x[i];
-    } else if (a.interleaved) {
+    if (a.interleaved) {
+        if (d >= 2 * a.half) return;
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-            const float p = x[2 * i], r = x[2 * i + 1];
+            const float p = v[2 * i], r = v[2 * i + 1];
             v[2 * i] = p * c(i) - r * s(i);
             v[2 * i + 1] = r * c(i) + p * s(i);
         }
-    } else if (d < a.half) {
-#pragma unroll
-        for (int i = 0; i < 8; i++) v[i] = x[i] * c(i) - y[i] * s(i);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; i++) v[i] = x[i] * c(i) + y[i] * s(i);
+        return;
     }
+    const int mate = ((threadIdx.x & 63) + (d < a.half ? a.half / 8 : -a.half / 8)) & 63;
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) y[i] = __shfl(v[i], mate);
+    if (d >= 2 * a.half) return;
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        const float ys = y[i] * s(i);
+        v[i] = v[i] * c(i) + (d < a.half ? -ys : ys);
+    }
+}
+__device__ __forceinline__ void load_weight(const float *weight, int d, float w[8]) {
+    if (!weight) return;
+#pragma unroll
+    for (int i = 0; i < 8; i++) w[i] = weight[d + i];
 }
 
 // Sequence of a row (uniform): the last that begins at or before it; -1 for rows
@@ -280,7 +315,7 @@ __device__ __forceinline__ int kv_piece_byte(int t) { return (t >> 3 & 1) * 8 + 
 // One block of one head for a workgroup: the rows of new tokens that fall in it.
 template <int D>
 __device__ __forceinline__ void append_block(const AppendArgs &a, int id, uint8_t *smem) {
-    constexpr int LANES = D / 8, ROWS = KV_THREADS / LANES, PASSES = KV_BLOCK / ROWS;
+    constexpr int THREADS = kv_threads(D), LANES = D / 8, ROWS = THREADS / LANES, PASSES = KV_BLOCK / ROWS;
     const int tid = threadIdx.x, lane = tid & 63, page_tokens = a.pool.per_page * KV_BLOCK;
     const int head = id % a.pool.heads;
     int32_t slot = id / a.pool.heads;
@@ -291,20 +326,19 @@ __device__ __forceinline__ void append_block(const AppendArgs &a, int id, uint8_
     const int kept = max(s.first() - t0, 0), lo = kept, hi = min(s.len - t0, KV_BLOCK);  // new tokens lo .. hi - 1
 
     const int d = tid % LANES * 8, r0 = tid / LANES, size = row_size(a.dt);
-    HeadRaw raw[PASSES] = {};
-    Raw8 vraw[PASSES] = {};
+    Raw8 raw[PASSES] = {}, vraw[PASSES] = {};
     Turn turn[PASSES] = {};
-    HeadWeight weight = {};
+    float weight[8] = {};
 #pragma unroll
     for (int p = 0; p < PASSES; p++) {
         const int t = r0 + p * ROWS, index = t0 + t;
         if (t < lo || t >= hi) continue;
         const int64_t row = s.row + (index - s.first());
-        load_head(a, a.k + (row * a.k_row + head * a.k_head) * size, d, raw[p]);
+        raw[p] = load_raw8(a.k + (row * a.k_row + head * a.k_head + d) * size, a.dt);
         vraw[p] = load_raw8(a.v + (row * a.v_row + head * a.v_head + d) * size, a.dt);
         rope_turn(a, (int)row, index, d, turn[p]);
     }
-    load_weight(a, a.k_weight, d, weight);
+    load_weight(a.k_weight, d, weight);
     const int at = kv_block(a.pool, a.batch, b, head, blk);
     if (at < 0) return;
     uint8_t *codes = a.pool.codes + (int64_t)at * (64 * D);
@@ -320,7 +354,7 @@ __device__ __forceinline__ void append_block(const AppendArgs &a, int id, uint8_
         const bool live = t >= lo && t < hi;
         lost[p] = false;
         if (p * ROWS >= hi || (p + 1) * ROWS <= lo) continue;  // uniform
-        head_row<D>(a, raw[p], a.k_weight != nullptr, weight, turn[p], d, k[p]);
+        head_row<D>(a, raw[p], a.k_weight, weight, turn[p], d, k[p]);
         to_f32(vraw[p], a.dt, v[p]);
         uint32_t kt = 0, vt = 0;
 #pragma unroll
@@ -333,17 +367,13 @@ __device__ __forceinline__ void append_block(const AppendArgs &a, int id, uint8_
         lost[p] = (bad >> (lane / LANES * LANES) & ((1ull << LANES) - 1)) != 0;
         if (live && !lost[p]) ktop = max(ktop, kt), vtop = max(vtop, vt);
     }
-#pragma unroll
-    for (int m = 1; m < 64; m *= 2) {
-        ktop = max(ktop, (uint32_t)__shfl_xor((int)ktop, m));
-        vtop = max(vtop, (uint32_t)__shfl_xor((int)vtop, m));
-    }
-    uint32_t *tops = reinterpret_cast<uint32_t *>(smem + 32 * D);
-    if (lane == 0) tops[tid / 64] = ktop, tops[4 + tid / 64] = vtop;
+    ktop = wave_max(ktop), vtop = wave_max(vtop);
+    uint32_t *tops = reinterpret_cast<uint32_t *>(smem + 32 * D);  // [waves][2]
+    if (lane == 0) tops[tid / 64 * 2] = ktop, tops[tid / 64 * 2 + 1] = vtop;
     asm volatile("" : "+v"(was));  // every wave has read the old scales before one writes the new
     __syncthreads();
-    ktop = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
-    vtop = max(max(tops[4], tops[5]), max(tops[6], tops[7]));
+#pragma unroll
+    for (int w = 0; w < THREADS / 64; w++) ktop = max(ktop, tops[2 * w]), vtop = max(vtop, tops[2 * w + 1]);
     const int kwas = (was & 255) - 127, vwas = (was >> 8) - 127;
     const int ke = kept ? max(kv_exponent(ktop), kwas) : kv_exponent(ktop);
     const int ve = kept ? max(kv_exponent(vtop), vwas) : kv_exponent(vtop);
@@ -377,7 +407,7 @@ __device__ __forceinline__ void append_block(const AppendArgs &a, int id, uint8_
         }
     }
     if (kept && ke > kwas) {  // the tokens before, on the coarser grid
-        for (int u = tid; u < 2 * D; u += KV_THREADS) {
+        for (int u = tid; u < 2 * D; u += THREADS) {
             if (u % 32 >= kept) continue;
             v4u *p = reinterpret_cast<v4u *>(codes) + u;
             v4u x = *p;
@@ -389,7 +419,7 @@ __device__ __forceinline__ void append_block(const AppendArgs &a, int id, uint8_
     if (bytes) return;  // uniform
     __syncthreads();
     const bool grown = kept && ve > vwas, whole = hi - lo == KV_BLOCK;
-    for (int u = tid; u < 2 * D; u += KV_THREADS) {
+    for (int u = tid; u < 2 * D; u += THREADS) {
         const int h = u / 32 % 2, c = u / 64 * 32 + u % 32;
         v4u *p = reinterpret_cast<v4u *>(values) + u;
         v4u x = *reinterpret_cast<const v4u *>(smem + kv_lds_piece<D>(c, h));
@@ -414,19 +444,19 @@ template <int D>
 __device__ __forceinline__ void append_queries(const AppendArgs &a, int id) {
     constexpr int LANES = D / 8, HEADS = 64 / LANES, AHEAD = 4;
     const int lane = threadIdx.x & 63, per = HEADS * a.q_passes, groups = (a.q_heads + per - 1) / per;
-    const int64_t task = (int64_t)id * (KV_THREADS / 64) + threadIdx.x / 64;
+    const int64_t task = (int64_t)id * (kv_threads(D) / 64) + threadIdx.x / 64;
     const int row = __builtin_amdgcn_readfirstlane((int)(task / groups)), head0 = (int)(task % groups) * per + lane / LANES;
     if (row >= a.batch.tokens) return;
     const int d = lane % LANES * 8, size = row_size(a.dt), end = min(a.q_heads, head0 - lane / LANES + per);
-    const uint8_t *src = a.q + (int64_t)row * a.q_row * size;
-    HeadRaw raw[AHEAD] = {};
-    auto load = [&](int h, HeadRaw &x) {
-        if (h < end) load_head(a, src + h * a.q_head * size, d, x);
+    const uint8_t *src = a.q + ((int64_t)row * a.q_row + d) * size;
+    Raw8 raw[AHEAD] = {};
+    auto load = [&](int h, Raw8 &x) {
+        if (h < end) x = load_raw8(src + h * a.q_head * size, a.dt);
     };
 #pragma unroll
     for (int i = 0; i < AHEAD; i++) load(head0 + i * HEADS, raw[i]);
-    HeadWeight weight = {};
-    load_weight(a, a.q_weight, d, weight);
+    float weight[8] = {};
+    load_weight(a.q_weight, d, weight);
     const int b = seq_of_row(a.batch, row, lane);
     if (b < 0) return;
     Turn turn = {};
@@ -444,7 +474,7 @@ __device__ __forceinline__ void append_queries(const AppendArgs &a, int id) {
         for (int i = 0; i < AHEAD; i++) {
             const int at = h + i * HEADS;
             float x[8];
-            head_row<D>(a, raw[i], a.q_weight != nullptr, weight, turn, d, x);
+            head_row<D>(a, raw[i], a.q_weight, weight, turn, d, x);
             if (at < end) store_row8(dst + (int64_t)at * a.o_head * 2, a.odt, x);
             load(at + AHEAD * HEADS, raw[i]);
         }
@@ -452,8 +482,8 @@ __device__ __forceinline__ void append_queries(const AppendArgs &a, int id) {
 }
 
 template <int D>
-__global__ __launch_bounds__(KV_THREADS) void append_kernel(AppendArgs a) {
-    __shared__ __align__(16) uint8_t smem[32 * D + 32];
+__global__ __launch_bounds__(kv_threads(D)) void append_kernel(AppendArgs a) {
+    __shared__ __align__(16) uint8_t smem[32 * D + kv_threads(D) / 8];
     if ((int)blockIdx.x < a.kv_groups) append_block<D>(a, (int)blockIdx.x, smem);
     else append_queries<D>(a, (int)blockIdx.x - a.kv_groups);
 }
@@ -469,8 +499,8 @@ struct KvReadArgs {
 // A batch's last rows' keys and values: one block of one head a workgroup.
 // Tokens without a page, or before a sequence's first, read as zeros.
 template <int D>
-__global__ __launch_bounds__(KV_THREADS) void read_kv_kernel(KvReadArgs a) {
-    constexpr int LANES = D / 8, ROWS = KV_THREADS / LANES, PASSES = KV_BLOCK / ROWS;
+__global__ __launch_bounds__(kv_threads(D)) void read_kv_kernel(KvReadArgs a) {
+    constexpr int THREADS = kv_threads(D), LANES = D / 8, ROWS = THREADS / LANES, PASSES = KV_BLOCK / ROWS;
     __shared__ __align__(16) uint8_t smem[32 * D];
     const int tid = threadIdx.x, lane = tid & 63, page_tokens = a.pool.per_page * KV_BLOCK;
     const int head = (int)(blockIdx.x % a.pool.heads);
@@ -490,7 +520,7 @@ __global__ __launch_bounds__(KV_THREADS) void read_kv_kernel(KvReadArgs a) {
     if (at >= 0) {
         const int e = reinterpret_cast<const uint16_t *>(a.pool.scales)[at];
         ke = (e & 255) - 127, ve = (e >> 8) - 127;
-        for (int u = tid; u < 2 * D; u += KV_THREADS)
+        for (int u = tid; u < 2 * D; u += THREADS)
             *reinterpret_cast<v4u *>(smem + kv_lds_piece<D>(u / 64 * 32 + u % 32, u / 32 % 2)) =
                 reinterpret_cast<const v4u *>(codes + 32 * D)[u];
     }

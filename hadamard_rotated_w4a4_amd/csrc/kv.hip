@@ -61,8 +61,12 @@ KvPool pool_of(const w4a4_kv_cache *c) {
 KvBatch batch_of(const w4a4_kv_batch *s) {
     return KvBatch{s->pages, s->starts, s->lens, s->ld, (int32_t)s->pages_per_seq, (int32_t)s->seqs, (int32_t)s->rows};
 }
-// At least the blocks that a batch's rows reach: n rows touch at most n / 32 + 2.
-int64_t block_bound(const w4a4_kv_batch *s) { return s->rows / KV_BLOCK + 2 * std::min(s->seqs, s->rows); }
+// At least the blocks that a batch's rows reach: one row reaches one, a second may
+// reach another, and each 32 more one more.
+int64_t block_bound(const w4a4_kv_batch *s) {
+    const int64_t some = std::min(s->seqs, s->rows), more = s->rows - some;
+    return some + std::min(more, some) + std::max<int64_t>(more - some, 0) / KV_BLOCK;
+}
 
 template <class F>
 void with_dim(int64_t dim, F f) {
@@ -176,8 +180,8 @@ w4a4_status w4a4_append_kv(w4a4_dtype dt, const w4a4_head_rows *k, const w4a4_he
             (rope->positions && rope->axes && rope->n_axes > 1 && rope->ld < rows) || rope->ld < 0)
             return W4A4_ERR_INVALID_VALUE;
     }
-    const int64_t blocks = block_bound(batch) * cache->heads, waves = rows * ((q_heads * dim / 8 + 63) / 64);
-    if (blocks > kMax31 || !grid_fits((blocks + waves / 4 + 1) * KV_THREADS)) return W4A4_ERR_INVALID_VALUE;
+    const int64_t blocks = block_bound(batch) * cache->heads, threads = kv_threads((int)dim);
+    if (blocks > kMax31 || !grid_fits(blocks * threads + rows * ((q_heads * dim / 8 + 63) / 64 * 64) + threads)) return W4A4_ERR_INVALID_VALUE;
     if (no_work(batch)) return W4A4_OK;
     if (!k->data || !v->data || (rope && !rope->table && rope->table_rows)) return W4A4_ERR_INVALID_VALUE;
     const w4a4_status st = check_batch(cache, batch);
@@ -205,8 +209,8 @@ w4a4_status w4a4_append_kv(w4a4_dtype dt, const w4a4_head_rows *k, const w4a4_he
     const int64_t passes = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(steps, 8), rows * steps / 2048));
     const int64_t tasks = rows * ((steps + passes - 1) / passes);
     a.q_passes = (int32_t)passes;
-    const unsigned grid = (unsigned)(blocks + (tasks + 3) / 4);
-    with_dim(dim, [&](auto d) { append_kernel<decltype(d)::value><<<grid, KV_THREADS, 0, as_stream(stream)>>>(a); });
+    const unsigned grid = (unsigned)(blocks + (tasks * 64 + threads - 1) / threads);
+    with_dim(dim, [&](auto d) { append_kernel<decltype(d)::value><<<grid, (unsigned)threads, 0, as_stream(stream)>>>(a); });
     return hip_status("append_kernel");
 }
 
@@ -216,7 +220,8 @@ w4a4_status w4a4_read_kv(const w4a4_kv_cache *cache, const w4a4_kv_batch *batch,
     if (!sizes_valid(cache, batch) || !k || !v) return W4A4_ERR_INVALID_VALUE;
     if (!apart(k, batch->rows, cache->heads, cache->dim) || !apart(v, batch->rows, cache->heads, cache->dim)) return W4A4_ERR_INVALID_VALUE;
     const int64_t blocks = block_bound(batch) * cache->heads;
-    if (blocks > kMax31 || !grid_fits(blocks * KV_THREADS)) return W4A4_ERR_INVALID_VALUE;
+    const int64_t threads = kv_threads((int)cache->dim);
+    if (blocks > kMax31 || !grid_fits(blocks * threads)) return W4A4_ERR_INVALID_VALUE;
     if (no_work(batch)) return W4A4_OK;
     if (!k->data || !v->data) return W4A4_ERR_INVALID_VALUE;
     const w4a4_status st = check_batch(cache, batch);
@@ -224,7 +229,7 @@ w4a4_status w4a4_read_kv(const w4a4_kv_cache *cache, const w4a4_kv_batch *batch,
     if (!aligned(k->data, size_of(dt)) || !aligned(v->data, size_of(dt))) return W4A4_ERR_MISALIGNED;
     const KvReadArgs a{pool_of(cache), batch_of(batch), static_cast<uint8_t *>(k->data), static_cast<uint8_t *>(v->data),
                        k->row_stride, k->head_stride, v->row_stride, v->head_stride, dt};
-    with_dim(cache->dim, [&](auto d) { read_kv_kernel<decltype(d)::value><<<(unsigned)blocks, KV_THREADS, 0, as_stream(stream)>>>(a); });
+    with_dim(cache->dim, [&](auto d) { read_kv_kernel<decltype(d)::value><<<(unsigned)blocks, (unsigned)threads, 0, as_stream(stream)>>>(a); });
     return hip_status("read_kv_kernel");
 }
 
