@@ -223,13 +223,21 @@ __device__ __forceinline__ void rope_turn(const AppendArgs &a, int row, int inde
     if (d >= 2 * a.half) return;
     const int pair = a.interleaved ? d / 2 : d >= a.half ? d - a.half : d;
     constexpr uint32_t bad = 0x7FC00000u;
-    if (!a.axes) {
-        const int at = a.positions ? a.positions[row] : index;
+    int axis = 0;
+    bool mixed = false;  // pairs of more than one axis among this lane's
+    if (a.axes) {
+        axis = a.axes[pair];
+#pragma unroll
+        for (int i = 1; i < 8; i++)
+            if (i < 4 || !a.interleaved) mixed |= a.axes[pair + i] != axis;
+    }
+    if (!mixed) {
+        const int at = !a.positions ? index : axis < a.n_axes ? a.positions[axis * a.ld_positions + row] : -1;
         const bool in = (uint32_t)at < (uint32_t)a.rope_rows;
         const float *p = a.rope + (in ? (int64_t)at * 2 * a.half : 0) + pair;
 #pragma unroll
         for (int i = 0; i < 2; i++) {
-            if (i && a.interleaved) break;
+            if (i && a.interleaved) continue;
             t.c[i] = in ? reinterpret_cast<const v4u_word *>(p)[i] : v4u{bad, bad, bad, bad};
             t.s[i] = in ? reinterpret_cast<const v4u_word *>(p + a.half)[i] : v4u{bad, bad, bad, bad};
         }
@@ -237,9 +245,8 @@ __device__ __forceinline__ void rope_turn(const AppendArgs &a, int row, int inde
     }
 #pragma unroll
     for (int i = 0; i < 8; i++) {
-        if (i >= 4 && a.interleaved) break;
-        const int axis = a.axes[pair + i];
-        const int at = axis < a.n_axes ? a.positions[axis * a.ld_positions + row] : -1;
+        if (i >= 4 && a.interleaved) continue;
+        const int of = a.axes[pair + i], at = of < a.n_axes ? a.positions[of * a.ld_positions + row] : -1;
         const bool in = (uint32_t)at < (uint32_t)a.rope_rows;
         const float *p = a.rope + (in ? (int64_t)at * 2 * a.half : 0) + pair + i;
         t.c[i / 4][i % 4] = in ? __float_as_uint(p[0]) : bad, t.s[i / 4][i % 4] = in ? __float_as_uint(p[a.half]) : bad;
