@@ -107,22 +107,30 @@ __device__ __forceinline__ Span span_of(const AttendArgs &a, const KvSeq &s, int
     return Span{(int)(low > 0 ? low : 0), a.causal ? min(s.len, last + 1) : s.len};
 }
 
-// Four channels of a row's result: sums y on maximum m (a power of two, above
-// LIFT), weights that sum to `total`.  A row that sees nothing has total 0.
-__device__ __forceinline__ void attend_store(const AttendArgs &a, int row0, int r, int head, int d, v4f y, float m, float total) {
-    const int i = r / a.group, h = head * a.group + (r - i * a.group);
-    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-    uint32_t w[2];
+// Where a row's result goes, and its inverse sum: sums y stand on maximum m (a
+// power of two, above LIFT), weights that sum to `total`.  A row that sees nothing
+// has total 0.
+struct RowOut {
+    uint8_t *out;
+    float inv;
+    int odt;
+    __device__ __forceinline__ void store(int d, v4f y) const {  // four channels
+        uint32_t w[2];
 #pragma unroll
-    for (int x = 0; x < 2; x++) {
-        const float lo = y[2 * x] * inv, hi = y[2 * x + 1] * inv;
-        w[x] = a.odt == ROW_F16 ? f16_bits(lo) | (uint32_t)f16_bits(hi) << 16 : bf16_bits(lo) | (uint32_t)bf16_bits(hi) << 16;
+        for (int x = 0; x < 2; x++) {
+            const float lo = y[2 * x] * inv, hi = y[2 * x + 1] * inv;
+            w[x] = odt == ROW_F16 ? f16_pair(lo, hi) : __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{lo, hi}), v2b));
+        }
+        typedef v2u v2u_any __attribute__((aligned(2)));
+        *reinterpret_cast<v2u_any *>(out + d * 2) = v2u{w[0], w[1]};
     }
-    typedef v2u v2u_any __attribute__((aligned(2)));
-    *reinterpret_cast<v2u_any *>(a.out + ((int64_t)(row0 + i) * a.o_row + (int64_t)h * a.o_head + d) * 2) = v2u{w[0], w[1]};
-    if (a.lse && d == 0)
+};
+__device__ __forceinline__ RowOut row_out(const AttendArgs &a, int row0, int r, int head, float m, float total, bool lse) {
+    const int i = r / a.group, h = head * a.group + (r - i * a.group);
+    if (lse && a.lse)
         a.lse[(int64_t)(row0 + i) * a.lse_row + h] =
             total == 0.0f ? -INFINITY : (m - ATT_LIFT + __builtin_amdgcn_logf(total)) * 0.693147180559945309f;
+    return RowOut{a.out + ((int64_t)(row0 + i) * a.o_row + (int64_t)h * a.o_head) * 2, total == 0.0f ? 0.0f : 1.0f / total, a.odt};
 }
 
 // Tiles of R rows of a sequence, for one head.
@@ -408,7 +416,7 @@ __global__ __launch_bounds__(64 * STREAM_WAVES) void attend_stream_kernel(Attend
                 if (d == 0) a.part_ml[(slot * R + r) * 2] = M, a.part_ml[(slot * R + r) * 2 + 1] = total;
                 continue;
             }
-            attend_store(a, s.row, tile * R + r, head, d, y, M, total);
+            row_out(a, s.row, tile * R + r, head, M, total, d == 0).store(d, y);
         }
         left -= stop - step;
         if (left <= 0 || !a.workers) return;
@@ -479,7 +487,7 @@ __global__ __launch_bounds__(64 * STREAM_WAVES) void attend_join_kernel(AttendAr
     total = 0.0f;
 #pragma unroll
     for (int w = 0; w < STREAM_WAVES; w++) z += reinterpret_cast<const v4f *>(sums[w])[tid], total += weights[w];
-    attend_store(a, s.row, tile * R + row, head, tid * 4, z, m, total);
+    row_out(a, s.row, tile * R + row, head, m, total, tid == 0).store(tid * 4, z);
 }
 
 
@@ -513,7 +521,7 @@ struct AttTile {
     static constexpr int RING = SB * BLOCK_BYTES > 49152 ? 2 : 3;                // stages in LDS
     static constexpr int LOADS = SB * BLOCK_BYTES / 1024 / WAVES;                // of a wave and stage
     static constexpr int RING_BYTES = RING * SB * BLOCK_BYTES;
-    static constexpr int JOIN_BYTES = TW > 1 ? 4 * 32 * D * 4 + 4 * 64 * 8 + 64 : 0;  // half the waves' sums, maxima and exponents
+    static constexpr int JOIN_BYTES = TW > 1 ? 4 * 32 * D * 4 + WAVES * (64 * 8 + 4) : 0;  // half of the waves' sums, maxima and exponents
     static constexpr int LDS = RING_BYTES > JOIN_BYTES ? RING_BYTES : JOIN_BYTES;
     static_assert(SB % TW == 0 && 64 % SB == 0 && LOADS >= 1 && LOADS * WAVES * 1024 == SB * BLOCK_BYTES && LDS <= 163840, "");
 };
@@ -562,6 +570,19 @@ __global__ __launch_bounds__(C::THREADS) void attend_tile_kernel(AttendArgs a) {
     const int begin = (int)((int64_t)stages_all * split / a.splits), stages = (int)((int64_t)stages_all * (split + 1) / a.splits) - begin;
     const int block0 = first_block + begin * C::SB, blocks = min(stages * C::SB, blocks_all - begin * C::SB);
 
+    // lane i: block i of the next 64 of this workgroup's; scales -1 where it is none
+    int held_block = 0, held_scale = -1, before_scale = -1, held_chunk = 0;
+    auto fetch_block = [&](int chunk) {
+        const int rel = chunk * 64 + lane;
+        held_chunk = chunk;
+        held_block = rel < blocks ? kv_block(a.pool, a.batch, b, head, block0 + rel) : -1;
+    };
+    auto fetch_scale = [&] {
+        before_scale = held_scale;
+        held_scale = held_block >= 0 ? reinterpret_cast<const uint16_t *>(a.pool.scales)[held_block] : -1;
+    };
+    fetch_block(0);  // first: all that follows waits for the pages
+
     // this wave's rows
     const int wrow0 = row0 + 32 * rw, wrows = min(max(rows - 32 * rw, 0), 32);
     const bool live = col < wrows;
@@ -574,32 +595,20 @@ __global__ __launch_bounds__(C::THREADS) void attend_tile_kernel(AttendArgs a) {
 #pragma unroll
             for (int i = 0; i < 2; i++) q[c][i] = *reinterpret_cast<const v4u_any *>(p + (32 * c + 16 * h + 8 * i) * 2);
     }
-    // here once, or the compiler waits for them in the loop, and for the loads that it does not see
-#pragma unroll
-    for (int c = 0; c < N; c++) asm volatile("" : "+v"(q[c][0]), "+v"(q[c][1]));
     const Span mine = span_of(a, s, r, r + 1);
     const int row_lo = mine.lo, row_hi = live ? mine.hi : 0;
     const Span wspan = wrows ? span_of(a, s, wrow0, wrow0 + wrows) : Span{0, 0};
     const int every_lo = wrows ? span_of(a, s, wrow0 + wrows - 1, wrow0 + wrows).lo : 0;
     const int every_hi = wrows ? span_of(a, s, wrow0, wrow0 + 1).hi : 0;
 
-    // lane i: block i of the next 64 of this workgroup's; scales -1 where it is none
-    int held_block = 0, held_scale = -1, before_scale = -1, held_chunk = -1;
-    auto fetch = [&](int chunk) {
-        const int rel = chunk * 64 + lane, blk = block0 + rel;
-        before_scale = held_scale, held_chunk = chunk;
-        const int at = rel < blocks ? kv_block(a.pool, a.batch, b, head, blk) : -1;
-        held_block = max(at, 0);
-        held_scale = at >= 0 ? reinterpret_cast<const uint16_t *>(a.pool.scales)[at] : -1;
-    };
     const uint32_t ring = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)smem;
     auto load = [&](int stage) {
-        if (stage * C::SB / 64 != held_chunk) fetch(stage * C::SB / 64);
+        if (stage * C::SB / 64 != held_chunk) fetch_block(stage * C::SB / 64), fetch_scale();
         const uint32_t to = ring + (uint32_t)(stage % C::RING) * (C::SB * C::BLOCK_BYTES);
 #pragma unroll
         for (int i = 0; i < C::LOADS; i++) {
             const int unit = wave + i * C::WAVES, j = unit / (D / 16);
-            const int at = wave_pick(held_block, (stage * C::SB + j) & 63);
+            const int at = max(wave_pick(held_block, (stage * C::SB + j) & 63), 0);
             att_load16(a.pool.codes + (int64_t)at * C::BLOCK_BYTES + unit % (D / 16) * 1024, lane * 16, to + unit * 1024);
         }
     };
@@ -610,8 +619,14 @@ __global__ __launch_bounds__(C::THREADS) void attend_tile_kernel(AttendArgs a) {
 #pragma unroll
     for (int c = 0; c < N; c++) o[c] = v16f{};
 
+    if (stages > 0) load(0);
+    fetch_scale();
+    // the queries here once, or the compiler waits for them in the loop, and with them
+    // for the loads that it does not see
 #pragma unroll
-    for (int i = 0; i < C::RING - 1; i++)
+    for (int c = 0; c < N; c++) asm volatile("" : "+v"(q[c][0]), "+v"(q[c][1]), "+v"(held_scale));
+#pragma unroll
+    for (int i = 1; i < C::RING - 1; i++)
         if (i < stages) load(i);
     for (int st = 0; st < stages; st++) {
         if (C::RING > 2 && st + 1 < stages) att_wait<(C::RING - 2) * C::LOADS>();
@@ -694,60 +709,63 @@ __global__ __launch_bounds__(C::THREADS) void attend_tile_kernel(AttendArgs a) {
         }
     }
 
-    // the waves of the same rows, two by two
+    // The waves of the same rows: each pair exchanges halves of its channels, until a
+    // wave has 4 N / TW quads of channels, from quad `base` on, of all.
     l = over_halves(l, Sum{});
+    constexpr int QUADS = 4 * N / C::TW;
+    int base = 0;
     if constexpr (C::TW > 1) {
-        v4f *sums = reinterpret_cast<v4f *>(smem);  // [wave][N][4][64 lanes]
+        v4f *sums = reinterpret_cast<v4f *>(smem);  // [wave][quad][64 lanes]
         v2f *mls = reinterpret_cast<v2f *>(smem + 4 * 32 * D * 4);
-        int *es = reinterpret_cast<int *>(smem + 4 * 32 * D * 4 + 4 * 64 * 8);
+        int *es = reinterpret_cast<int *>(smem + 4 * 32 * D * 4 + C::WAVES * 64 * 8);
+        auto quad = [&](int z) { return v4f{o[z / 4][z % 4 * 4], o[z / 4][z % 4 * 4 + 1], o[z / 4][z % 4 * 4 + 2], o[z / 4][z % 4 * 4 + 3]}; };
 #pragma unroll
-        for (int half = C::TW / 2; half > 0; half /= 2) {
+        for (int half = C::TW / 2, n = 2 * N; half > 0; half /= 2, n /= 2) {  // n: quads kept, and given
+            const bool upper = (tw & half) != 0;
+            const int other = wave ^ (half * C::RW);
             __syncthreads();
-            if (tw >= half && tw < 2 * half) {
-                const int at = wave - half * C::RW;
-                mls[at * 64 + lane] = v2f{m, l};
-                if (lane == 0) es[at] = E;
+            mls[wave * 64 + lane] = v2f{m, l};
+            if (lane == 0) es[wave] = E;
+            if (upper) {
 #pragma unroll
-                for (int c = 0; c < N; c++)
+                for (int z = 0; z < n; z++) sums[(wave * n + z) * 64 + lane] = quad(z);
+            } else {
 #pragma unroll
-                    for (int x = 0; x < 4; x++)
-                        sums[((at * N + c) * 4 + x) * 64 + lane] = v4f{o[c][4 * x], o[c][4 * x + 1], o[c][4 * x + 2], o[c][4 * x + 3]};
+                for (int z = 0; z < n; z++) sums[(wave * n + z) * 64 + lane] = quad(n + z);
             }
             __syncthreads();
-            if (tw < half) {
-                const v2f ml = mls[wave * 64 + lane];
-                const int e = __builtin_amdgcn_readfirstlane(es[wave]), eb = max(e, E);
-                const float mb = fmaxf(m, ml.x);
-                const float own = m > -INFINITY ? __builtin_amdgcn_exp2f(m - mb) : 1.0f, other = ml.x > -INFINITY ? __builtin_amdgcn_exp2f(ml.x - mb) : 1.0f;
-                const float fo = own * power_of_two(E - eb), fe = other * power_of_two(e - eb);
-                l = l * own + ml.y * other, m = mb, E = eb;
+            const v2f ml = mls[other * 64 + lane];
+            const int e = __builtin_amdgcn_readfirstlane(es[other]), eb = max(e, E);
+            const float mb = fmaxf(m, ml.x);
+            const float own = m > -INFINITY ? __builtin_amdgcn_exp2f(m - mb) : 1.0f, theirs = ml.x > -INFINITY ? __builtin_amdgcn_exp2f(ml.x - mb) : 1.0f;
+            const float fo = own * power_of_two(E - eb), fe = theirs * power_of_two(e - eb);
+            l = l * own + ml.y * theirs, m = mb, E = eb;
+            if (upper) base += n;
 #pragma unroll
-                for (int c = 0; c < N; c++)
+            for (int z = 0; z < n; z++) {
+                const v4f x = upper ? quad(n + z) : quad(z), y = sums[(other * n + z) * 64 + lane];
 #pragma unroll
-                    for (int x = 0; x < 4; x++) {
-                        const v4f y = sums[((wave * N + c) * 4 + x) * 64 + lane];
-#pragma unroll
-                        for (int i = 0; i < 4; i++) o[c][4 * x + i] = o[c][4 * x + i] * fo + y[i] * fe;
-                    }
+                for (int i = 0; i < 4; i++) o[z / 4][z % 4 * 4 + i] = x[i] * fo + y[i] * fe;
             }
         }
-        if (tw) return;
     }
     if (!live) return;
     const int64_t slot = ((int64_t)(order * heads + head) * a.splits + split) * C::ROWS + 32 * rw + col;
-    if (a.splits > 1 && h == 0) a.part_ml[slot * 2] = m, a.part_ml[slot * 2 + 1] = l;
-    if (a.splits > 1 && E == -1000) return;  // no block: never read
+    const bool first = tw == 0 && h == 0;
+    if (a.splits > 1) {
+        if (first) a.part_ml[slot * 2] = m, a.part_ml[slot * 2 + 1] = l;
+        if (E == -1000) return;  // no block: never read
+    }
+    const RowOut to = row_out(a, s.row, r, head, m, l, first && a.splits == 1);
 #pragma unroll
-    for (int c = 0; c < N; c++)
+    for (int z = 0; z < QUADS; z++) {
+        v4f y;
 #pragma unroll
-        for (int x = 0; x < 4; x++) {
-            v4f y;
-#pragma unroll
-            for (int i = 0; i < 4; i++) y[i] = ldexpf(o[c][4 * x + i], E);
-            const int d = 32 * c + 8 * x + 4 * h;
-            if (a.splits > 1) *reinterpret_cast<v4f *>(a.part + slot * D + d) = y;
-            else attend_store(a, s.row, r, head, d, y, m, l);
-        }
+        for (int i = 0; i < 4; i++) y[i] = ldexpf(o[z / 4][z % 4 * 4 + i], E);
+        const int d = (base + z) * 8 + 4 * h;
+        if (a.splits > 1) *reinterpret_cast<v4f *>(a.part + slot * D + d) = y;
+        else to.store(d, y);
+    }
 }
 
 // The rows of a tile that `splits` workgroups had the tokens of, a wave a row.
@@ -779,7 +797,7 @@ __global__ __launch_bounds__(256) void attend_splits_kernel(AttendArgs a) {
         const v4f x = d < D ? *reinterpret_cast<const v4f *>(a.part + (slot0 + (int64_t)i * ROWS) * D + d) : v4f{0, 0, 0, 0};
         y = some >> i & 1 ? y + fi * x : y;
     }
-    if (d < D) attend_store(a, s.row, tile * ROWS + row, head, d, y, m, total);
+    if (d < D) row_out(a, s.row, tile * ROWS + row, head, m, total, d == 0).store(d, y);
 }
 
 }  // namespace w4a4

@@ -137,6 +137,7 @@ __device__ __forceinline__ int64_t wave_pick(int64_t x, int lane) {
 // itself: 64 sequences a step, no barrier.
 template <class T, class F>
 __device__ __forceinline__ int kv_find(int seqs, T &id, int lane, F weight) {
+    if (seqs == 1) return id < weight(0) ? 0 : -1;
     for (int base = 0; base < seqs; base += 64) {
         const T w = base + lane < seqs ? weight(base + lane) : 0;
         const T sum = wave_scan(w), total = wave_pick(sum, 63);
