@@ -16,6 +16,8 @@
 // and full precision down to 2^-(14 + LIFT) of the nominal maximum.
 #pragma once
 
+#include <type_traits>
+
 #include "common.h"
 #include "k_kv.h"
 
@@ -516,6 +518,7 @@ __device__ __forceinline__ void att_load16(const uint8_t *p, uint32_t at, uint32
 template <int D_, int RW_>
 struct AttTile {
     static constexpr int D = D_, RW = RW_, WAVES = 8, TW = WAVES / RW, ROWS = 32 * RW, THREADS = 64 * WAVES;
+    static constexpr int EU_WAVES = D == 64 ? 4 : 2;  // a SIMD's waves: what the registers are held to
     static constexpr int BLOCK_BYTES = 64 * D;
     static constexpr int SB = D == 256 ? (TW > 2 ? TW : 2) : (TW > 4 ? TW : 4);  // blocks of a stage
     static constexpr int RING = SB * BLOCK_BYTES > 49152 ? 2 : 3;                // stages in LDS
@@ -548,7 +551,7 @@ __device__ __forceinline__ void att_interleave() {
 }
 
 template <class C, bool BF16>
-__global__ __launch_bounds__(C::THREADS) void attend_tile_kernel(AttendArgs a) {
+__global__ __launch_bounds__(C::THREADS, C::EU_WAVES) void attend_tile_kernel(AttendArgs a) {
     constexpr int D = C::D, N = D / 32;
     __shared__ __align__(1024) uint8_t smem[C::LDS];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid / 64);
@@ -602,15 +605,11 @@ __global__ __launch_bounds__(C::THREADS) void attend_tile_kernel(AttendArgs a) {
     const int every_hi = wrows ? span_of(a, s, wrow0, wrow0 + 1).hi : 0;
 
     const uint32_t ring = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)smem;
-    auto load = [&](int stage) {
-        if (stage * C::SB / 64 != held_chunk) fetch_block(stage * C::SB / 64), fetch_scale();
-        const uint32_t to = ring + (uint32_t)(stage % C::RING) * (C::SB * C::BLOCK_BYTES);
-#pragma unroll
-        for (int i = 0; i < C::LOADS; i++) {
-            const int unit = wave + i * C::WAVES, j = unit / (D / 16);
-            const int at = max(wave_pick(held_block, (stage * C::SB + j) & 63), 0);
-            att_load16(a.pool.codes + (int64_t)at * C::BLOCK_BYTES + unit % (D / 16) * 1024, lane * 16, to + unit * 1024);
-        }
+    auto load = [&](int stage, int i) {  // this wave's i-th of a stage
+        const int unit = wave + i * C::WAVES, j = unit / (D / 16);
+        const int at = max(wave_pick(held_block, (stage * C::SB + j) & 63), 0);
+        att_load16(a.pool.codes + (int64_t)at * C::BLOCK_BYTES + unit % (D / 16) * 1024, lane * 16,
+                   ring + (uint32_t)(stage % C::RING) * (C::SB * C::BLOCK_BYTES) + unit * 1024);
     };
 
     float m = -INFINITY, l = 0.0f;
@@ -619,21 +618,32 @@ __global__ __launch_bounds__(C::THREADS) void attend_tile_kernel(AttendArgs a) {
 #pragma unroll
     for (int c = 0; c < N; c++) o[c] = v16f{};
 
-    if (stages > 0) load(0);
+    if (stages > 0) {
+#pragma unroll
+        for (int i = 0; i < C::LOADS; i++) load(0, i);
+    }
     fetch_scale();
     // the queries here once, or the compiler waits for them in the loop, and with them
     // for the loads that it does not see
 #pragma unroll
     for (int c = 0; c < N; c++) asm volatile("" : "+v"(q[c][0]), "+v"(q[c][1]), "+v"(held_scale));
 #pragma unroll
-    for (int i = 1; i < C::RING - 1; i++)
-        if (i < stages) load(i);
+    for (int st = 1; st < C::RING - 1; st++) {
+        if (st >= stages) break;
+#pragma unroll
+        for (int i = 0; i < C::LOADS; i++) load(st, i);
+    }
     for (int st = 0; st < stages; st++) {
         if (C::RING > 2 && st + 1 < stages) att_wait<(C::RING - 2) * C::LOADS>();
         else att_wait<0>();
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");  // no read of the stage moves up
-        if (st + C::RING - 1 < stages) load(st + C::RING - 1);
+        const int next = st + C::RING - 1;  // the stage to ask for, while this one is worked on
+        const bool more = next < stages;
+        if (more && next * C::SB / 64 != held_chunk) {
+            fetch_block(next * C::SB / 64), fetch_scale();
+            asm volatile("" : "+v"(held_scale));  // waited for here, and not every stage
+        }
         uint8_t *stage = smem + st % C::RING * (C::SB * C::BLOCK_BYTES);
         // no value but zero where there is no token: once a sequence, in its last stage
         if ((block0 + (st + 1) * C::SB) * KV_BLOCK > s.len) {
@@ -648,11 +658,26 @@ __global__ __launch_bounds__(C::THREADS) void attend_tile_kernel(AttendArgs a) {
             }
             __syncthreads();
         }
+        // as if neither were known: a turn taken out of the loop moves every sum between registers
+        int j = tw, step = C::TW;
+        asm("" : "+s"(j), "+s"(step));
 #pragma unroll 1
-        for (int j = tw; j < C::SB; j += C::TW) {
+        for (int turn = 0; j < C::SB; j += step, turn++) {
             const int rel = st * C::SB + j, token0 = (block0 + rel) * KV_BLOCK;
             const int scale = wave_pick(rel / 64 == held_chunk ? held_scale : before_scale, rel & 63);
-            if (scale < 0 || token0 + KV_BLOCK <= wspan.lo || token0 >= wspan.hi) continue;
+            const bool some = scale >= 0 && token0 + KV_BLOCK > wspan.lo && token0 < wspan.hi;
+            // a turn's share of the loads, in two parts: all at once they wait for each other
+            auto ask = [&](auto part) {
+                constexpr int SHARE = (C::LOADS * C::TW + C::SB - 1) / C::SB, LO = part ? (SHARE + 1) / 2 : 0, HI = part ? SHARE : (SHARE + 1) / 2;
+#pragma unroll
+                for (int i = LO; i < HI; i++)
+                    if (more && turn * SHARE + i < C::LOADS) load(next, turn * SHARE + i);
+            };
+            ask(std::integral_constant<int, 0>{});
+            if (!some) {
+                ask(std::integral_constant<int, 1>{});
+                continue;
+            }
             const uint8_t *p = stage + j * C::BLOCK_BYTES + lane * 16;
             v16f t = {};
             __builtin_amdgcn_sched_barrier(0);
@@ -664,6 +689,7 @@ __global__ __launch_bounds__(C::THREADS) void attend_tile_kernel(AttendArgs a) {
             }
             att_interleave<N>();
             __builtin_amdgcn_sched_barrier(0);
+            ask(std::integral_constant<int, 1>{});
             const float f = fmaxf(ldexpf(a.scale_log2, (scale & 255) - 127), 1.17549435e-38f);  // never 0: -infinity stays
             if (token0 < every_lo || token0 + KV_BLOCK > every_hi) {
 #pragma unroll
