@@ -98,6 +98,20 @@ struct Sum {
     __device__ __forceinline__ float operator()(float x, float y) const { return x + y; }
 };
 
+// The wave's lanes' largest (NaN passed over), and their sum in a fixed order, in each.
+__device__ __forceinline__ float wave_larger(float x) {
+    x = fmaxf(x, dpp_of<DPP_XOR1>(x));
+    x = fmaxf(x, dpp_of<DPP_XOR2>(x));
+    x = fmaxf(x, dpp_of<DPP_MIRROR8>(x));
+    return over_groups(fmaxf(x, dpp_of<DPP_MIRROR16>(x)), Larger{});
+}
+__device__ __forceinline__ float wave_sum32(float x) {
+    x += dpp_of<DPP_XOR1>(x);
+    x += dpp_of<DPP_XOR2>(x);
+    x += dpp_of<DPP_MIRROR8>(x);
+    return over_groups(x + dpp_of<DPP_MIRROR16>(x), Sum{});
+}
+
 // The tokens that rows [r0, r1) of a sequence's head group see: [lo, hi), in
 // tokens; hi <= lo: none.
 struct Span {
@@ -147,6 +161,7 @@ __device__ __forceinline__ int tiles_of(const AttendArgs &a, const KvSeq &s) {
 
 constexpr int STREAM_WAVES = 4, STREAM_PAIR = 2 * KV_BLOCK;  // a step of a wave: two blocks
 constexpr int STREAM_LEAST = 8;                              // steps of a worker, at least
+constexpr int STREAM_WORKERS = 256;                          // at most: a thread each where they are joined
 
 template <int R>
 __device__ __forceinline__ int steps_of(const AttendArgs &a, const KvSeq &s, int tile) {
@@ -441,8 +456,8 @@ __global__ __launch_bounds__(64 * STREAM_WAVES) void attend_stream_kernel(Attend
 // in the workers' order.
 template <int D, int R>
 __global__ __launch_bounds__(64 * STREAM_WAVES) void attend_join_kernel(AttendArgs a) {
-    __shared__ __align__(16) float sums[STREAM_WAVES][D];
-    __shared__ float weights[STREAM_WAVES];
+    __shared__ v4f sums[1024 / D][D / 4];
+    __shared__ float weights[STREAM_WAVES], tops[STREAM_WAVES], factors[STREAM_WORKERS];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid / 64);
     const int page_tokens = a.pool.per_page * KV_BLOCK, heads = a.pool.heads, row = (int)blockIdx.y;
     int32_t tile = (int32_t)(blockIdx.x / heads);
@@ -468,30 +483,32 @@ __global__ __launch_bounds__(64 * STREAM_WAVES) void attend_join_kernel(AttendAr
     if (w0 == w1) return;  // written by its only worker
 
     auto slot = [&](int w) { return (int64_t)(2 * w + (w == w0 ? 1 : 0)) * R + row; };
-    float m = -INFINITY;
-    for (int w = w0 + lane; w <= w1; w += 64) m = fmaxf(m, a.part_ml[slot(w) * 2]);
-#pragma unroll
-    for (int x = 1; x < 64; x *= 2) m = fmaxf(m, __shfl_xor(m, x));
-    float y[D / 64] = {}, total = 0.0f;
-#pragma unroll 4
-    for (int w = w0 + wave; w <= w1; w += STREAM_WAVES) {
-        const float mw = a.part_ml[slot(w) * 2], f = mw > -INFINITY ? __builtin_amdgcn_exp2f(mw - m) : 1.0f;
-        total += f * a.part_ml[slot(w) * 2 + 1];
-#pragma unroll
-        for (int i = 0; i < D / 64; i++) y[i] += f * a.part[slot(w) * D + 64 * i + lane];
-    }
-#pragma unroll
-    for (int i = 0; i < D / 64; i++) sums[wave][64 * i + lane] = y[i];
+    const int count = w1 - w0 + 1;  // at most STREAM_WORKERS
+    v2f ml = {-INFINITY, 0.0f};
+    if (tid < count) ml = *reinterpret_cast<const v2f *>(a.part_ml + slot(w0 + tid) * 2);
+    float m = wave_larger(ml.x);
+    if (lane == 0) tops[wave] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+    const float f = ml.x > -INFINITY ? __builtin_amdgcn_exp2f(ml.x - m) : 1.0f;
+    if (tid < count) factors[tid] = f;
+    float total = wave_sum32(tid < count ? f * ml.y : 0.0f);
     if (lane == 0) weights[wave] = total;
     __syncthreads();
-    if (tid >= D / 4) return;
-    v4f z = {0, 0, 0, 0};
-    total = 0.0f;
+    // 4 channels a lane: a load of a wave holds 256 / D workers' rows
+    constexpr int LANES = D / 4, SIDE = 256 / LANES;
+    const int d = tid % LANES * 4, side = tid / LANES;
+    v4f y = {0, 0, 0, 0};
+#pragma unroll 8
+    for (int i = side; i < count; i += SIDE) y += factors[i] * *reinterpret_cast<const v4f *>(a.part + slot(w0 + i) * D + d);
+    sums[side][tid % LANES] = y;
+    __syncthreads();
+    if (tid >= LANES) return;
 #pragma unroll
-    for (int w = 0; w < STREAM_WAVES; w++) z += reinterpret_cast<const v4f *>(sums[w])[tid], total += weights[w];
-    row_out(a, s.row, tile * R + row, head, m, total, tid == 0).store(tid * 4, z);
+    for (int i = 1; i < SIDE; i++) y += sums[i][tid];
+    total = (weights[0] + weights[1]) + (weights[2] + weights[3]);
+    row_out(a, s.row, tile * R + row, head, m, total, tid == 0).store(d, y);
 }
-
 
 // ---------------------------------------------------------------------------
 // Many rows: a workgroup's waves share the cache's blocks through LDS
@@ -794,36 +811,39 @@ __global__ __launch_bounds__(C::THREADS, C::EU_WAVES) void attend_tile_kernel(At
     }
 }
 
+constexpr int SPLITS_MOST = 32;
+
 // The rows of a tile that `splits` workgroups had the tokens of, a wave a row.
 template <int D, int ROWS>
 __global__ __launch_bounds__(256) void attend_splits_kernel(AttendArgs a) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const int page_tokens = a.pool.per_page * KV_BLOCK, heads = a.pool.heads, row = (int)blockIdx.y * 4 + wave;
+    __shared__ float factors[4][SPLITS_MOST];
+    const int page_tokens = a.pool.per_page * KV_BLOCK, heads = a.pool.heads;
     const int order = (int)(blockIdx.x / heads), head = (int)(blockIdx.x % heads);
     int32_t tile = order;
     const int b = kv_find(a.batch.seqs, tile, lane, [&](int i) { return tiles_of<ROWS>(a, kv_seq(a.batch, page_tokens, i)); });
     if (b < 0) return;
     const KvSeq s = kv_seq(a.batch, page_tokens, b);
-    if (row >= (int64_t)s.n * a.group - (int64_t)tile * ROWS) return;
+    const int rows = (int)min((int64_t)ROWS, (int64_t)s.n * a.group - (int64_t)tile * ROWS);
+    if ((int)blockIdx.y * 4 >= rows) return;
+    const int row = min((int)blockIdx.y * 4 + wave, rows - 1);  // the last again, where there are no more
     const int64_t slot0 = (int64_t)(order * heads + head) * a.splits * ROWS + row;
     const v2f own = lane < a.splits ? *reinterpret_cast<const v2f *>(a.part_ml + (slot0 + (int64_t)lane * ROWS) * 2) : v2f{-INFINITY, 0.0f};
-    float m = own.x;
-#pragma unroll
-    for (int x = 1; x < 64; x *= 2) m = fmaxf(m, __shfl_xor(m, x));
-    const float f = own.x > -INFINITY ? __builtin_amdgcn_exp2f(own.x - m) : 1.0f;
-    float total = f * own.y;
-#pragma unroll
-    for (int x = 1; x < 64; x *= 2) total += __shfl_xor(total, x);
-    const uint64_t some = __ballot(own.x > -INFINITY || own.y != 0.0f);  // a split without tokens wrote no sums
+    const float m = wave_larger(own.x), f = own.x > -INFINITY ? __builtin_amdgcn_exp2f(own.x - m) : 1.0f;
+    const float total = wave_sum32(f * own.y);
+    // a split without tokens wrote no sums: whatever lies there is not taken
+    if (lane < a.splits) factors[wave][lane] = own.x > -INFINITY || own.y != 0.0f ? f : -1.0f;
+    __syncthreads();
     const int d = lane * 4;
+    if (d >= D) return;
     v4f y = {0, 0, 0, 0};
-#pragma unroll 4
+#pragma unroll 8
     for (int i = 0; i < a.splits; i++) {
-        const float fi = __uint_as_float(wave_pick((int32_t)__float_as_uint(f), i));
-        const v4f x = d < D ? *reinterpret_cast<const v4f *>(a.part + (slot0 + (int64_t)i * ROWS) * D + d) : v4f{0, 0, 0, 0};
-        y = some >> i & 1 ? y + fi * x : y;
+        const v4f x = *reinterpret_cast<const v4f *>(a.part + (slot0 + (int64_t)i * ROWS) * D + d);
+        const float fi = factors[wave][i];
+        y = fi >= 0.0f ? y + fi * x : y;
     }
-    if (d < D) row_out(a, s.row, tile * ROWS + row, head, m, total, d == 0).store(d, y);
+    row_out(a, s.row, tile * ROWS + row, head, m, total, lane == 0).store(d, y);
 }
 
 }  // namespace w4a4

@@ -79,6 +79,10 @@ template <int CTRL, int ROWS = 0xF>
 __device__ __forceinline__ double dpp_of(double x) {
     return __builtin_bit_cast(double, dpp_of<CTRL, ROWS>(__builtin_bit_cast(int64_t, x)));
 }
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ float dpp_of(float x) {
+    return __builtin_bit_cast(float, dpp_of<CTRL, ROWS>(__builtin_bit_cast(int32_t, x)));
+}
 constexpr int DPP_SHR1 = 0x111, DPP_SHR2 = 0x112, DPP_SHR4 = 0x114, DPP_SHR8 = 0x118, DPP_BCAST15 = 0x142, DPP_BCAST31 = 0x143,
               DPP_XOR1 = 0xB1, DPP_XOR2 = 0x4E, DPP_MIRROR8 = 0x141, DPP_MIRROR16 = 0x140;
 // Inclusive sum over the wave's lanes.

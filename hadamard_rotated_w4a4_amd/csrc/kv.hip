@@ -5,6 +5,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <numeric>
 
 #include "abi.h"
 #include "common.h"
@@ -84,13 +85,11 @@ struct Plan {
     int64_t splits;   // many rows: workgroups that share a tile's tokens
     int64_t slots(int64_t heads) const { return waves ? (splits > 1 ? tiles * heads * splits : 0) : 2 * workers; }
 };
+// Tiles of all sequences, at most: n rows of `group` heads have at most (n group +
+// tile - g) / tile, g the largest common divisor.
 int64_t tile_bound(int64_t rows, int64_t seqs, int64_t group, int64_t tile) {
-    return std::min(rows * group / tile + std::min(rows, seqs), rows * ((group + tile - 1) / tile));
+    return (rows * group + std::min(rows, seqs) * (tile - std::gcd(group, tile))) / tile;
 }
-// A workgroup's time for 32 tokens and the 32 rows of each of its waves (us, two
-// waves a SIMD), by the width of a head.
-double block_us(int64_t dim) { return 0.2 + 0.8 * (double)dim / 256; }
-
 Plan plan_of(int64_t rows, int64_t seqs, int64_t q_heads, int64_t heads, int64_t dim, int64_t tokens) {
     const int64_t group = q_heads / heads;
     Plan p{};
@@ -98,21 +97,37 @@ Plan plan_of(int64_t rows, int64_t seqs, int64_t q_heads, int64_t heads, int64_t
         p.rows = rows * group <= 16 * seqs ? 16 : 32, p.splits = 1;
         p.tiles = tile_bound(rows, seqs, group, p.rows);
         const int64_t steps = (tokens + STREAM_PAIR - 1) / STREAM_PAIR, tasks = p.tiles * heads;
-        p.workers = steps <= STREAM_LEAST || tasks >= 4096 ? 0 : std::min<int64_t>(512, tasks * (steps / STREAM_LEAST + 1));
+        // A workgroup a tile and head, or all steps shared evenly and joined (us).  Measured:
+        // a wave's step 1.3 us at D = 256, 0.9 at 128, 0.6 at 64; 5 TB/s with all CUs at work;
+        // start and end 8, or 13 with a join, and 0.03 a task joined.  Sequences of other
+        // lengths than the longest cost the first kind more than this knows: 14 us or less is
+        // taken as it is, and a quarter more than the second.
+        const double bytes_us = (double)(std::min(rows, seqs) * tokens * heads * 2 * dim) / 5e6;
+        const double step_us = (dim == 256 ? 1.3 : dim == 128 ? 0.9 : 0.6) * (p.rows == 32 ? 1.6 : 1.0);
+        const double rounds = (double)((tasks + 256 * (512 / dim) - 1) / (256 * (512 / dim)));
+        const double whole = 8 + std::max(rounds * std::ceil((double)steps / STREAM_WAVES) * step_us, bytes_us);
+        const double shared = 13 + bytes_us + 0.03 * (double)tasks;
+        if (steps > STREAM_LEAST && whole > 14 && shared < 1.25 * whole)
+            p.workers = std::min<int64_t>(STREAM_WORKERS, tasks * (steps / STREAM_LEAST + 1));
         return p;
     }
-    // The waves of a workgroup over rows or over tokens, and tiles whole or split: what
-    // the rounds of 256 workgroups would take, by a workgroup's blocks, its start and
-    // end, and the partial sums written and read.
+    // The waves of a workgroup over rows or over tokens, and tiles whole or split: the
+    // least of what the rounds of workgroups would take (us), by a workgroup's start and
+    // end and its waves' blocks of tokens, and what the partial sums would, written and read.
+    // Measured: a block with all CUs at work 1.9 us at D = 256 and 1.2 at 128, two waves a
+    // SIMD, 0.85 and with two workgroups a CU 1.45 at 64, an eighth more where four waves
+    // take four blocks in turns; start and end 13, joining 4 and 0.45 a split.
     double best = 1e30;
     const double blocks = (double)((tokens + KV_BLOCK - 1) / KV_BLOCK);
+    const int64_t slots = dim == 64 ? 512 : 256;
     for (int waves = 8; waves >= 2; waves /= 2) {
         const int64_t tiles = tile_bound(rows, seqs, group, 32 * waves), tasks = tiles * heads;
-        for (int64_t splits = 1; splits <= 32; splits++) {
+        for (int64_t splits = 1; splits <= SPLITS_MOST; splits++) {
             if (splits > 1 && (tasks * splits > 1024 || blocks < 4 * (double)splits)) break;
-            const double turns = 8 / waves, rounds = (double)((tasks * splits + 255) / 256);
-            double us = rounds * (4 + std::ceil(blocks / (double)splits / turns) * block_us(dim) + (waves < 8 ? 2 : 0));
-            if (splits > 1) us += 4 + (double)(tasks * splits * 32 * waves * dim * 8) / 4e6;
+            const int64_t all = tasks * splits;
+            const double block = (dim == 256 ? 1.9 : dim == 128 ? 1.2 : all > 256 ? 1.45 : 0.85) * (waves == 2 ? 1.13 : 1.0);
+            double us = (double)((all + slots - 1) / slots) * (13 + std::ceil(blocks / (double)splits * waves / 8) * block);
+            if (splits > 1) us += 4 + 0.45 * (double)splits + (double)(all * 32 * waves * dim * 8) / 8e6;
             if (us < best) best = us, p = Plan{32 * waves, waves, tiles, 0, splits};
         }
     }
@@ -263,7 +278,7 @@ w4a4_status w4a4_attention_kv(const w4a4_head_rows *q, w4a4_dtype dt, int64_t q_
     if (!q->data || !out->data) return W4A4_ERR_INVALID_VALUE;
     const size_t need = workspace_of(p, heads, dim);
     if (window) {  // a tile's rows see fewer tokens; the workspace is as the sizes alone have it
-        const Plan less = plan_of(rows, batch->seqs, q_heads, heads, dim, std::min(tokens, window + 2 * KV_BLOCK));
+        const Plan less = plan_of(rows, batch->seqs, q_heads, heads, dim, std::min(tokens, window + 3 * KV_BLOCK));
         if (workspace_of(less, heads, dim) <= need) p = less;
     }
     if (need && !workspace) return W4A4_ERR_INVALID_VALUE;
