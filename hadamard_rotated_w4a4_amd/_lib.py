@@ -100,6 +100,7 @@ def lib() -> ctypes.CDLL:
             "w4a4_append_kv": ([ST, P, P, P, I64, P, ST, P, P, ctypes.c_double, P, P, P, P], ST),
             "w4a4_read_kv": ([P, P, ST, P, P, P], ST),
             "w4a4_attention_kv_workspace_bytes": ([I64, I64, I64, I64, I64, I64], SZ),
+            "w4a4_attention_kv_plan": ([I64, I64, I64, I64, I64, I64, I64, ctypes.c_char_p, SZ], SZ),
             "w4a4_attention_kv": ([P, ST, I64, P, ST, P, I64, ctypes.c_double, ST, I64, P, P, P, SZ, P], ST),
         }
         for name, (args, res) in sigs.items():
@@ -806,6 +807,14 @@ def read_kv(codes: torch.Tensor, scales: torch.Tensor, pages: torch.Tensor, star
 def attention_kv_workspace_bytes(rows: int, seqs: int, q_heads: int, heads: int, dim: int, tokens: int) -> int:
     """tokens: pages of a sequence (pages.size(1)) times their length."""
     return int(lib().w4a4_attention_kv_workspace_bytes(rows, seqs, q_heads, heads, dim, tokens))
+
+
+def attention_kv_plan(rows: int, seqs: int, q_heads: int, heads: int, dim: int, tokens: int, window: int = 0) -> str:
+    """The kernels that attention_kv launches for these sizes (include/w4a4.h); ""
+    for empty or invalid sizes."""
+    text = ctypes.create_string_buffer(64)
+    lib().w4a4_attention_kv_plan(rows, seqs, q_heads, heads, dim, tokens, window, text, len(text))
+    return text.value.decode()
 
 
 def attention_kv(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, pages: torch.Tensor, starts: torch.Tensor,

@@ -5,6 +5,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <cstdio>
 #include <numeric>
 
 #include "abi.h"
@@ -139,6 +140,18 @@ size_t workspace_of(const Plan &p, int64_t heads, int64_t dim) {
     return p.slots(heads) ? up256_bytes(part_bytes(p, heads, dim)) + up256_bytes(ml_bytes(p, heads)) : 0;
 }
 
+// With a window a tile's rows see fewer tokens; the workspace is as the sizes alone have it.
+Plan plan_of(int64_t rows, int64_t seqs, int64_t q_heads, int64_t heads, int64_t dim, int64_t tokens, int64_t window) {
+    const Plan all = plan_of(rows, seqs, q_heads, heads, dim, tokens);
+    if (!window) return all;
+    const Plan less = plan_of(rows, seqs, q_heads, heads, dim, std::min(tokens, window + 3 * KV_BLOCK));
+    return workspace_of(less, heads, dim) <= workspace_of(all, heads, dim) ? less : all;
+}
+bool plan_sizes_valid(int64_t rows, int64_t seqs, int64_t q_heads, int64_t heads, int64_t dim, int64_t tokens) {
+    return rows >= 0 && rows <= kMaxRows && seqs >= 0 && seqs <= kMaxSeqs && geometry_valid(0, KV_BLOCK, heads, dim) && q_heads >= heads &&
+           q_heads <= kMaxHeads && q_heads % heads == 0 && tokens >= 0 && tokens <= kMax31;
+}
+
 template <int D, bool BF16, int NR>
 void launch_stream(const AttendArgs &a, const Plan &p, hipStream_t s) {
     const unsigned tasks = (unsigned)(p.tiles * a.pool.heads);
@@ -250,11 +263,21 @@ w4a4_status w4a4_read_kv(const w4a4_kv_cache *cache, const w4a4_kv_batch *batch,
 
 size_t w4a4_attention_kv_workspace_bytes(int64_t rows, int64_t seqs, int64_t q_heads, int64_t heads, int64_t dim,
                                          int64_t tokens) {
-    if (rows < 0 || rows > kMaxRows || seqs < 0 || seqs > kMaxSeqs || !geometry_valid(0, KV_BLOCK, heads, dim) || q_heads < heads ||
-        q_heads > kMaxHeads || q_heads % heads || tokens < 0 || tokens > kMax31)
-        return 0;
-    if (rows == 0 || seqs == 0) return 0;
+    if (!plan_sizes_valid(rows, seqs, q_heads, heads, dim, tokens) || rows == 0 || seqs == 0) return 0;
     return workspace_of(plan_of(rows, seqs, q_heads, heads, dim, tokens), heads, dim);
+}
+
+size_t w4a4_attention_kv_plan(int64_t rows, int64_t seqs, int64_t q_heads, int64_t heads, int64_t dim, int64_t tokens,
+                              int64_t window, char *text, size_t bytes) {
+    if (!text) bytes = 0;
+    if (bytes) text[0] = 0;
+    if (!plan_sizes_valid(rows, seqs, q_heads, heads, dim, tokens) || window < 0 || rows == 0 || seqs == 0) return 0;
+    const Plan p = plan_of(rows, seqs, q_heads, heads, dim, tokens, window);
+    int len;
+    if (p.waves && p.splits > 1) len = std::snprintf(text, bytes, "tile %d split %d", p.rows, (int)p.splits);
+    else if (p.workers) len = std::snprintf(text, bytes, "stream %d shared %d", p.rows, (int)p.workers);
+    else len = std::snprintf(text, bytes, "%s %d", p.waves ? "tile" : "stream", p.rows);
+    return (size_t)len;
 }
 
 w4a4_status w4a4_attention_kv(const w4a4_head_rows *q, w4a4_dtype dt, int64_t q_heads, const w4a4_head_rows *out,
@@ -272,15 +295,12 @@ w4a4_status w4a4_attention_kv(const w4a4_head_rows *q, w4a4_dtype dt, int64_t q_
         (odt != dt || (rows > 1 && q->row_stride != out->row_stride) || (q_heads > 1 && q->head_stride != out->head_stride)))
         return W4A4_ERR_INVALID_VALUE;
     const int64_t tokens = batch->pages_per_seq * cache->page, heads = cache->heads;
-    Plan p = plan_of(std::max<int64_t>(rows, 1), std::max<int64_t>(batch->seqs, 1), q_heads, heads, dim, tokens);
+    const int64_t some_rows = std::max<int64_t>(rows, 1), some_seqs = std::max<int64_t>(batch->seqs, 1);
+    const Plan p = plan_of(some_rows, some_seqs, q_heads, heads, dim, tokens, window);
     if (p.tiles > kMax31 / heads || !grid_fits(p.tiles * heads * p.splits * 512)) return W4A4_ERR_INVALID_VALUE;
     if (no_work(batch)) return W4A4_OK;
     if (!q->data || !out->data) return W4A4_ERR_INVALID_VALUE;
-    const size_t need = workspace_of(p, heads, dim);
-    if (window) {  // a tile's rows see fewer tokens; the workspace is as the sizes alone have it
-        const Plan less = plan_of(rows, batch->seqs, q_heads, heads, dim, std::min(tokens, window + 3 * KV_BLOCK));
-        if (workspace_of(less, heads, dim) <= need) p = less;
-    }
+    const size_t need = workspace_of(plan_of(rows, batch->seqs, q_heads, heads, dim, tokens), heads, dim);
     if (need && !workspace) return W4A4_ERR_INVALID_VALUE;
     const w4a4_status st = check_batch(cache, batch);
     if (st != W4A4_OK) return st;

@@ -779,11 +779,19 @@ w4a4_status w4a4_read_kv(const w4a4_kv_cache *cache, const w4a4_kv_batch *batch,
  *         replays of captured calls among them.
  * The result of a row does not depend on the other sequences of the call but for
  * the order of its fp32 sums, which is fixed for a call's sizes and lens.
+ *
+ * w4a4_attention_kv_plan: the kernels of a call of these sizes, for tests and
+ * measurements, as a line of text (as w4a4_gemm_mx4_plan): "stream R" (few rows:
+ * tiles of R, a workgroup each), "stream R shared W" (the tokens of all tiles shared
+ * evenly by W workgroups, then joined), "tile R" or "tile R split S" (a tile's tokens
+ * shared by S workgroups, then joined).  0 for empty or invalid sizes.
  * Errors: dt or odt neither fp16 nor bf16 -> W4A4_ERR_UNSUPPORTED_DTYPE; the others
  * as w4a4_append_kv, with W4A4_ERR_WORKSPACE_TOO_SMALL.
  */
 size_t w4a4_attention_kv_workspace_bytes(int64_t rows, int64_t seqs, int64_t q_heads, int64_t heads, int64_t dim,
                                          int64_t tokens);
+size_t w4a4_attention_kv_plan(int64_t rows, int64_t seqs, int64_t q_heads, int64_t heads, int64_t dim, int64_t tokens,
+                              int64_t window, char *text, size_t bytes);
 w4a4_status w4a4_attention_kv(const w4a4_head_rows *q, w4a4_dtype dt, int64_t q_heads, const w4a4_head_rows *out,
                               w4a4_dtype odt, float *lse, int64_t ld_lse, double scale, int causal, int64_t window,
                               const w4a4_kv_cache *cache, const w4a4_kv_batch *batch, void *workspace,

@@ -202,6 +202,43 @@ def test_attention(shape, seqs, mask, dt):
                     dt=torch.float16 if dt == "bf16" else torch.bfloat16)
 
 
+# the kernels of a call, and sizes for which it takes them: q heads, heads, (rows, tokens) of each
+# sequence; pages of 64 tokens
+PLANS = [
+    ("stream 16", (2, 2, [(1, 90)])),
+    ("stream 16 shared", (2, 2, [(1, 2755), (1, 0), (1, 77), (0, 900)])),
+    ("stream 32", (6, 1, [(3, 90), (4, 64), (2, 33)])),
+    ("stream 32 shared", (6, 1, [(3, 2600), (4, 1111)])),
+    ("tile 64", (20, 1, [(2, 90), (40, 41)])),
+    ("tile 64 split", (20, 1, [(2, 1300)])),
+    ("tile 128", (64, 64, [(70, 96), (100, 100), (40, 90), (70, 71), (70, 95)])),
+    ("tile 128 split", (20, 1, [(300, 2600)])),
+    ("tile 256", (64, 64, [(300, 319), (260, 300), (333, 333)])),
+    ("tile 256 split", (32, 4, [(513, 3200), (540, 999)])),
+]
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("plan,sizes", PLANS)
+def test_every_plan(plan, sizes, dim):
+    q_heads, heads, seqs = sizes
+    rng = np.random.default_rng([dim, len(plan)])
+    per = [-(-t // 64) for _, t in seqs]
+    rows, pool = sum(n for n, _ in seqs), sum(per) + 1
+    took = ops.attention_kv_plan(rows, len(seqs), q_heads, heads, dim, max(per) * 64)
+    assert took.rstrip("0123456789").rstrip() == plan.rstrip("0123456789").rstrip() and took.split()[:2] == plan.split()[:2], took
+    print(f"[gpu kv] {took}, D = {dim}", flush=True)
+    codes, scales = filled(rng, pool, 64, heads, dim)
+    codes[..., 0, :] = rng.choice(codes.reshape(-1)[codes.reshape(-1) & 127 < 60], codes[..., 0, :].shape)
+    starts = np.cumsum([0] + [n for n, _ in seqs]).astype(np.int32)
+    q = torch.from_numpy(rng.standard_normal((rows, q_heads, dim))).to(DEV, torch.float16 if dim == 128 else torch.bfloat16)
+    pages = page_table(rng, per, pool)
+    check_attention(q, codes, scales, pages, starts, np.array([t for _, t in seqs], np.int32))
+    if pages.shape[1] > 3:  # a hole, and a window that leaves workgroups without tokens
+        pages[0, 1] = -1
+        check_attention(q, codes, scales, pages, starts, np.array([t for _, t in seqs], np.int32), window=100, causal=dim != 64)
+
+
 def small_case(seed=0, dt=torch.float16, dim=128, n=5, tokens=100, heads=2, group=3, page=32):
     rng = np.random.default_rng(seed)
     pool = -(-tokens // page) + 1

@@ -88,6 +88,22 @@ def test_size_queries(L):
         assert query(*bad) == 0
 
 
+def test_attention_plan(L):
+    sizes = (512, 1, 24, 4, 256, 32768)
+    whole = ops.attention_kv_plan(*sizes)
+    assert whole.startswith("tile 256 split ") and ops.attention_kv_plan(*sizes, 64).startswith("tile ")
+    query = L.w4a4_attention_kv_plan
+    assert query(*sizes, 0, None, 99) == len(whole)
+    text = ctypes.create_string_buffer(b"left", 8)
+    assert query(*sizes, 0, text, 5) == len(whole) and text.value == b"tile"
+    for bad in ((0, 1, 24, 4, 256, 100, 0), (1, 0, 24, 4, 256, 100, 0), (1, 1, 23, 4, 256, 100, 0), (1, 1, 24, 4, 255, 100, 0),
+                (1, 1, 24, 4, 256, -1, 0), (1, 1, 24, 4, 256, 100, -1)):
+        assert query(*bad, text, 8) == 0 and text.value == b""
+    # a window never takes more workspace than the sizes alone
+    for tokens in (500, 3000, 40000):
+        assert ops.attention_kv_plan(300, 2, 24, 4, 128, tokens, 1) != ""
+
+
 @pytest.mark.parametrize("call", [append, attend, read])
 def test_sizes_are_refused_and_nothing_to_do_is_fine(L, call):
     for bad in BAD_CACHES:
