@@ -163,7 +163,8 @@ void launch_tile(const AttendArgs &a, const Plan &p, hipStream_t s) {
     using C = AttTile<D, RW>;
     const unsigned tasks = (unsigned)(p.tiles * a.pool.heads);
     attend_tile_kernel<C, BF16><<<tasks * (unsigned)p.splits, C::THREADS, 0, s>>>(a);
-    if (p.splits > 1) attend_splits_kernel<D, C::ROWS><<<dim3(tasks, C::ROWS / 4), 256, 0, s>>>(a);
+    if (p.splits > 8) attend_splits_kernel<D, C::ROWS, 4><<<dim3(tasks, C::ROWS), 256, 0, s>>>(a);
+    else if (p.splits > 1) attend_splits_kernel<D, C::ROWS, 1><<<dim3(tasks, C::ROWS / 4), 256, 0, s>>>(a);
 }
 template <int D, bool BF16>
 void launch_attend(const AttendArgs &a, const Plan &p, hipStream_t s) {
