@@ -519,7 +519,7 @@ PyObject *attention_kv(PyObject *const *a) {
         scale = PyFloat_AsDouble(a[6]);
         if (scale == -1.0 && PyErr_Occurred()) throw PythonError{};
     }
-    if (!(scale > 0.0) || !std::isfinite((float)scale)) refuse("scale = " + std::to_string(scale) + ", expected a positive number");
+    if (!(scale > 0.0) || !std::isfinite(scale)) refuse("scale = " + std::to_string(scale) + ", expected a positive number");
     const int causal = PyObject_IsTrue(a[7]);
     if (causal < 0) throw PythonError{};
     const int64_t window = integer(a[8]);

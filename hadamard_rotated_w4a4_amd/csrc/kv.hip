@@ -18,20 +18,22 @@ using namespace w4a4;
 namespace {
 
 constexpr int64_t kMaxSeqs = 65536, kMaxHeads = 8192, kMax31 = (int64_t{1} << 31) - 1;
+constexpr double kLog2e = 1.4426950408889634;
+constexpr int64_t kMaxTokens = int64_t{1} << 30;  // of a sequence: block ends stay within 31 bits
 
 inline bool known(w4a4_dtype t) { return t == W4A4_DTYPE_F32 || t == W4A4_DTYPE_F16 || t == W4A4_DTYPE_BF16; }
 inline bool known16(w4a4_dtype t) { return t == W4A4_DTYPE_F16 || t == W4A4_DTYPE_BF16; }
 inline int64_t size_of(w4a4_dtype t) { return t == W4A4_DTYPE_F32 ? 4 : 2; }
 
 inline bool geometry_valid(int64_t pages, int64_t page, int64_t heads, int64_t dim) {
-    return pages >= 0 && pages <= kMax31 && page > 0 && page <= kMax31 && page % KV_BLOCK == 0 && heads > 0 && heads <= kMaxHeads &&
+    return pages >= 0 && pages <= kMax31 && page > 0 && page <= kMaxTokens && page % KV_BLOCK == 0 && heads > 0 && heads <= kMaxHeads &&
            (dim == 64 || dim == 128 || dim == 256) && pages * heads <= kMax31 && pages * heads * (page / KV_BLOCK) <= kMax31;
 }
 
 // Sizes of a call, before anything is known of its pointers.
 bool sizes_valid(const w4a4_kv_cache *c, const w4a4_kv_batch *s) {
     return c && s && geometry_valid(c->pages, c->page, c->heads, c->dim) && s->seqs >= 0 && s->seqs <= kMaxSeqs && s->rows >= 0 &&
-           s->rows <= kMaxRows && s->pages_per_seq >= 0 && s->pages_per_seq <= kMax31 / c->page && s->ld >= s->pages_per_seq &&
+           s->rows <= kMaxRows && s->pages_per_seq >= 0 && s->pages_per_seq <= kMaxTokens / c->page && s->ld >= s->pages_per_seq &&
            s->ld <= kMax31;
 }
 inline bool no_work(const w4a4_kv_batch *s) { return s->rows == 0 || s->seqs == 0; }
@@ -149,7 +151,7 @@ Plan plan_of(int64_t rows, int64_t seqs, int64_t q_heads, int64_t heads, int64_t
 }
 bool plan_sizes_valid(int64_t rows, int64_t seqs, int64_t q_heads, int64_t heads, int64_t dim, int64_t tokens) {
     return rows >= 0 && rows <= kMaxRows && seqs >= 0 && seqs <= kMaxSeqs && geometry_valid(0, KV_BLOCK, heads, dim) && q_heads >= heads &&
-           q_heads <= kMaxHeads && q_heads % heads == 0 && tokens >= 0 && tokens <= kMax31;
+           q_heads <= kMaxHeads && q_heads % heads == 0 && tokens >= 0 && tokens <= kMaxTokens;
 }
 
 template <int D, bool BF16, int NR>
@@ -289,7 +291,7 @@ w4a4_status w4a4_attention_kv(const w4a4_head_rows *q, w4a4_dtype dt, int64_t q_
     if (!sizes_valid(cache, batch) || !q || !out || q_heads < cache->heads || q_heads > kMaxHeads || q_heads % cache->heads)
         return W4A4_ERR_INVALID_VALUE;
     const int64_t rows = batch->rows, dim = cache->dim;
-    if (!(scale > 0.0) || !std::isfinite((float)scale) || window < 0 || !strides_valid(q) || !apart(out, rows, q_heads, dim) ||
+    if (!(scale > 0.0) || !std::isfinite((float)(scale * kLog2e)) || window < 0 || !strides_valid(q) || !apart(out, rows, q_heads, dim) ||
         (lse && ld_lse < q_heads))
         return W4A4_ERR_INVALID_VALUE;
     if (q->data && q->data == out->data &&
@@ -311,7 +313,7 @@ w4a4_status w4a4_attention_kv(const w4a4_head_rows *q, w4a4_dtype dt, int64_t q_
     AttendArgs a{};
     a.q = static_cast<const uint8_t *>(q->data), a.q_row = q->row_stride, a.q_head = q->head_stride;
     a.out = static_cast<uint8_t *>(out->data), a.o_row = out->row_stride, a.o_head = out->head_stride;
-    a.lse = lse, a.lse_row = ld_lse, a.scale_log2 = (float)(scale * 1.4426950408889634);
+    a.lse = lse, a.lse_row = ld_lse, a.scale_log2 = (float)(scale * kLog2e);
     a.heads = (int32_t)q_heads, a.group = (int32_t)(q_heads / cache->heads), a.causal = causal != 0;
     a.window = (int32_t)std::min<int64_t>(window, kMax31), a.odt = odt;
     a.pool = pool_of(cache), a.batch = batch_of(batch);

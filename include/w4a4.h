@@ -673,7 +673,7 @@ w4a4_status w4a4_gemm_mx4(const void *packed_w, const uint8_t *codes, const uint
  * These arrays are read on the device; no entry makes a call read or write
  * outside its buffers.  Rows outside every sequence are left as they were.
  * Bounds: rows at most 2097120, seqs at most 65536, query heads at most 8192, pages
- * * heads * (page / 32) and pages_per_seq * page below 2^31.
+ * * heads * (page / 32) below 2^31, pages_per_seq * page at most 2^30.
  */
 typedef struct {
     void *codes;

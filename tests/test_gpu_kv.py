@@ -181,6 +181,8 @@ ATTENDS = [
     ((32, 2, 2, 64), [(9, 70)], (True, 1)),
     ((32, 4, 16, 128), [(300, 900)], (True, 0)),
     ((64, 2, 12, 256), [(150, 600), (20, 20)], (True, 0)),
+    ((32, 1, 71, 64), [(1, 500), (3, 77)], (True, 0)),  # more heads of a group than rows of a tile
+    ((32, 1, 150, 128), [(1, 300), (7, 70)], (True, 60)),
 ]
 
 
@@ -404,6 +406,27 @@ def test_in_place():
     want = ops.append_kv(packed[:, 6:8], packed[:, 8:], *cache, q=packed[:, :6], rope=rope, dtype=torch.float16)
     ops.append_kv(mine[:, 6:8], mine[:, 8:], *cache, q=mine[:, :6], rope=rope, q_out=mine[:, :6])
     assert torch.equal(mine[:, :6], want) and torch.equal(mine[:, 6:], packed[:, 6:])
+
+
+def test_rows_at_any_element():
+    """Heads and rows that begin at odd elements, heads outside rows."""
+    rng = np.random.default_rng(12)
+    for dt in (torch.float16, torch.bfloat16, torch.float32):
+        flat = torch.from_numpy(rng.standard_normal(1 + 9 * 5 * 67)).to(DEV, dt)
+        odd = flat[1:].view(9, 5, 67)[:, :, 1:65]  # strides 335 and 67
+        codes, scales = filled(rng, 3, 32, 1, 64)
+        pages, starts, lens = np.array([[2, 0]], np.int32), np.array([0, 9], np.int32), np.array([40], np.int32)
+        c, s = gpu(codes), gpu(scales)
+        out = torch.zeros(1 + 3 * 9 * 65, dtype=torch.float16, device=DEV)[1:].view(3, 9, 65).transpose(0, 1)[:, :, :64]  # heads outside rows
+        ops.append_kv(odd[:, 3:4], odd[:, 4:], c, s, gpu(pages), gpu(starts), gpu(lens), q=odd[:, :3], q_out=out, rope=gpu(rope_table(50, 48)))
+        host = odd.float().cpu().numpy()
+        want = twin.append(host[:, 3:4], host[:, 4:], codes, scales, pages, starts, lens, q=host[:, :3], rope=rope_table(50, 48))
+        assert np.array_equal(c.cpu().numpy(), codes) and np.array_equal(s.cpu().numpy(), scales)
+        assert torch.equal(out.cpu(), torch.from_numpy(want).half())
+        if dt != torch.float32:
+            check_attention(odd[:, :3], codes, scales, pages, starts, lens)
+            near = ops.attention_kv(out, c, s, gpu(pages), gpu(starts), gpu(lens))
+            assert torch.equal(ops.attention_kv(out, c, s, gpu(pages), gpu(starts), gpu(lens), out=torch.zeros_like(odd[:, :3], dtype=dt).half()), near)
 
 
 def test_offsets_past_32_bits():

@@ -69,9 +69,9 @@ def read(L, dt=BF16, k=A, v=A, strides=(512, 128), cache={}, batch={}):
 
 
 BAD_CACHES = [dict(dim=96), dict(dim=512), dict(page=48), dict(page=0), dict(heads=0), dict(heads=8193), dict(pages=-1),
-              dict(pages=1 << 31), dict(pages=1 << 28, heads=4, page=64), dict(page=1 << 31)]
+              dict(pages=1 << 31), dict(pages=1 << 28, heads=4, page=64), dict(page=(1 << 30) + 32)]
 BAD_BATCHES = [dict(seqs=-1), dict(seqs=65537), dict(rows=-1), dict(rows=2097121), dict(ld=4), dict(pages_per_seq=-1),
-               dict(pages_per_seq=1 << 26, ld=1 << 26), dict(ld=1 << 31)]
+               dict(pages_per_seq=(1 << 24) + 1, ld=1 << 26), dict(ld=1 << 31)]
 NULLS = [dict(pages=None), dict(starts=None), dict(lens=None)]
 
 
@@ -84,7 +84,7 @@ def test_size_queries(L):
     assert query(1, 1, 24, 4, 256, 1 << 17) > 0
     assert query(1, 1, 24, 4, 256, 256) == 0  # few tokens: nothing to share
     for bad in ((-1, 1, 24, 4, 256, 100), (1, 1, 23, 4, 256, 1 << 17), (1, 1, 2, 4, 256, 1 << 17), (1, 1, 24, 4, 250, 1 << 17),
-                (1, 1, 24, 4, 256, 1 << 31), (2097121, 1, 24, 4, 256, 1 << 17), (1, 65537, 24, 4, 256, 1 << 17)):
+                (1, 1, 24, 4, 256, (1 << 30) + 1), (2097121, 1, 24, 4, 256, 1 << 17), (1, 65537, 24, 4, 256, 1 << 17)):
         assert query(*bad) == 0
 
 
@@ -143,7 +143,7 @@ def test_append_refusals(L):
 def test_attention_refusals(L):
     long = dict(pages_per_seq=4096, ld=4096)
     for bad in (dict(q=None), dict(out=None), dict(q_heads=6), dict(q_heads=0), dict(q_heads=2), dict(scale=0.0), dict(scale=-1.0),
-                dict(scale=float("nan")), dict(scale=1e60), dict(window=-1), dict(lse=A, ld=7), dict(strides=(-1, 128)), dict(strides=(1024, 64)),
+                dict(scale=float("nan")), dict(scale=1e60), dict(scale=3e38), dict(window=-1), dict(lse=A, ld=7), dict(strides=(-1, 128)), dict(strides=(1024, 64)),
                 dict(out=A), dict(batch=long, ws=None)):
         assert attend(L, **bad) == INVALID, bad
     assert attend(L, dt=F32) == DTYPE and attend(L, odt=F32) == DTYPE
