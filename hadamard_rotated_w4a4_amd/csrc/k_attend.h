@@ -540,7 +540,7 @@ struct AttTile {
     static constexpr int SB = D == 256 ? (TW > 2 ? TW : 2) : (TW > 4 ? TW : 4);  // blocks of a stage
     static constexpr int RING = SB * BLOCK_BYTES > 49152 ? 2 : 3;                // stages in LDS
     static constexpr int LOADS = SB * BLOCK_BYTES / 1024 / WAVES;                // of a wave and stage
-    static constexpr int RING_BYTES = RING * SB * BLOCK_BYTES;
+    static constexpr int STAGE_BYTES = SB * BLOCK_BYTES, RING_BYTES = RING * STAGE_BYTES;
     static constexpr int JOIN_BYTES = TW > 1 ? 4 * 32 * D * 4 + WAVES * (64 * 8 + 4) : 0;  // half of the waves' sums, maxima and exponents
     static constexpr int LDS = RING_BYTES > JOIN_BYTES ? RING_BYTES : JOIN_BYTES;
     static_assert(SB % TW == 0 && 64 % SB == 0 && LOADS >= 1 && LOADS * WAVES * 1024 == SB * BLOCK_BYTES && LDS <= 163840, "");
@@ -587,24 +587,37 @@ __global__ __launch_bounds__(C::THREADS, C::EU_WAVES) void attend_tile_kernel(At
     const Span span = span_of(a, s, row0, row0 + rows);
     const int first_block = span.lo / KV_BLOCK, blocks_all = span.hi <= span.lo ? 0 : (span.hi - 1) / KV_BLOCK + 1 - first_block;
     const int stages_all = (blocks_all + C::SB - 1) / C::SB;
-    const int begin = (int)((int64_t)stages_all * split / a.splits), stages = (int)((int64_t)stages_all * (split + 1) / a.splits) - begin;
-    const int block0 = first_block + begin * C::SB, blocks = min(stages * C::SB, blocks_all - begin * C::SB);
+    const int begin = (int)((int64_t)stages_all * split / a.splits), stages = __builtin_amdgcn_readfirstlane((int)((int64_t)stages_all * (split + 1) / a.splits) - begin);
+    const int block0 = __builtin_amdgcn_readfirstlane(first_block + begin * C::SB), blocks = __builtin_amdgcn_readfirstlane(min(stages * C::SB, blocks_all - begin * C::SB));
 
-    // lane i: block i of the next 64 of this workgroup's; scales -1 where it is none
-    int held_block = 0, held_scale = -1, before_scale = -1, held_chunk = 0;
+    // this wave's rows, and what they see: each its own [row_lo, row_hi), one of them
+    // [wspan.lo, wspan.hi), all [every_lo, every_hi)
+    const int wrow0 = row0 + 32 * rw, wrows = min(max(rows - 32 * rw, 0), 32);
+    const Span wspan = wrows ? span_of(a, s, wrow0, wrow0 + wrows) : Span{0, 0};
+    const int every_lo = wrows ? span_of(a, s, wrow0 + wrows - 1, wrow0 + wrows).lo : 0;
+    const int every_hi = wrows ? span_of(a, s, wrow0, wrow0 + 1).hi : 0;
+
+    // lane i, for block i of 64 of this workgroup's: where it lies, and its scales (16
+    // bits, and EDGE where not every row sees all of it), or -1 where this wave has
+    // nothing to do.  One read of a lane a block then, not a dozen scalar operations.
+    constexpr int EDGE = 1 << 16;
+    int held_block = -1, held_info = -1, held_chunk = 0;
+    uint32_t held_lo = 0, held_hi = 0;
     auto fetch_block = [&](int chunk) {
         const int rel = chunk * 64 + lane;
         held_chunk = chunk;
         held_block = rel < blocks ? kv_block(a.pool, a.batch, b, head, block0 + rel) : -1;
+        const uint64_t at = reinterpret_cast<uint64_t>(a.pool.codes) + (uint64_t)max(held_block, 0) * C::BLOCK_BYTES;
+        held_lo = (uint32_t)at, held_hi = (uint32_t)(at >> 32);
     };
-    auto fetch_scale = [&] {
-        before_scale = held_scale;
-        held_scale = held_block >= 0 ? reinterpret_cast<const uint16_t *>(a.pool.scales)[held_block] : -1;
+    auto fetch_info = [&] {
+        const int token = (block0 + held_chunk * 64 + lane) * KV_BLOCK;
+        const bool some = held_block >= 0 && token + KV_BLOCK > wspan.lo && token < wspan.hi;
+        held_info = some ? reinterpret_cast<const uint16_t *>(a.pool.scales)[held_block] : -1;
+        if (some && (token < every_lo || token + KV_BLOCK > every_hi)) held_info |= EDGE;
     };
     fetch_block(0);  // first: all that follows waits for the pages
 
-    // this wave's rows
-    const int wrow0 = row0 + 32 * rw, wrows = min(max(rows - 32 * rw, 0), 32);
     const bool live = col < wrows;
     const int r = live ? wrow0 + col : row0, qi = r / a.group;
     v4u q[N][2];
@@ -617,16 +630,16 @@ __global__ __launch_bounds__(C::THREADS, C::EU_WAVES) void attend_tile_kernel(At
     }
     const Span mine = span_of(a, s, r, r + 1);
     const int row_lo = mine.lo, row_hi = live ? mine.hi : 0;
-    const Span wspan = wrows ? span_of(a, s, wrow0, wrow0 + wrows) : Span{0, 0};
-    const int every_lo = wrows ? span_of(a, s, wrow0 + wrows - 1, wrow0 + wrows).lo : 0;
-    const int every_hi = wrows ? span_of(a, s, wrow0, wrow0 + 1).hi : 0;
 
+    // This wave's i-th load of a stage: unit (KB) wave + 8 i of its blocks.  at: the
+    // stage's first block in the held 64; into: its place in LDS.
     const uint32_t ring = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)smem;
-    auto load = [&](int stage, int i) {  // this wave's i-th of a stage
-        const int unit = wave + i * C::WAVES, j = unit / (D / 16);
-        const int at = max(wave_pick(held_block, (stage * C::SB + j) & 63), 0);
-        att_load16(a.pool.codes + (int64_t)at * C::BLOCK_BYTES + unit % (D / 16) * 1024, lane * 16,
-                   ring + (uint32_t)(stage % C::RING) * (C::SB * C::BLOCK_BYTES) + unit * 1024);
+    constexpr int PIECES = D / 16;  // of a block
+    const uint32_t lane_at = (wave % PIECES) * 1024 + lane * 16;
+    auto load = [&](int at, uint32_t into, int i) {
+        const int block = at + (wave + i * C::WAVES) / PIECES;
+        const uint64_t p = (uint64_t)(uint32_t)wave_pick((int)held_hi, block) << 32 | (uint32_t)wave_pick((int)held_lo, block);
+        att_load16(reinterpret_cast<const uint8_t *>(p), lane_at + i * C::WAVES % PIECES * 1024, into + wave * 1024 + i * (C::WAVES * 1024));
     };
 
     float m = -INFINITY, l = 0.0f;
@@ -637,35 +650,38 @@ __global__ __launch_bounds__(C::THREADS, C::EU_WAVES) void attend_tile_kernel(At
 
     if (stages > 0) {
 #pragma unroll
-        for (int i = 0; i < C::LOADS; i++) load(0, i);
+        for (int i = 0; i < C::LOADS; i++) load(0, ring, i);
     }
-    fetch_scale();
+    fetch_info();
     // the queries here once, or the compiler waits for them in the loop, and with them
     // for the loads that it does not see
 #pragma unroll
-    for (int c = 0; c < N; c++) asm volatile("" : "+v"(q[c][0]), "+v"(q[c][1]), "+v"(held_scale));
+    for (int c = 0; c < N; c++) asm volatile("" : "+v"(q[c][0]), "+v"(q[c][1]), "+v"(held_info));
 #pragma unroll
     for (int st = 1; st < C::RING - 1; st++) {
         if (st >= stages) break;
 #pragma unroll
-        for (int i = 0; i < C::LOADS; i++) load(st, i);
+        for (int i = 0; i < C::LOADS; i++) load(st * C::SB, ring + st * C::STAGE_BYTES, i);
     }
+    int info = held_info, from = 0, to = C::RING - 1;  // the stage's blocks, its place, and that of the next to ask for
+    const int tail = __builtin_amdgcn_readfirstlane(s.len / KV_BLOCK - block0);               // the block with the sequence's end, of this workgroup's
     for (int st = 0; st < stages; st++) {
         if (C::RING > 2 && st + 1 < stages) att_wait<(C::RING - 2) * C::LOADS>();
         else att_wait<0>();
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");  // no read of the stage moves up
-        const int next = st + C::RING - 1;  // the stage to ask for, while this one is worked on
-        const bool more = next < stages;
-        if (more && next * C::SB / 64 != held_chunk) {
-            fetch_block(next * C::SB / 64), fetch_scale();
-            asm volatile("" : "+v"(held_scale));  // waited for here, and not every stage
+        const int first = st * C::SB, next = first + (C::RING - 1) * C::SB;  // blocks
+        const bool more = st + C::RING - 1 < stages;  // a stage to ask for, while this one is worked on
+        if ((first & 63) == 0 && st) info = held_info;
+        if (more && (next & 63) == 0) {
+            fetch_block(next / 64), fetch_info();
+            asm volatile("" : "+v"(held_info));  // waited for here, and not every stage
         }
-        uint8_t *stage = smem + st % C::RING * (C::SB * C::BLOCK_BYTES);
+        uint8_t *stage = smem + from * C::STAGE_BYTES;
         // no value but zero where there is no token: once a sequence, in its last stage
-        if ((block0 + (st + 1) * C::SB) * KV_BLOCK > s.len) {
+        if (tail < first + C::SB) {
             for (int u = tid; u < C::SB * 2 * D; u += C::THREADS) {
-                const int j = u / (2 * D), x = u % (2 * D), in = s.len - (block0 + st * C::SB + j) * KV_BLOCK;
+                const int j = u / (2 * D), x = u % (2 * D), in = s.len - (block0 + first + j) * KV_BLOCK;
                 if (in >= KV_BLOCK) continue;
                 v4u *piece = reinterpret_cast<v4u *>(stage + j * C::BLOCK_BYTES + 32 * D) + x;
                 v4u y = *piece;
@@ -675,22 +691,23 @@ __global__ __launch_bounds__(C::THREADS, C::EU_WAVES) void attend_tile_kernel(At
             }
             __syncthreads();
         }
+        const uint32_t into = ring + to * C::STAGE_BYTES;
         // as if neither were known: a turn taken out of the loop moves every sum between registers
         int j = tw, step = C::TW;
         asm("" : "+s"(j), "+s"(step));
 #pragma unroll 1
         for (int turn = 0; j < C::SB; j += step, turn++) {
-            const int rel = st * C::SB + j, token0 = (block0 + rel) * KV_BLOCK;
-            const int scale = wave_pick(rel / 64 == held_chunk ? held_scale : before_scale, rel & 63);
-            const bool some = scale >= 0 && token0 + KV_BLOCK > wspan.lo && token0 < wspan.hi;
+            int scale = wave_pick(info, (first & 63) + j);
+            asm volatile("" : "+s"(scale));  // nor this (the second test below is a part of the same: -1 says it all)
             // a turn's share of the loads, in two parts: all at once they wait for each other
             auto ask = [&](auto part) {
                 constexpr int SHARE = (C::LOADS * C::TW + C::SB - 1) / C::SB, LO = part ? (SHARE + 1) / 2 : 0, HI = part ? SHARE : (SHARE + 1) / 2;
 #pragma unroll
                 for (int i = LO; i < HI; i++)
-                    if (more && turn * SHARE + i < C::LOADS) load(next, turn * SHARE + i);
+                    if (more && turn * SHARE + i < C::LOADS) load(next & 63, into, turn * SHARE + i);
             };
             ask(std::integral_constant<int, 0>{});
+            const bool some = scale >= 0 && (block0 + first + j) * KV_BLOCK < wspan.hi;
             if (!some) {
                 ask(std::integral_constant<int, 1>{});
                 continue;
@@ -708,10 +725,11 @@ __global__ __launch_bounds__(C::THREADS, C::EU_WAVES) void attend_tile_kernel(At
             __builtin_amdgcn_sched_barrier(0);
             ask(std::integral_constant<int, 1>{});
             const float f = fmaxf(ldexpf(a.scale_log2, (scale & 255) - 127), 1.17549435e-38f);  // never 0: -infinity stays
-            if (token0 < every_lo || token0 + KV_BLOCK > every_hi) {
+            if (scale & EDGE) {
+                const int token = (block0 + first + j) * KV_BLOCK;
 #pragma unroll
                 for (int v = 0; v < 16; v++) {
-                    const int at = token0 + mfma32_row(v, lane);
+                    const int at = token + mfma32_row(v, lane);
                     if (at < row_lo || at >= row_hi) t[v] = -INFINITY;
                 }
             }
@@ -720,7 +738,7 @@ __global__ __launch_bounds__(C::THREADS, C::EU_WAVES) void attend_tile_kernel(At
             for (int v = 1; v < 16; v++) top = fmaxf(top, t[v]);
             top = over_halves(top * f, Larger{});
             const bool up = top > m + ATT_RAISE;
-            const int e = (scale >> 8) - 127;
+            const int e = (scale >> 8 & 255) - 127;
             if (__ballot(up) != 0 || e > E) {
                 const float alpha = up ? __builtin_amdgcn_exp2f(m - top) : 1.0f, beta = alpha * (e > E ? power_of_two(E - e) : 1.0f);
                 if (up) m = top;
@@ -750,6 +768,7 @@ __global__ __launch_bounds__(C::THREADS, C::EU_WAVES) void attend_tile_kernel(At
             att_interleave<N>();
             __builtin_amdgcn_sched_barrier(0);
         }
+        from = from + 1 == C::RING ? 0 : from + 1, to = to + 1 == C::RING ? 0 : to + 1;
     }
 
     // The waves of the same rows: each pair exchanges halves of its channels, until a
@@ -799,7 +818,7 @@ __global__ __launch_bounds__(C::THREADS, C::EU_WAVES) void attend_tile_kernel(At
         if (first) a.part_ml[slot * 2] = m, a.part_ml[slot * 2 + 1] = l;
         if (E == -1000) return;  // no block: never read
     }
-    const RowOut to = row_out(a, s.row, r, head, m, l, first && a.splits == 1);
+    const RowOut out = row_out(a, s.row, r, head, m, l, first && a.splits == 1);
 #pragma unroll
     for (int z = 0; z < QUADS; z++) {
         v4f y;
@@ -807,7 +826,7 @@ __global__ __launch_bounds__(C::THREADS, C::EU_WAVES) void attend_tile_kernel(At
         for (int i = 0; i < 4; i++) y[i] = ldexpf(o[z / 4][z % 4 * 4 + i], E);
         const int d = (base + z) * 8 + 4 * h;
         if (a.splits > 1) *reinterpret_cast<v4f *>(a.part + slot * D + d) = y;
-        else to.store(d, y);
+        else out.store(d, y);
     }
 }
 
