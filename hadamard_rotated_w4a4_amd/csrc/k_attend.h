@@ -11,6 +11,13 @@
 // as the output's own type or better), and summed as rounded, so that a row's weights
 // add up to one.
 //
+// One row of 131072 tokens (24 heads over 4 of 256, 268 MB) takes 59 us, 4.5 TB/s; 32
+// sequences of up to 16384 (48 over 8 of 128, 683 MB) 132, 5.2 TB/s: memory, where a
+// copy reaches 4.9.  512 rows of 32768 tokens take 405 us, 1010 TFLOP/s at D = 256, and
+// of 8192 144, 690, at D = 128, where a large product reaches 1200: a block's 32 x 32
+// scores cost a wave the same 75 vector instructions and 16 exponentials whatever D,
+// and its keys and values D / 2 conversions, beside D / 8 products.
+//
 // m is raised only where a tile's maximum passes it by over RAISE: accumulators are
 // rescaled seldom.  Weights carry a factor 2^LIFT: at most 2^(LIFT + RAISE) < 65504,
 // and full precision down to 2^-(14 + LIFT) of the nominal maximum.
@@ -189,6 +196,9 @@ __device__ __forceinline__ int64_t workers_used(int64_t steps, int workers) {
 // R = 16 NR rows (one head group's) of one sequence against its tokens, 64 a step:
 // S^T = K Q^T by 16 x 16 x 32 products, whose rows are chosen such that lane group
 // g holds the tokens of block g / 2 and half g % 2 as the value pieces have them.
+// A wave asks for a step's 128 D bytes at once, 16 contiguous bytes a lane: with 4 waves
+// a CU 128 KB in flight at D = 256, and no faster with 8 or 16.  Short sequences are a
+// chain of latencies (lengths, page, codes, two steps, the waves' sums): 300 tokens 8.6 us.
 template <int D, bool BF16, int NR>
 __global__ __launch_bounds__(64 * STREAM_WAVES) void attend_stream_kernel(AttendArgs a) {
     constexpr int R = 16 * NR, J = D / 64, C = D / 32, PITCH = D + 4;
@@ -531,6 +541,16 @@ __device__ __forceinline__ void att_load16(const uint8_t *p, uint32_t at, uint32
     asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" : "={m0}"(m0) : "v"(at), "s"(p), "s"(lds) : "memory");
 }
 
+// What holds a workgroup here: blocks come to LDS as 8-bit codes by direct loads (2
+// a wave and block at D = 256), so that 8 waves share each; a wave converts what it
+// reads.  Converted once, in LDS, they would be twice the reads, as long as the products
+// take.  Measured at D = 256, two waves a SIMD, cycles a block: keys 1050 and values 1050
+// (the matrix cores' 512 each, for both waves), softmax 820, loads, barrier and loop 600;
+// the two waves' products hardly meet the other's softmax.  Half a turn apart by barriers
+// (one multiplies while the other exponentiates) it was slower, 505 us against 428: a wave
+// alone issues a vector instruction every 7 to 8 cycles.  64 rows a wave (D = 64, 128)
+// changed nothing, nor did reads further ahead.
+//
 // RW waves of 32 rows each, times TW that take turns at a stage's blocks.
 template <int D_, int RW_>
 struct AttTile {
