@@ -317,6 +317,7 @@ w4a4_status w4a4_attention_kv(const w4a4_head_rows *q, w4a4_dtype dt, int64_t q_
     a.heads = (int32_t)q_heads, a.group = (int32_t)(q_heads / cache->heads), a.causal = causal != 0;
     a.window = (int32_t)std::min<int64_t>(window, kMax31), a.odt = odt;
     a.pool = pool_of(cache), a.batch = batch_of(batch);
+    if (!cache->pages) a.batch.per_seq = 0;  // no block at all: none may stand in for one that a sequence lacks
     a.part = static_cast<float *>(workspace), a.tile_bound = (int32_t)p.tiles;
     a.workers = (int32_t)p.workers, a.splits = (int32_t)p.splits;
     if (p.slots(heads)) a.part_ml = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + up256_bytes(part_bytes(p, heads, dim)));

@@ -394,6 +394,25 @@ def test_nothing_to_do():
     assert not bool(k.any()) and not bool(v.any())
 
 
+@pytest.mark.parametrize("plan,sizes", PLANS)
+def test_a_cache_without_pages(plan, sizes):
+    """Every sequence's entries name pages, of a pool that has none: rows see nothing."""
+    q_heads, heads, seqs = sizes
+    rng = np.random.default_rng(len(plan))
+    codes, scales = ops.new_kv_cache(0, 64, heads, 128, DEV)
+    starts = np.cumsum([0] + [n for n, _ in seqs]).astype(np.int32)
+    lens = np.array([t for _, t in seqs], np.int32)
+    pages = np.zeros((len(seqs), -(-int(lens.max()) // 64)), np.int32)
+    q = torch.from_numpy(rng.standard_normal((int(starts[-1]), q_heads, 128))).to(DEV, torch.bfloat16)
+    print(f"[gpu kv] no pages, {plan}", flush=True)
+    for causal in (True, False):
+        check_attention(q, codes.cpu().numpy(), scales.cpu().numpy(), pages, starts, lens, causal=causal)
+    k = torch.ones((len(q), heads, 128), device=DEV)
+    assert torch.equal(ops.append_kv(k, k, codes, scales, gpu(pages), gpu(starts), gpu(lens), q=k), k.bfloat16())
+    back = ops.read_kv(codes, scales, gpu(pages), gpu(starts), gpu(lens), len(q))
+    assert not back[0].any() and not back[1].any()
+
+
 def test_in_place():
     q, codes, scales, pages, starts, lens = small_case(n=40, dim=128, tokens=700)
     cache = gpu(codes), gpu(scales), gpu(pages), gpu(starts), gpu(lens)
