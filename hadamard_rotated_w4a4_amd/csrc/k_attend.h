@@ -6,10 +6,11 @@
 // fp32, 16 products in 16 bits an fp32 accumulator.  Keys become the queries' type
 // (fp16 or bf16; an E4M3 code is exact in both) and values fp16 by the conversion
 // instruction, two a lane.  The keys' scale goes into the factor of the exponent.
-// The values' is applied by their conversion relative to the largest one so far, 2^E,
-// so that they stay within fp16, and 2^E at the end.  p is rounded to fp16 (11 bits,
-// as the output's own type or better), and summed as rounded, so that a row's weights
-// add up to one.
+// p is rounded to fp16 (11 bits, as the output's own type or better), and summed as
+// rounded, so that a row's weights add up to one.  The values' scale goes into the
+// weights then, relative to the largest one that the row has seen so far, 2^E, and 2^E
+// at the end: a power of two, exact but below 2^-14.  (Applied by the values' conversion
+// it would be one E for all rows of a wave, and one that not all of them may see.)
 //
 // One row of 131072 tokens (24 heads over 4 of 256, 268 MB) takes 59 us, 4.5 TB/s; 32
 // sequences of up to 16384 (48 over 8 of 128, 683 MB) 132, 5.2 TB/s: memory, where a
@@ -48,7 +49,7 @@ struct AttendArgs {
     int32_t causal, window, odt;
     KvPool pool;
     KvBatch batch;
-    // partial results: [slots][rows of a tile][D] sums, then [slots][rows][2] maxima and sums
+    // partial results: [slots][rows of a tile][D] weighted means, then [slots][rows][2] maxima and sums
     float *part, *part_ml;
     int32_t splits;      // workgroups that share a tile's tokens (many rows)
     int32_t workers;     // workgroups that share all tiles' tokens evenly; 0: one workgroup a tile and head
@@ -81,22 +82,29 @@ __device__ __forceinline__ v4f mfma_16x16x32(v4u a, v4u b, v4f c) {
 __device__ __forceinline__ uint32_t f16_pair(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{a, b}), v2h));
 }
+// Two fp16 values times 2^e, e <= 0.
+__device__ __forceinline__ uint32_t scale_pair(uint32_t x, _Float16 f) { return __builtin_bit_cast(uint32_t, __builtin_bit_cast(v2h, x) * v2h{f, f}); }
+__device__ __forceinline__ _Float16 half_power(int e) { return (_Float16)ldexpf(1.0f, e); }
 // c + the sum of two fp16 values.
 __device__ __forceinline__ float add_pair(uint32_t x, float c) {
     return __builtin_amdgcn_fdot2(__builtin_bit_cast(v2h, x), v2h{(_Float16)1.0f, (_Float16)1.0f}, c, false);
 }
 __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(min(max(e, -126), 127) + 127) << 23); }
 
-// x over the lanes l and l ^ 32; over l, l ^ 16, l ^ 32 and l ^ 48.
+// x over the lanes l and l ^ 32; l and l ^ 16; l, l ^ 16, l ^ 32 and l ^ 48.
 template <class F>
 __device__ __forceinline__ float over_halves(float x, F f) {
     const auto y = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
     return f(__uint_as_float(y[0]), __uint_as_float(y[1]));
 }
 template <class F>
-__device__ __forceinline__ float over_groups(float x, F f) {
+__device__ __forceinline__ float over_pairs(float x, F f) {
     const auto y = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    return over_halves(f(__uint_as_float(y[0]), __uint_as_float(y[1])), f);
+    return f(__uint_as_float(y[0]), __uint_as_float(y[1]));
+}
+template <class F>
+__device__ __forceinline__ float over_groups(float x, F f) {
+    return over_halves(over_pairs(x, f), f);
 }
 struct Larger {
     __device__ __forceinline__ float operator()(float x, float y) const { return fmaxf(x, y); }
@@ -130,30 +138,33 @@ __device__ __forceinline__ Span span_of(const AttendArgs &a, const KvSeq &s, int
     return Span{(int)(low > 0 ? low : 0), a.causal ? min(s.len, last + 1) : s.len};
 }
 
-// Where a row's result goes, and its inverse sum: sums y stand on maximum m (a
-// power of two, above LIFT), weights that sum to `total`.  A row that sees nothing
-// has total 0.
+// What sums of weighted values are multiplied with: the weights' sum, inverse; 0 for
+// a row that sees nothing.  Before the values' own exponent, so that no product on the
+// way is larger than the values are.
+__device__ __forceinline__ float inverse(float total) { return total == 0.0f ? 0.0f : 1.0f / total; }
+
+// Where a row's result goes.
 struct RowOut {
     uint8_t *out;
-    float inv;
     int odt;
     __device__ __forceinline__ void store(int d, v4f y) const {  // four channels
         uint32_t w[2];
 #pragma unroll
         for (int x = 0; x < 2; x++) {
-            const float lo = y[2 * x] * inv, hi = y[2 * x + 1] * inv;
+            const float lo = y[2 * x], hi = y[2 * x + 1];
             w[x] = odt == ROW_F16 ? f16_pair(lo, hi) : __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{lo, hi}), v2b));
         }
         typedef v2u v2u_any __attribute__((aligned(2)));
         *reinterpret_cast<v2u_any *>(out + d * 2) = v2u{w[0], w[1]};
     }
 };
+// Weights that sum to `total` stand on maximum m (a power of two, above LIFT).
 __device__ __forceinline__ RowOut row_out(const AttendArgs &a, int row0, int r, int head, float m, float total, bool lse) {
     const int i = r / a.group, h = head * a.group + (r - i * a.group);
     if (lse && a.lse)
         a.lse[(int64_t)(row0 + i) * a.lse_row + h] =
             total == 0.0f ? -INFINITY : (m - ATT_LIFT + __builtin_amdgcn_logf(total)) * 0.693147180559945309f;
-    return RowOut{a.out + ((int64_t)(row0 + i) * a.o_row + (int64_t)h * a.o_head) * 2, total == 0.0f ? 0.0f : 1.0f / total, a.odt};
+    return RowOut{a.out + ((int64_t)(row0 + i) * a.o_row + (int64_t)h * a.o_head) * 2, a.odt};
 }
 
 // Tiles of R rows of a sequence, for one head.
@@ -204,6 +215,7 @@ __global__ __launch_bounds__(64 * STREAM_WAVES) void attend_stream_kernel(Attend
     constexpr int R = 16 * NR, J = D / 64, C = D / 32, PITCH = D + 4;
     __shared__ __align__(16) float sums[STREAM_WAVES * R * PITCH];
     __shared__ float mls[STREAM_WAVES][R][2];
+    __shared__ int es[STREAM_WAVES][R];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid / 64);
     const int t16 = lane & 15, g = lane >> 4, page_tokens = a.pool.per_page * KV_BLOCK, heads = a.pool.heads;
 
@@ -262,10 +274,10 @@ __global__ __launch_bounds__(64 * STREAM_WAVES) void attend_stream_kernel(Attend
 
         float m[NR], l[NR];
         v4f o[NR][C][2];
-        int E = -1000;
+        int E[NR];
 #pragma unroll
         for (int n = 0; n < NR; n++) {
-            m[n] = -INFINITY, l[n] = 0.0f;
+            m[n] = -INFINITY, l[n] = 0.0f, E[n] = -1000;
 #pragma unroll
             for (int c = 0; c < C; c++) o[n][c][0] = o[n][c][1] = v4f{0, 0, 0, 0};
         }
@@ -340,7 +352,9 @@ __global__ __launch_bounds__(64 * STREAM_WAVES) void attend_stream_kernel(Attend
                 }
             }
 
+            const int e = have ? (mine >> 8) - 127 : -1000;  // of this lane's tokens' values
             float top[NR];
+            int seen[NR];  // the larger of the step's exponents that a row sees
             bool raise = false;
 #pragma unroll
             for (int n = 0; n < NR; n++) {
@@ -349,19 +363,20 @@ __global__ __launch_bounds__(64 * STREAM_WAVES) void attend_stream_kernel(Attend
                 for (int x = 0; x < 4; x++)
 #pragma unroll
                     for (int r = 0; r < 4; r++) t = fmaxf(t, st[n][x][r]);
-                top[n] = over_groups(t * f, Larger{});
-                raise |= top[n] > m[n] + ATT_RAISE;
+                t = over_pairs(t * f, Larger{});
+                const int own = t > -INFINITY ? e : -1000;
+                top[n] = over_halves(t, Larger{});
+                seen[n] = (int)swap32((uint32_t)own, [](uint32_t x, uint32_t y) { return (uint32_t)max((int)x, (int)y); });
+                raise |= top[n] > m[n] + ATT_RAISE || seen[n] > E[n];
             }
-            const int e0 = b0 >= 0 ? (s0 >> 8) - 127 : -1000, e1 = b1 >= 0 ? (s1 >> 8) - 127 : -1000;
-            const int e = max(e0, e1);
-            if (__ballot(raise) != 0 || e > E) {
-                const float down = e > E ? power_of_two(E - e) : 1.0f;
+            if (__ballot(raise) != 0) {
 #pragma unroll
                 for (int n = 0; n < NR; n++) {
                     const bool up = top[n] > m[n] + ATT_RAISE;
-                    const float alpha = up ? __builtin_amdgcn_exp2f(m[n] - top[n]) : 1.0f, beta = alpha * down;
+                    const float alpha = up ? __builtin_amdgcn_exp2f(m[n] - top[n]) : 1.0f;
+                    const float beta = alpha * power_of_two(min(E[n] - seen[n], 0));
                     if (up) m[n] = top[n];
-                    l[n] *= alpha;
+                    l[n] *= alpha, E[n] = max(E[n], seen[n]);
 #pragma unroll
                     for (int c = 0; c < C; c++)
 #pragma unroll
@@ -369,12 +384,12 @@ __global__ __launch_bounds__(64 * STREAM_WAVES) void attend_stream_kernel(Attend
 #pragma unroll
                             for (int r = 0; r < 4; r++) o[n][c][x][r] *= beta;
                 }
-                E = max(E, e);
             }
             uint32_t p[NR][4][2];
 #pragma unroll
             for (int n = 0; n < NR; n++) {
                 const float base = (m[n] > -INFINITY ? m[n] : 0.0f) - ATT_LIFT;
+                const _Float16 unit = half_power(min(e - E[n], 0));
 #pragma unroll
                 for (int x = 0; x < 4; x++)
 #pragma unroll
@@ -382,16 +397,16 @@ __global__ __launch_bounds__(64 * STREAM_WAVES) void attend_stream_kernel(Attend
                         p[n][x][r] = f16_pair(__builtin_amdgcn_exp2f(__builtin_fmaf(st[n][x][2 * r], f, -base)),
                                               __builtin_amdgcn_exp2f(__builtin_fmaf(st[n][x][2 * r + 1], f, -base)));
                         l[n] = add_pair(p[n][x][r], l[n]);
+                        p[n][x][r] = scale_pair(p[n][x][r], unit);
                     }
             }
-            const float unit = power_of_two((have ? (mine >> 8) - 127 : -1000) - E);
 #pragma unroll
             for (int c = 0; c < C; c++)
 #pragma unroll
                 for (int x = 0; x < 2; x++)
 #pragma unroll
                     for (int i = 0; i < 2; i++) {
-                        const v4u v = widen_e4m3<false>(vr[c][x][i], vr[c][x][2 + i], unit);
+                        const v4u v = widen_e4m3<false>(vr[c][x][i], vr[c][x][2 + i], 1.0f);
 #pragma unroll
                         for (int n = 0; n < NR; n++)
                             o[n][c][x] = mfma_16x16x32<false>(
@@ -404,15 +419,16 @@ __global__ __launch_bounds__(64 * STREAM_WAVES) void attend_stream_kernel(Attend
 #pragma unroll
         for (int n = 0; n < NR; n++) {
             l[n] = over_groups(l[n], Sum{});
-            if (g == 0) mls[wave][16 * n + t16][0] = m[n], mls[wave][16 * n + t16][1] = l[n];
+            if (g == 0) mls[wave][16 * n + t16][0] = m[n], mls[wave][16 * n + t16][1] = l[n], es[wave][16 * n + t16] = E[n];
         }
         __syncthreads();
 #pragma unroll
         for (int n = 0; n < NR; n++) {
             float M = -INFINITY;
+            int top = E[n];
 #pragma unroll
-            for (int w = 0; w < STREAM_WAVES; w++) M = fmaxf(M, mls[w][16 * n + t16][0]);
-            const float alpha = m[n] > -INFINITY ? __builtin_amdgcn_exp2f(m[n] - M) : 0.0f;
+            for (int w = 0; w < STREAM_WAVES; w++) M = fmaxf(M, mls[w][16 * n + t16][0]), top = max(top, es[w][16 * n + t16]);
+            const float alpha = (m[n] > -INFINITY ? __builtin_amdgcn_exp2f(m[n] - M) : 0.0f) * power_of_two(E[n] - top);
             if (16 * n + t16 < rows) {
 #pragma unroll
                 for (int c = 0; c < C; c++)
@@ -420,7 +436,7 @@ __global__ __launch_bounds__(64 * STREAM_WAVES) void attend_stream_kernel(Attend
                     for (int x = 0; x < 2; x++) {
                         v4f y = o[n][c][x];
 #pragma unroll
-                        for (int r = 0; r < 4; r++) y[r] = ldexpf(y[r] * alpha, E);
+                        for (int r = 0; r < 4; r++) y[r] *= alpha;
                         *reinterpret_cast<v4f *>(sums + (wave * R + 16 * n + t16) * PITCH + 32 * c + 16 * x + 4 * g) = y;
                     }
             }
@@ -430,14 +446,18 @@ __global__ __launch_bounds__(64 * STREAM_WAVES) void attend_stream_kernel(Attend
         for (int at = tid; at < rows * (D / 4); at += 64 * STREAM_WAVES) {
             const int r = at / (D / 4), d = at % (D / 4) * 4;
             float M = -INFINITY, total = 0.0f;
+            int top = -1000;
 #pragma unroll
-            for (int w = 0; w < STREAM_WAVES; w++) M = fmaxf(M, mls[w][r][0]);
+            for (int w = 0; w < STREAM_WAVES; w++) M = fmaxf(M, mls[w][r][0]), top = max(top, es[w][r]);
 #pragma unroll
             for (int w = 0; w < STREAM_WAVES; w++)
                 total += mls[w][r][0] > -INFINITY ? __builtin_amdgcn_exp2f(mls[w][r][0] - M) * mls[w][r][1] : mls[w][r][1];
             v4f y = {0, 0, 0, 0};
 #pragma unroll
             for (int w = 0; w < STREAM_WAVES; w++) y += *reinterpret_cast<const v4f *>(sums + (w * R + r) * PITCH + d);
+            const float inv = inverse(total);
+#pragma unroll
+            for (int i = 0; i < 4; i++) y[i] = ldexpf(y[i] * inv, top);
             if (!done) {
                 *reinterpret_cast<v4f *>(a.part + (slot * R + r) * D + d) = y;
                 if (d == 0) a.part_ml[(slot * R + r) * 2] = M, a.part_ml[(slot * R + r) * 2 + 1] = total;
@@ -501,9 +521,11 @@ __global__ __launch_bounds__(64 * STREAM_WAVES) void attend_join_kernel(AttendAr
     __syncthreads();
     m = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
     const float f = ml.x > -INFINITY ? __builtin_amdgcn_exp2f(ml.x - m) : 1.0f;
-    if (tid < count) factors[tid] = f;
     float total = wave_sum32(tid < count ? f * ml.y : 0.0f);
     if (lane == 0) weights[wave] = total;
+    __syncthreads();
+    total = (weights[0] + weights[1]) + (weights[2] + weights[3]);
+    if (tid < count) factors[tid] = f * ml.y * inverse(total);
     __syncthreads();
     // 4 channels a lane: a load of a wave holds 256 / D workers' rows
     constexpr int LANES = D / 4, SIDE = 256 / LANES;
@@ -516,7 +538,6 @@ __global__ __launch_bounds__(64 * STREAM_WAVES) void attend_join_kernel(AttendAr
     if (tid >= LANES) return;
 #pragma unroll
     for (int i = 1; i < SIDE; i++) y += sums[i][tid];
-    total = (weights[0] + weights[1]) + (weights[2] + weights[3]);
     row_out(a, s.row, tile * R + row, head, m, total, tid == 0).store(d, y);
 }
 
@@ -561,7 +582,7 @@ struct AttTile {
     static constexpr int RING = SB * BLOCK_BYTES > 49152 ? 2 : 3;                // stages in LDS
     static constexpr int LOADS = SB * BLOCK_BYTES / 1024 / WAVES;                // of a wave and stage
     static constexpr int STAGE_BYTES = SB * BLOCK_BYTES, RING_BYTES = RING * STAGE_BYTES;
-    static constexpr int JOIN_BYTES = TW > 1 ? 4 * 32 * D * 4 + WAVES * (64 * 8 + 4) : 0;  // half of the waves' sums, maxima and exponents
+    static constexpr int JOIN_BYTES = TW > 1 ? 4 * 32 * D * 4 + WAVES * 64 * 12 : 0;  // half of the waves' sums, maxima and exponents
     static constexpr int LDS = RING_BYTES > JOIN_BYTES ? RING_BYTES : JOIN_BYTES;
     static_assert(SB % TW == 0 && 64 % SB == 0 && LOADS >= 1 && LOADS * WAVES * 1024 == SB * BLOCK_BYTES && LDS <= 163840, "");
 };
@@ -759,31 +780,33 @@ __global__ __launch_bounds__(C::THREADS, C::EU_WAVES) void attend_tile_kernel(At
             top = over_halves(top * f, Larger{});
             const bool up = top > m + ATT_RAISE;
             const int e = (scale >> 8 & 255) - 127;
-            if (__ballot(up) != 0 || e > E) {
-                const float alpha = up ? __builtin_amdgcn_exp2f(m - top) : 1.0f, beta = alpha * (e > E ? power_of_two(E - e) : 1.0f);
+            const bool grow = e > E && top > -INFINITY;  // only what the row sees
+            if (__ballot(up || grow) != 0) {
+                const float alpha = up ? __builtin_amdgcn_exp2f(m - top) : 1.0f, beta = alpha * (grow ? power_of_two(E - e) : 1.0f);
                 if (up) m = top;
-                l *= alpha, E = max(E, e);
+                if (grow) E = e;
+                l *= alpha;
 #pragma unroll
                 for (int c = 0; c < N; c++)
 #pragma unroll
                     for (int v = 0; v < 16; v++) o[c][v] *= beta;
             }
             const float base = (m > -INFINITY ? m : 0.0f) - ATT_LIFT;
+            const _Float16 unit = half_power(min(e - E, 0));
             v4u w[2];
 #pragma unroll
             for (int v = 0; v < 8; v++) {
                 const uint32_t x = f16_pair(__builtin_amdgcn_exp2f(__builtin_fmaf(t[2 * v], f, -base)),
                                             __builtin_amdgcn_exp2f(__builtin_fmaf(t[2 * v + 1], f, -base)));
-                w[v / 4][v % 4] = x;
+                w[v / 4][v % 4] = scale_pair(x, unit);
                 l = add_pair(x, l);
             }
-            const float unit = power_of_two(e - E);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int c = 0; c < N; c++) {
                 const v4u x = *reinterpret_cast<const v4u *>(p + 32 * D + c * 1024);
-                o[c] = mfma_32x32x16_f16(widen_e4m3<false>(x[0], x[2], unit), w[0], o[c]);
-                o[c] = mfma_32x32x16_f16(widen_e4m3<false>(x[1], x[3], unit), w[1], o[c]);
+                o[c] = mfma_32x32x16_f16(widen_e4m3<false>(x[0], x[2], 1.0f), w[0], o[c]);
+                o[c] = mfma_32x32x16_f16(widen_e4m3<false>(x[1], x[3], 1.0f), w[1], o[c]);
             }
             att_interleave<N>();
             __builtin_amdgcn_sched_barrier(0);
@@ -807,7 +830,7 @@ __global__ __launch_bounds__(C::THREADS, C::EU_WAVES) void attend_tile_kernel(At
             const int other = wave ^ (half * C::RW);
             __syncthreads();
             mls[wave * 64 + lane] = v2f{m, l};
-            if (lane == 0) es[wave] = E;
+            es[wave * 64 + lane] = E;
             if (upper) {
 #pragma unroll
                 for (int z = 0; z < n; z++) sums[(wave * n + z) * 64 + lane] = quad(z);
@@ -817,7 +840,7 @@ __global__ __launch_bounds__(C::THREADS, C::EU_WAVES) void attend_tile_kernel(At
             }
             __syncthreads();
             const v2f ml = mls[other * 64 + lane];
-            const int e = __builtin_amdgcn_readfirstlane(es[other]), eb = max(e, E);
+            const int e = es[other * 64 + lane], eb = max(e, E);
             const float mb = fmaxf(m, ml.x);
             const float own = m > -INFINITY ? __builtin_amdgcn_exp2f(m - mb) : 1.0f, theirs = ml.x > -INFINITY ? __builtin_amdgcn_exp2f(ml.x - mb) : 1.0f;
             const float fo = own * power_of_two(E - eb), fe = theirs * power_of_two(e - eb);
@@ -836,14 +859,15 @@ __global__ __launch_bounds__(C::THREADS, C::EU_WAVES) void attend_tile_kernel(At
     const bool first = tw == 0 && h == 0;
     if (a.splits > 1) {
         if (first) a.part_ml[slot * 2] = m, a.part_ml[slot * 2 + 1] = l;
-        if (E == -1000) return;  // no block: never read
+        if (m == -INFINITY && l == 0.0f) return;  // nothing seen: never read
     }
     const RowOut out = row_out(a, s.row, r, head, m, l, first && a.splits == 1);
+    const float inv = inverse(l);
 #pragma unroll
     for (int z = 0; z < QUADS; z++) {
         v4f y;
 #pragma unroll
-        for (int i = 0; i < 4; i++) y[i] = ldexpf(o[z / 4][z % 4 * 4 + i], E);
+        for (int i = 0; i < 4; i++) y[i] = ldexpf(o[z / 4][z % 4 * 4 + i] * inv, E);
         const int d = (base + z) * 8 + 4 * h;
         if (a.splits > 1) *reinterpret_cast<v4f *>(a.part + slot * D + d) = y;
         else out.store(d, y);
@@ -875,7 +899,7 @@ __global__ __launch_bounds__(256) void attend_splits_kernel(AttendArgs a) {
     const float m = wave_larger(own.x), f = own.x > -INFINITY ? __builtin_amdgcn_exp2f(own.x - m) : 1.0f;
     const float total = wave_sum32(f * own.y);
     // a split without tokens wrote no sums: whatever lies there is not taken
-    if (lane < a.splits) factors[wave][lane] = own.x > -INFINITY || own.y != 0.0f ? f : -1.0f;
+    if (lane < a.splits) factors[wave][lane] = own.x > -INFINITY || own.y != 0.0f ? f * own.y * inverse(total) : -1.0f;
     __syncthreads();
     const int at = threadIdx.x % ROW_THREADS, d = at % LANES * 4, side = at / LANES;
     v4f y = {0, 0, 0, 0};
@@ -883,7 +907,7 @@ __global__ __launch_bounds__(256) void attend_splits_kernel(AttendArgs a) {
     for (int i = side; i < a.splits; i += SIDE) {
         const v4f x = *reinterpret_cast<const v4f *>(a.part + (slot0 + (int64_t)i * ROWS) * D + d);
         const float fi = factors[wave][i];
-        y = fi >= 0.0f ? y + fi * x : y;
+        y = fi != -1.0f ? y + fi * x : y;
     }
     sums[of][side][at % LANES] = y;
     __syncthreads();

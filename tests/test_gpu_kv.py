@@ -290,6 +290,40 @@ def test_scales_far_apart():
         check_attention(q, codes, scales, pages, starts, lens)
 
 
+# q heads, heads, rows, tokens, window: which kernels run is test_every_plan's matter
+UNSEEN = [(2, 2, 14, 100, 0), (2, 1, 16, 1284, 0), (6, 2, 5, 99, 32), (4, 1, 8, 2597, 31), (20, 1, 70, 99, 0),
+          (20, 1, 40, 1300, 46), (64, 64, 70, 100, 0), (32, 4, 300, 999, 100),
+          (1, 1, 700, 2600, 64), (20, 1, 300, 2600, 0), (32, 4, 530, 2000, 0)]
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("q_heads,heads,rows,tokens,window", UNSEEN)
+def test_values_that_only_other_rows_see(q_heads, heads, rows, tokens, window, dim):
+    """The largest values in the last block, which the last rows alone see, and with a
+    window in one that only the first do: not a bit changes in the others.  Of the
+    scales 2^118 and 2^120, codes of 448 on the second are 2^128.8, past the 2^128 that
+    fp32 and bf16 hold: the rows that see those have no value to compare with."""
+    q, codes, scales, pages, starts, lens = small_case(n=rows, tokens=tokens, dim=dim, heads=heads, group=q_heads // heads, page=64,
+                                                      dt=torch.bfloat16)
+    args = dict(window=window)
+    clean = check_attention(q, codes, scales, pages, starts, lens, **args)
+    at = tokens - rows + np.arange(rows)
+    last, first = (tokens - 1) // 32, max(tokens - rows - window + 1, 0) // 32
+    same, edge = at < last * 32, bool(window) and first < last - 1
+    if edge:
+        same &= at - window >= first * 32 + 31
+    assert same.any() and not same.all()
+    for e in (118, 120):
+        scales[pages[0, last // 2], :, last % 2, 1] = 127 + e
+        if edge:
+            scales[pages[0, first // 2], :, first % 2, 1] = 127 + e
+        if e == 118:
+            got = check_attention(q, codes, scales, pages, starts, lens, **args)
+        else:
+            got = ops.attention_kv(q, gpu(codes), gpu(scales), gpu(pages), gpu(starts), gpu(lens), **args).float().cpu().numpy()
+        assert np.array_equal(got[same], clean[same])
+
+
 def test_queries_of_any_size():
     """Rows of zeros, of fp16's largest and least values, of an infinity and of NaN."""
     q, codes, scales, pages, starts, lens = small_case(n=6, dim=64)
