@@ -104,13 +104,16 @@ Plan plan_of(int64_t rows, int64_t seqs, int64_t q_heads, int64_t heads, int64_t
         // a wave's step 1.3 us at D = 256, 0.9 at 128, 0.6 at 64; 5 TB/s with all CUs at work;
         // start and end 8, or 13 with a join, and 0.03 a task joined.  Sequences of other
         // lengths than the longest cost the first kind more than this knows: 14 us or less is
-        // taken as it is, and a quarter more than the second.
+        // taken as it is, and a quarter more than the second, up to 512 tasks.  With those the
+        // CUs have more than one each and even out by themselves: 66 sequences of up to 8192
+        // tokens (8 heads of 256) 217 us, shared 243; 160 (8 of 64) 141 and 211; 50 of up to
+        // 16384 (8 of 128), 400 tasks, 173 shared.
         const double bytes_us = (double)(std::min(rows, seqs) * tokens * heads * 2 * dim) / 5e6;
         const double step_us = (dim == 256 ? 1.3 : dim == 128 ? 0.9 : 0.6) * (p.rows == 32 ? 1.6 : 1.0);
         const double rounds = (double)((tasks + 256 * (512 / dim) - 1) / (256 * (512 / dim)));
         const double whole = 8 + std::max(rounds * std::ceil((double)steps / STREAM_WAVES) * step_us, bytes_us);
         const double shared = 13 + bytes_us + 0.03 * (double)tasks;
-        if (steps > STREAM_LEAST && whole > 14 && shared < 1.25 * whole)
+        if (steps > STREAM_LEAST && whole > 14 && shared < (tasks >= 512 ? 1.0 : 1.25) * whole)
             p.workers = std::min<int64_t>(STREAM_WORKERS, tasks * (steps / STREAM_LEAST + 1));
         return p;
     }

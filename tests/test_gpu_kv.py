@@ -241,6 +241,27 @@ def test_every_plan(plan, sizes, dim):
         check_attention(q, codes, scales, pages, starts, np.array([t for _, t in seqs], np.int32), window=100, causal=dim != 64)
 
 
+MIXED = [[(1, 2000), (1, 1), (70, 1400), (0, 300), (1, 700), (1, 2111), (100, 60), (2, 1999)],
+         [(200, 2100)] + [(1, 100 + 150 * i) for i in range(14)]]
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("seqs", MIXED)
+@pytest.mark.parametrize("mask", [(True, 0), (True, 70), (True, 1), (True, 1300), (False, 0), (False, 1300)])
+def test_prompts_beside_single_tokens(seqs, mask, dim):
+    """Sequences of many tiles among those of one, all shared by the same workgroups."""
+    heads, group, page = 2, 1, 64
+    rng = np.random.default_rng([dim, len(seqs)])
+    per = [-(-t // page) for _, t in seqs]
+    rows, pool = sum(n for n, _ in seqs), sum(per) + 1
+    assert "stream" in ops.attention_kv_plan(rows, len(seqs), heads * group, heads, dim, max(per) * page)
+    codes, scales = filled(rng, pool, page, heads, dim)
+    codes[..., 0, :] = rng.choice(codes.reshape(-1)[codes.reshape(-1) & 127 < 60], codes[..., 0, :].shape)
+    q = torch.from_numpy(rng.standard_normal((rows, heads * group, dim))).to(DEV, torch.bfloat16)
+    check_attention(q, codes, scales, page_table(rng, per, pool), np.cumsum([0] + [n for n, _ in seqs]).astype(np.int32),
+                    np.array([t for _, t in seqs], np.int32), causal=mask[0], window=mask[1])
+
+
 def small_case(seed=0, dt=torch.float16, dim=128, n=5, tokens=100, heads=2, group=3, page=32):
     rng = np.random.default_rng(seed)
     pool = -(-tokens // page) + 1
