@@ -210,7 +210,7 @@ w4a4_status w4a4_append_kv(w4a4_dtype dt, const w4a4_head_rows *k, const w4a4_he
     if ((q_weight || k_weight) && (!(eps > 0.0) || !std::isfinite(eps))) return W4A4_ERR_INVALID_VALUE;
     if (rope) {
         if (rope->width <= 0 || rope->width > dim || rope->width % 16 || rope->table_rows < 0 || rope->table_rows > kMax31 ||
-            (rope->axes && (!rope->positions || rope->n_axes < 1 || rope->n_axes > 256)) || (!rope->axes && rope->n_axes > 1) ||
+            (rope->axes && (!rope->positions || rope->n_axes > 256)) || (rope->positions && rope->n_axes < 1) || (!rope->axes && rope->n_axes > 1) ||
             (rope->positions && rope->axes && rope->n_axes > 1 && rope->ld < rows) || rope->ld < 0)
             return W4A4_ERR_INVALID_VALUE;
     }

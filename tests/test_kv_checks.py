@@ -140,6 +140,13 @@ def test_append_refusals(L):
     assert append(L, q_heads=8192, batch=dict(rows=2097120)) == INVALID
 
 
+def test_positions_of_no_axis_are_refused(L):
+    """As with axes: every pair would turn by NaN."""
+    for n in (0, -1):
+        assert append(L, rope=dict(positions=A, n_axes=n)) == INVALID
+    assert append(L, rope=dict(positions=A, n_axes=1), batch=NOTHING) == OK and append(L, rope=dict(n_axes=0), batch=NOTHING) == OK
+
+
 def test_attention_refusals(L):
     long = dict(pages_per_seq=4096, ld=4096)
     for bad in (dict(q=None), dict(out=None), dict(q_heads=6), dict(q_heads=0), dict(q_heads=2), dict(scale=0.0), dict(scale=-1.0),
