@@ -13,10 +13,10 @@
 // it would be one E for all rows of a wave, and one that not all of them may see.)
 //
 // One row of 131072 tokens (24 heads over 4 of 256, 268 MB) takes 59 us, 4.5 TB/s; 32
-// sequences of up to 16384 (48 over 8 of 128, 683 MB) 132, 5.2 TB/s: memory, where a
-// copy reaches 4.9.  512 rows of 32768 tokens take 405 us, 1010 TFLOP/s at D = 256, and
-// of 8192 144, 690, at D = 128, where a large product reaches 1200: a block's 32 x 32
-// scores cost a wave the same 75 vector instructions and 16 exponentials whatever D,
+// sequences of up to 16384 (48 over 8 of 128, 683 MB) 133, 5.1 TB/s: memory, where a
+// copy reaches 4.9.  512 rows of 32768 tokens take 400 to 408 us, 1010 TFLOP/s at D = 256,
+// and of 8192 148, 680, at D = 128, where a large product reaches 1200: a block's 32 x 32
+// scores cost a wave the same 85 vector instructions and 16 exponentials whatever D,
 // and its keys and values D / 2 conversions, beside D / 8 products.
 //
 // m is raised only where a tile's maximum passes it by over RAISE: accumulators are
@@ -82,7 +82,7 @@ __device__ __forceinline__ v4f mfma_16x16x32(v4u a, v4u b, v4f c) {
 __device__ __forceinline__ uint32_t f16_pair(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{a, b}), v2h));
 }
-// Two fp16 values times 2^e, e <= 0.
+// Two fp16 values times f; 2^e.
 __device__ __forceinline__ uint32_t scale_pair(uint32_t x, _Float16 f) { return __builtin_bit_cast(uint32_t, __builtin_bit_cast(v2h, x) * v2h{f, f}); }
 __device__ __forceinline__ _Float16 half_power(int e) { return (_Float16)ldexpf(1.0f, e); }
 // c + the sum of two fp16 values.
@@ -214,7 +214,7 @@ __device__ __forceinline__ int64_t workers_used(int64_t steps, int workers) {
 // g holds the tokens of block g / 2 and half g % 2 as the value pieces have them.
 // A wave asks for a step's 128 D bytes at once, 16 contiguous bytes a lane: with 4 waves
 // a CU 128 KB in flight at D = 256, and no faster with 8 or 16.  Short sequences are a
-// chain of latencies (lengths, page, codes, two steps, the waves' sums): 300 tokens 8.6 us.
+// chain of latencies (lengths, page, codes, two steps, the waves' sums): 300 tokens 8.9 us.
 template <int D, bool BF16, int NR>
 __global__ __launch_bounds__(64 * STREAM_WAVES) void attend_stream_kernel(AttendArgs a) {
     constexpr int R = 16 * NR, J = D / 64, C = D / 32, PITCH = D + 4;
@@ -883,7 +883,7 @@ constexpr int SPLITS_MOST = 32;
 
 // The rows of a tile that `splits` workgroups had the tokens of, WAVES waves a row:
 // one where the splits are few, four where the loads of many would follow each
-// other (16 splits of 96 rows: 6 us against 9).
+// other (16 splits of 96 rows: 4.7 us against 8.4).
 template <int D, int ROWS, int WAVES>
 __global__ __launch_bounds__(256) void attend_splits_kernel(AttendArgs a) {
     constexpr int LANES = D / 4, SIDE = 64 * WAVES / LANES, ROW_THREADS = 64 * WAVES, TOGETHER = 4 / WAVES;

@@ -22,7 +22,7 @@
 //
 // What bounds these kernels: memory for many tokens (8 prompts of up to 1023 tokens,
 // 32 + 2 x 4 heads of 128, three axes, 94 MB: 31 us, 3.0 TB/s; the vector issue of
-// norm and rotation keeps it from a copy's 4.9; without them 19 us), and for a decode
+// norm and rotation keeps it from a copy's 4.9: the queries copied alone take 19), and for a decode
 // step the chain of dependent loads: lengths, page, scale (one token 5.8 us, 64
 // sequences' 6.0; the norm's sum and the table's row cost 1 us each of it).
 #pragma once
@@ -456,7 +456,8 @@ __device__ __forceinline__ void append_block(const AppendArgs &a, int id, uint8_
 
 // The queries of a row: D / 8 lanes a head, a wave's heads from one row, so that
 // cosines, sines and weights are loaded once for a.q_passes steps of 64 / LANES
-// heads (5156 rows of 32 heads of 128: 46 us with one step a wave, 38 with eight).
+// heads (5156 rows of 32 heads of 128: 99 us before that and without loads ahead, 46 with
+// both, 31 with the pairs exchanged between lanes and one table row a lane).
 template <int D>
 __device__ __forceinline__ void append_queries(const AppendArgs &a, int id) {
     constexpr int LANES = D / 8, HEADS = 64 / LANES, AHEAD = 4;
