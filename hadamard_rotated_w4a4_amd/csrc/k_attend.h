@@ -38,6 +38,11 @@ typedef __bf16 v8b __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 
 constexpr float ATT_RAISE = 8.0f, ATT_LIFT = 6.0f;  // powers of two
+// A row's exponents t f - m + LIFT come from one fused step up to this |m - LIFT|: what m's
+// rounding took is then 2^-4 at most.  From |m| of 2^24 on it would carry weights over
+// fp16's range, or all of a row's below it; past this bound products are rounded as m
+// was, and m is taken from them before LIFT comes to it: the largest is 2^LIFT exactly.
+constexpr float ATT_FAR = 1048576.0f;
 
 struct AttendArgs {
     const uint8_t *q;
@@ -372,12 +377,12 @@ __global__ __launch_bounds__(64 * STREAM_WAVES) void attend_stream_kernel(Attend
                 const int own = t > -INFINITY ? e : -1000;
                 top[n] = over_halves(t, Larger{});
                 seen[n] = (int)swap32((uint32_t)own, [](uint32_t x, uint32_t y) { return (uint32_t)max((int)x, (int)y); });
-                raise |= top[n] > m[n] + ATT_RAISE || seen[n] > E[n];
+                raise |= top[n] - m[n] > ATT_RAISE || seen[n] > E[n];
             }
             if (__ballot(raise) != 0) {
 #pragma unroll
                 for (int n = 0; n < NR; n++) {
-                    const bool up = top[n] > m[n] + ATT_RAISE;
+                    const bool up = top[n] - m[n] > ATT_RAISE;
                     const float alpha = up ? __builtin_amdgcn_exp2f(m[n] - top[n]) : 1.0f;
                     const float beta = alpha * power_of_two(min(E[n] - seen[n], 0));
                     if (up) m[n] = top[n];
@@ -393,14 +398,22 @@ __global__ __launch_bounds__(64 * STREAM_WAVES) void attend_stream_kernel(Attend
             uint32_t p[NR][4][2];
 #pragma unroll
             for (int n = 0; n < NR; n++) {
-                const float base = (m[n] > -INFINITY ? m[n] : 0.0f) - ATT_LIFT;
+                float base = (m[n] > -INFINITY ? m[n] : 0.0f) - ATT_LIFT, by = f;
                 const _Float16 unit = half_power(min(e - E[n], 0));
+                if (__ballot(fabsf(base) > ATT_FAR) != 0) {
+                    const bool far = fabsf(base) > ATT_FAR;
+#pragma unroll
+                    for (int x = 0; x < 4; x++)
+#pragma unroll
+                        for (int r = 0; r < 4; r++) st[n][x][r] = far ? st[n][x][r] * f - m[n] : st[n][x][r];
+                    base = far ? -ATT_LIFT : base, by = far ? 1.0f : by;
+                }
 #pragma unroll
                 for (int x = 0; x < 4; x++)
 #pragma unroll
                     for (int r = 0; r < 2; r++) {
-                        p[n][x][r] = f16_pair(__builtin_amdgcn_exp2f(__builtin_fmaf(st[n][x][2 * r], f, -base)),
-                                              __builtin_amdgcn_exp2f(__builtin_fmaf(st[n][x][2 * r + 1], f, -base)));
+                        p[n][x][r] = f16_pair(__builtin_amdgcn_exp2f(__builtin_fmaf(st[n][x][2 * r], by, -base)),
+                                              __builtin_amdgcn_exp2f(__builtin_fmaf(st[n][x][2 * r + 1], by, -base)));
                         l[n] = add_pair(p[n][x][r], l[n]);
                         p[n][x][r] = scale_pair(p[n][x][r], unit);
                     }
@@ -783,7 +796,7 @@ __global__ __launch_bounds__(C::THREADS, C::EU_WAVES) void attend_tile_kernel(At
 #pragma unroll
             for (int v = 1; v < 16; v++) top = fmaxf(top, t[v]);
             top = over_halves(top * f, Larger{});
-            const bool up = top > m + ATT_RAISE;
+            const bool up = top - m > ATT_RAISE;
             const int e = (scale >> 8 & 255) - 127;
             const bool grow = e > E && top > -INFINITY;  // only what the row sees
             if (__ballot(up || grow) != 0) {
@@ -796,13 +809,19 @@ __global__ __launch_bounds__(C::THREADS, C::EU_WAVES) void attend_tile_kernel(At
 #pragma unroll
                     for (int v = 0; v < 16; v++) o[c][v] *= beta;
             }
-            const float base = (m > -INFINITY ? m : 0.0f) - ATT_LIFT;
+            float base = (m > -INFINITY ? m : 0.0f) - ATT_LIFT, by = f;
             const _Float16 unit = half_power(min(e - E, 0));
+            if (__ballot(fabsf(base) > ATT_FAR) != 0) {
+                const bool far = fabsf(base) > ATT_FAR;
+#pragma unroll
+                for (int v = 0; v < 16; v++) t[v] = far ? t[v] * f - m : t[v];
+                base = far ? -ATT_LIFT : base, by = far ? 1.0f : by;
+            }
             v4u w[2];
 #pragma unroll
             for (int v = 0; v < 8; v++) {
-                const uint32_t x = f16_pair(__builtin_amdgcn_exp2f(__builtin_fmaf(t[2 * v], f, -base)),
-                                            __builtin_amdgcn_exp2f(__builtin_fmaf(t[2 * v + 1], f, -base)));
+                const uint32_t x = f16_pair(__builtin_amdgcn_exp2f(__builtin_fmaf(t[2 * v], by, -base)),
+                                            __builtin_amdgcn_exp2f(__builtin_fmaf(t[2 * v + 1], by, -base)));
                 w[v / 4][v % 4] = scale_pair(x, unit);
                 l = add_pair(x, l);
             }
