@@ -8,9 +8,9 @@
 // instruction, two a lane.  The keys' scale goes into the factor of the exponent.
 // p is rounded to fp16 (11 bits, as the output's own type or better), and summed as
 // rounded, so that a row's weights add up to one.  The values' scale goes into the
-// weights then, relative to the largest one that the row has seen so far, 2^E, and 2^E
-// at the end: a power of two, exact but below 2^-14.  (Applied by the values' conversion
-// it would be one E for all rows of a wave, and one that not all of them may see.)
+// weights then, relative to a power of two of each row, 2^E (below), and 2^E at the end:
+// exact but below 2^-14.  (Applied by the values' conversion it would be one E for all
+// rows of a wave, and one that not all of them may see.)
 //
 // One row of 131072 tokens (24 heads over 4 of 256, 268 MB) takes 59 us, 4.5 TB/s; 32
 // sequences of up to 16384 (48 over 8 of 128, 683 MB) 133, 5.1 TB/s: memory, where a
@@ -43,6 +43,24 @@ constexpr float ATT_RAISE = 8.0f, ATT_LIFT = 6.0f;  // powers of two
 // fp16's range, or all of a row's below it; past this bound products are rounded as m
 // was, and m is taken from them before LIFT comes to it: the largest is 2^LIFT exactly.
 constexpr float ATT_FAR = 1048576.0f;
+
+// Weighted values are summed in units of 2^E, E whole, of each row.  What a block adds is
+// of the size of its value scale 2^e times its largest weight, and E follows the largest
+// size of what the row has seen (where m rises, all before get smaller), and not the
+// largest scale: beside one whose weights are almost nothing, others would lose their
+// bits.  Weights of a scale up to 2^ABOVE over the unit are multiplied by the ratio, as those
+// below it; further ones get it in the exponent, and are summed for themselves.  E stays
+// where it is up to SPARE over what it could be, so that blocks of nearly one scale raise
+// it seldom.  A weight times its scale is off by 2^-24 of the largest size at most:
+// fp16's half step, 2^-25, times 2^ABOVE, 2^(SPARE + 1), over 2^LIFT.
+constexpr float ATT_ABOVE = 4.0f, ATT_SPARE = 2.0f, ATT_NEVER = -2000.0f;
+constexpr float ATT_UNSEEN = 1000.0f;  // E of a row that has seen nothing
+// x <= 0, an exponent, up to the next whole number; NaN (neither has seen anything) as NEVER.
+__device__ __forceinline__ float att_whole(float x) { return ceilf(fmaxf(x, ATT_NEVER)); }
+// The least E for a block of scale 2^e and largest score top, and where E may stay if it holds m.
+__device__ __forceinline__ float att_size(float E, float e, float top, float m) {
+    return fmaxf(e + att_whole(fminf(top - m, 0.0f)), top >= m && E <= e + ATT_SPARE ? E : ATT_NEVER);
+}
 
 struct AttendArgs {
     const uint8_t *q;
@@ -87,14 +105,13 @@ __device__ __forceinline__ v4f mfma_16x16x32(v4u a, v4u b, v4f c) {
 __device__ __forceinline__ uint32_t f16_pair(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{a, b}), v2h));
 }
-// Two fp16 values times f; 2^e.
+// Two fp16 values times f; 2^e, e whole.
 __device__ __forceinline__ uint32_t scale_pair(uint32_t x, _Float16 f) { return __builtin_bit_cast(uint32_t, __builtin_bit_cast(v2h, x) * v2h{f, f}); }
-__device__ __forceinline__ _Float16 half_power(int e) { return (_Float16)ldexpf(1.0f, e); }
-// c + the sum of two fp16 values.
-__device__ __forceinline__ float add_pair(uint32_t x, float c) {
-    return __builtin_amdgcn_fdot2(__builtin_bit_cast(v2h, x), v2h{(_Float16)1.0f, (_Float16)1.0f}, c, false);
+__device__ __forceinline__ _Float16 half_power(float e) { return (_Float16)ldexpf(1.0f, (int)e); }
+// c + the sum of two fp16 values, times f.
+__device__ __forceinline__ float add_pair(uint32_t x, _Float16 f, float c) {
+    return __builtin_amdgcn_fdot2(__builtin_bit_cast(v2h, x), v2h{f, f}, c, false);
 }
-__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(min(max(e, -126), 127) + 127) << 23); }
 
 // x over the lanes l and l ^ 32; l and l ^ 16; l, l ^ 16, l ^ 32 and l ^ 48.
 template <class F>
@@ -225,7 +242,8 @@ __global__ __launch_bounds__(64 * STREAM_WAVES) void attend_stream_kernel(Attend
     constexpr int R = 16 * NR, J = D / 64, C = D / 32, PITCH = D + 4;
     __shared__ __align__(16) float sums[STREAM_WAVES * R * PITCH];
     __shared__ float mls[STREAM_WAVES][R][2];
-    __shared__ int es[STREAM_WAVES][R];
+    __shared__ float es[STREAM_WAVES][R];
+    __shared__ __align__(16) v4f stats[R];  // of all waves: maximum, sum, its inverse, exponent
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid / 64);
     const int t16 = lane & 15, g = lane >> 4, page_tokens = a.pool.per_page * KV_BLOCK, heads = a.pool.heads;
 
@@ -284,10 +302,10 @@ __global__ __launch_bounds__(64 * STREAM_WAVES) void attend_stream_kernel(Attend
 
         float m[NR], l[NR];
         v4f o[NR][C][2];
-        int E[NR];
+        float E[NR];
 #pragma unroll
         for (int n = 0; n < NR; n++) {
-            m[n] = -INFINITY, l[n] = 0.0f, E[n] = -1000;
+            m[n] = -INFINITY, l[n] = 0.0f, E[n] = ATT_UNSEEN;
 #pragma unroll
             for (int c = 0; c < C; c++) o[n][c][0] = o[n][c][1] = v4f{0, 0, 0, 0};
         }
@@ -362,9 +380,8 @@ __global__ __launch_bounds__(64 * STREAM_WAVES) void attend_stream_kernel(Attend
                 }
             }
 
-            const int e = have ? (mine >> 8) - 127 : -1000;  // of this lane's tokens' values
-            float top[NR];
-            int seen[NR];  // the larger of the step's exponents that a row sees
+            const float e = have ? (float)((mine >> 8) - 127) : ATT_NEVER;  // of this lane's tokens' values
+            float top[NR], own_top[NR];  // of the step's two blocks, and of this lane's
             bool raise = false;
 #pragma unroll
             for (int n = 0; n < NR; n++) {
@@ -374,19 +391,18 @@ __global__ __launch_bounds__(64 * STREAM_WAVES) void attend_stream_kernel(Attend
 #pragma unroll
                     for (int r = 0; r < 4; r++) t = fmaxf(t, st[n][x][r]);
                 t = over_pairs(t * f, Larger{});
-                const int own = t > -INFINITY ? e : -1000;
-                top[n] = over_halves(t, Larger{});
-                seen[n] = (int)swap32((uint32_t)own, [](uint32_t x, uint32_t y) { return (uint32_t)max((int)x, (int)y); });
-                raise |= top[n] - m[n] > ATT_RAISE || seen[n] > E[n];
+                own_top[n] = t, top[n] = over_halves(t, Larger{});
+                raise |= top[n] - m[n] > ATT_RAISE || (E[n] < e && t - m[n] > E[n] - e);
             }
             if (__ballot(raise) != 0) {
 #pragma unroll
                 for (int n = 0; n < NR; n++) {
                     const bool up = top[n] - m[n] > ATT_RAISE;
-                    const float alpha = up ? __builtin_amdgcn_exp2f(m[n] - top[n]) : 1.0f;
-                    const float beta = alpha * power_of_two(min(E[n] - seen[n], 0));
+                    const float fall = up ? m[n] - top[n] : 0.0f, was = E[n];
                     if (up) m[n] = top[n];
-                    l[n] *= alpha, E[n] = max(E[n], seen[n]);
+                    E[n] = fmaxf(E[n] + att_whole(fall), over_halves(att_size(E[n], e, own_top[n], m[n]), Larger{}));
+                    const float beta = __builtin_amdgcn_exp2f(fall + (was - E[n]));
+                    l[n] *= __builtin_amdgcn_exp2f(fall);
 #pragma unroll
                     for (int c = 0; c < C; c++)
 #pragma unroll
@@ -399,22 +415,31 @@ __global__ __launch_bounds__(64 * STREAM_WAVES) void attend_stream_kernel(Attend
 #pragma unroll
             for (int n = 0; n < NR; n++) {
                 float base = (m[n] > -INFINITY ? m[n] : 0.0f) - ATT_LIFT, by = f;
-                const _Float16 unit = half_power(min(e - E[n], 0));
-                if (__ballot(fabsf(base) > ATT_FAR) != 0) {
+                float shift = e - E[n];
+                _Float16 counted = (_Float16)1.0f;
+                if (__ballot(fabsf(base) > ATT_FAR || shift > ATT_ABOVE) != 0) {
                     const bool far = fabsf(base) > ATT_FAR;
 #pragma unroll
                     for (int x = 0; x < 4; x++)
 #pragma unroll
                         for (int r = 0; r < 4; r++) st[n][x][r] = far ? st[n][x][r] * f - m[n] : st[n][x][r];
                     base = far ? -ATT_LIFT : base, by = far ? 1.0f : by;
+                    if (shift > ATT_ABOVE) {
+#pragma unroll
+                        for (int x = 0; x < 4; x++)
+#pragma unroll
+                            for (int r = 0; r < 4; r++) l[n] += __builtin_amdgcn_exp2f(__builtin_fmaf(st[n][x][r], by, -base));
+                        base -= shift, shift = 0.0f, counted = (_Float16)0.0f;
+                    }
                 }
+                const _Float16 unit = half_power(shift);
 #pragma unroll
                 for (int x = 0; x < 4; x++)
 #pragma unroll
                     for (int r = 0; r < 2; r++) {
                         p[n][x][r] = f16_pair(__builtin_amdgcn_exp2f(__builtin_fmaf(st[n][x][2 * r], by, -base)),
                                               __builtin_amdgcn_exp2f(__builtin_fmaf(st[n][x][2 * r + 1], by, -base)));
-                        l[n] = add_pair(p[n][x][r], l[n]);
+                        l[n] = add_pair(p[n][x][r], counted, l[n]);
                         p[n][x][r] = scale_pair(p[n][x][r], unit);
                     }
             }
@@ -442,11 +467,17 @@ __global__ __launch_bounds__(64 * STREAM_WAVES) void attend_stream_kernel(Attend
         __syncthreads();
 #pragma unroll
         for (int n = 0; n < NR; n++) {
-            float M = -INFINITY;
-            int top = E[n];
+            float M = -INFINITY, top = 2 * ATT_NEVER, total = 0.0f;
 #pragma unroll
-            for (int w = 0; w < STREAM_WAVES; w++) M = fmaxf(M, mls[w][16 * n + t16][0]), top = max(top, es[w][16 * n + t16]);
-            const float alpha = (m[n] > -INFINITY ? __builtin_amdgcn_exp2f(m[n] - M) : 0.0f) * power_of_two(E[n] - top);
+            for (int w = 0; w < STREAM_WAVES; w++) M = fmaxf(M, mls[w][16 * n + t16][0]);
+#pragma unroll
+            for (int w = 0; w < STREAM_WAVES; w++) {
+                const float below = mls[w][16 * n + t16][0] - M;  // NaN where a wave has seen nothing
+                top = fmaxf(top, es[w][16 * n + t16] + att_whole(below));
+                total += mls[w][16 * n + t16][0] > -INFINITY ? __builtin_amdgcn_exp2f(below) * mls[w][16 * n + t16][1] : mls[w][16 * n + t16][1];
+            }
+            if (wave == 0 && g == 0) stats[16 * n + t16] = v4f{M, total, inverse(total), top};
+            const float alpha = m[n] > -INFINITY ? __builtin_amdgcn_exp2f(m[n] - M + (E[n] - top)) : 0.0f;
             if (16 * n + t16 < rows) {
 #pragma unroll
                 for (int c = 0; c < C; c++)
@@ -463,19 +494,13 @@ __global__ __launch_bounds__(64 * STREAM_WAVES) void attend_stream_kernel(Attend
         const int64_t slot = 2 * (int64_t)blockIdx.x + (step == 0 ? 1 : 0);  // of a tile begun here, or before
         for (int at = tid; at < rows * (D / 4); at += 64 * STREAM_WAVES) {
             const int r = at / (D / 4), d = at % (D / 4) * 4;
-            float M = -INFINITY, total = 0.0f;
-            int top = -1000;
-#pragma unroll
-            for (int w = 0; w < STREAM_WAVES; w++) M = fmaxf(M, mls[w][r][0]), top = max(top, es[w][r]);
-#pragma unroll
-            for (int w = 0; w < STREAM_WAVES; w++)
-                total += mls[w][r][0] > -INFINITY ? __builtin_amdgcn_exp2f(mls[w][r][0] - M) * mls[w][r][1] : mls[w][r][1];
+            const v4f of = stats[r];
+            const float M = of[0], total = of[1];
             v4f y = {0, 0, 0, 0};
 #pragma unroll
             for (int w = 0; w < STREAM_WAVES; w++) y += *reinterpret_cast<const v4f *>(sums + (w * R + r) * PITCH + d);
-            const float inv = inverse(total);
 #pragma unroll
-            for (int i = 0; i < 4; i++) y[i] = ldexpf(y[i] * inv, top);
+            for (int i = 0; i < 4; i++) y[i] = ldexpf(y[i] * of[2], (int)of[3]);
             if (!done) {
                 *reinterpret_cast<v4f *>(a.part + (slot * R + r) * D + d) = y;
                 if (d == 0) a.part_ml[(slot * R + r) * 2] = M, a.part_ml[(slot * R + r) * 2 + 1] = total;
@@ -702,7 +727,7 @@ __global__ __launch_bounds__(C::THREADS, C::EU_WAVES) void attend_tile_kernel(At
     };
 
     float m = -INFINITY, l = 0.0f;
-    int E = -1000;
+    float E = ATT_UNSEEN;
     v16f o[N];
 #pragma unroll
     for (int c = 0; c < N; c++) o[c] = v16f{};
@@ -797,33 +822,41 @@ __global__ __launch_bounds__(C::THREADS, C::EU_WAVES) void attend_tile_kernel(At
             for (int v = 1; v < 16; v++) top = fmaxf(top, t[v]);
             top = over_halves(top * f, Larger{});
             const bool up = top - m > ATT_RAISE;
-            const int e = (scale >> 8 & 255) - 127;
-            const bool grow = e > E && top > -INFINITY;  // only what the row sees
+            const float e = (float)((scale >> 8 & 255) - 127);
+            const bool grow = E < e && top - m > E - e;  // of what the row sees
             if (__ballot(up || grow) != 0) {
-                const float alpha = up ? __builtin_amdgcn_exp2f(m - top) : 1.0f, beta = alpha * (grow ? power_of_two(E - e) : 1.0f);
+                const float fall = up ? m - top : 0.0f, was = E;
                 if (up) m = top;
-                if (grow) E = e;
-                l *= alpha;
+                E = fmaxf(E + att_whole(fall), att_size(E, e, top, m));
+                const float beta = __builtin_amdgcn_exp2f(fall + (was - E));
+                l *= __builtin_amdgcn_exp2f(fall);
 #pragma unroll
                 for (int c = 0; c < N; c++)
 #pragma unroll
                     for (int v = 0; v < 16; v++) o[c][v] *= beta;
             }
             float base = (m > -INFINITY ? m : 0.0f) - ATT_LIFT, by = f;
-            const _Float16 unit = half_power(min(e - E, 0));
-            if (__ballot(fabsf(base) > ATT_FAR) != 0) {
+            float shift = e - E;
+            _Float16 counted = (_Float16)1.0f;
+            if (__ballot(fabsf(base) > ATT_FAR || shift > ATT_ABOVE) != 0) {
                 const bool far = fabsf(base) > ATT_FAR;
 #pragma unroll
                 for (int v = 0; v < 16; v++) t[v] = far ? t[v] * f - m : t[v];
                 base = far ? -ATT_LIFT : base, by = far ? 1.0f : by;
+                if (shift > ATT_ABOVE) {
+#pragma unroll
+                    for (int v = 0; v < 16; v++) l += __builtin_amdgcn_exp2f(__builtin_fmaf(t[v], by, -base));
+                    base -= shift, shift = 0.0f, counted = (_Float16)0.0f;
+                }
             }
+            const _Float16 unit = half_power(shift);
             v4u w[2];
 #pragma unroll
             for (int v = 0; v < 8; v++) {
                 const uint32_t x = f16_pair(__builtin_amdgcn_exp2f(__builtin_fmaf(t[2 * v], by, -base)),
                                             __builtin_amdgcn_exp2f(__builtin_fmaf(t[2 * v + 1], by, -base)));
                 w[v / 4][v % 4] = scale_pair(x, unit);
-                l = add_pair(x, l);
+                l = add_pair(x, counted, l);
             }
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -846,7 +879,7 @@ __global__ __launch_bounds__(C::THREADS, C::EU_WAVES) void attend_tile_kernel(At
     if constexpr (C::TW > 1) {
         v4f *sums = reinterpret_cast<v4f *>(smem);  // [wave][quad][64 lanes]
         v2f *mls = reinterpret_cast<v2f *>(smem + 4 * 32 * D * 4);
-        int *es = reinterpret_cast<int *>(smem + 4 * 32 * D * 4 + C::WAVES * 64 * 8);
+        float *es = reinterpret_cast<float *>(smem + 4 * 32 * D * 4 + C::WAVES * 64 * 8);
         auto quad = [&](int z) { return v4f{o[z / 4][z % 4 * 4], o[z / 4][z % 4 * 4 + 1], o[z / 4][z % 4 * 4 + 2], o[z / 4][z % 4 * 4 + 3]}; };
 #pragma unroll
         for (int half = C::TW / 2, n = 2 * N; half > 0; half /= 2, n /= 2) {  // n: quads kept, and given
@@ -864,10 +897,11 @@ __global__ __launch_bounds__(C::THREADS, C::EU_WAVES) void attend_tile_kernel(At
             }
             __syncthreads();
             const v2f ml = mls[other * 64 + lane];
-            const int e = es[other * 64 + lane], eb = max(e, E);
             const float mb = fmaxf(m, ml.x);
+            const float e = es[other * 64 + lane], eb = fmaxf(E + att_whole(m - mb), e + att_whole(ml.x - mb));
             const float own = m > -INFINITY ? __builtin_amdgcn_exp2f(m - mb) : 1.0f, theirs = ml.x > -INFINITY ? __builtin_amdgcn_exp2f(ml.x - mb) : 1.0f;
-            const float fo = own * power_of_two(E - eb), fe = theirs * power_of_two(e - eb);
+            const float fo = m > -INFINITY ? __builtin_amdgcn_exp2f(m - mb + (E - eb)) : 1.0f;
+            const float fe = ml.x > -INFINITY ? __builtin_amdgcn_exp2f(ml.x - mb + (e - eb)) : 1.0f;
             l = l * own + ml.y * theirs, m = mb, E = eb;
             if (upper) base += n;
 #pragma unroll
@@ -891,7 +925,7 @@ __global__ __launch_bounds__(C::THREADS, C::EU_WAVES) void attend_tile_kernel(At
     for (int z = 0; z < QUADS; z++) {
         v4f y;
 #pragma unroll
-        for (int i = 0; i < 4; i++) y[i] = ldexpf(o[z / 4][z % 4 * 4 + i] * inv, E);
+        for (int i = 0; i < 4; i++) y[i] = ldexpf(o[z / 4][z % 4 * 4 + i] * inv, (int)E);
         const int d = (base + z) * 8 + 4 * h;
         if (a.splits > 1) *reinterpret_cast<v4f *>(a.part + slot * D + d) = y;
         else out.store(d, y);

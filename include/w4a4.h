@@ -765,9 +765,11 @@ w4a4_status w4a4_read_kv(const w4a4_kv_cache *cache, const w4a4_kv_batch *batch,
  * lens[b] that have a page, with j <= p if causal, and j > p - window if window > 0:
  *   s_j = scale sum_i q_i k_ji,  out = sum_j e^(s_j) v_j / sum_j e^(s_j)
  * and lse = log sum_j e^(s_j).  A row that sees nothing, or only scores of minus
- * infinity, gets zeros and lse minus infinity.  Products are summed in fp32; weights are
- * rounded to fp16, the largest between 2^6 and 2^14, and times their block's value scale
- * over the largest that the row has seen to a step of 2^-24 at least.  Tokens that a row does not see do not reach it, whatever they hold
+ * infinity, gets zeros and lse minus infinity.  Products are summed in fp32, and scores past
+ * its range have no value.  Weights are rounded to fp16, the largest between 2^6 and 2^14;
+ * times its block's value scale a weight is off by 2^-24 more at most of the largest of
+ * the products, of a block's value scale and its largest weight, that the row has seen.
+ * Tokens that a row does not see do not reach it, whatever they hold
  * (value codes are taken to hold no NaN, and w4a4_append_kv writes none).
  *   q     [rows][q_heads][dim] of type dt, fp16 or bf16.
  *   out   [rows][q_heads][dim] of type odt, fp16 or bf16; may be q (odt == dt, same

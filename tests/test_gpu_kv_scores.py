@@ -88,3 +88,57 @@ def test_large_scores_of_any_kind(size):
         assert (np.isneginf(lse) == ~some).all(), plan
         # within a rounding of the largest, a score more: at most all of the tokens
         assert (off(lse, wlse)[some] <= 2.0 ** -23 * (64 + 8) * reach[some] + np.log(lens.max()) + 1).all(), plan
+
+
+# code of a key's first channel (times a query's 8, over sqrt(dim): 62 to 68, or 20 to 22), for each dim
+FAR, NEAR = {64: 64.0, 128: 96.0, 256: 128.0}, {64: 20.0, 128: 30.0, 256: 44.0}
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("plan,sizes", PLANS)
+@pytest.mark.parametrize("first,power", [(FAR, 30), (NEAR, 30), (FAR, -30)], ids=["no weight", "their share", "all the weight"])
+def test_blocks_of_other_value_scales(first, power, plan, sizes, dim):
+    """A third of a sequence's blocks have values 2^30 times the others', and weights of
+    e^-62 and less, or of about e^-21 (2^-30: what they add is of the others' size); or
+    2^-30 of the others' size and all the weight.  What counts keeps its bits: what a token
+    adds is off by 2^-24 at most of the largest scale times its block's largest weight, and
+    not of the largest scale."""
+    q_heads, heads, seqs = sizes
+    rng, pages, codes, scales, starts, lens = plan_case(plan, sizes, dim, 3)
+    dt = torch.float16 if dim == 128 else torch.bfloat16
+    keys = rng.choice(np.arange(256)[np.arange(256) & 127 < 60], (*codes.shape[:3], 32, dim)).astype(np.uint8)
+    keys[..., 0] = 0
+    put(codes, 0, keys, dim)
+    plain = codes.copy()  # the same without what sets blocks apart: what roundings of scores are measured by
+    chosen = np.full(len(seqs), 1 << 30)  # a sequence's first such block
+    sign = -1 if power > 0 else 1
+    code = int(np.argmin(np.abs(twin.E4M3[:127] - first[dim]))) | (128 if sign < 0 else 0)
+    for b, (_, tokens) in enumerate(seqs):
+        for blk in range(1, -(-tokens // 32)):
+            if rng.random() < 0.34:
+                at = pages[b, blk // 2], slice(None), blk % 2
+                keys[at][..., 0] = code
+                only = keys[at].copy()
+                only[..., 1:] = 0
+                codes[at][:, 0][:, twin.bytes_of(0, dim).reshape(-1)] = only.reshape(heads, -1)
+                scales[at] = np.array([127, int(scales[at][0, 1]) + power], np.uint8)
+                chosen[b] = min(chosen[b], blk)
+    rows = int(starts[-1])
+    queries = rng.standard_normal((rows, q_heads, dim))
+    queries[..., 0] = 8.0
+    q = torch.from_numpy(queries).to(DEV, dt)
+    exact = q.float().cpu().numpy()
+    want, wlse, spread, _ = twin.attention(exact, codes, scales, pages, starts, lens, dim ** -0.5)
+    reach = twin.attention(exact, plain, np.where(scales == 127, 122, scales), pages, starts, lens, dim ** -0.5)[3]
+    got, lse = run(q, codes, scales, pages, starts, lens)
+    s = sign * first[dim] * 8 * dim ** -0.5
+    unit = np.zeros((rows, 1, 1))  # the largest scale times its block's largest weight, of each row
+    for b, row0, n, at, _ in twin.rows_of(starts, lens, pages.shape[1] * 64, rows):
+        sees = np.arange(at, at + n) >= 32 * chosen[b]
+        unit[row0:row0 + n, 0, 0] = np.where(sees, max(2.0 ** -5 * np.exp(min(-s, 0)), 2.0 ** (power - 5) * np.exp(min(s, 0))) * np.e, 2.0 ** -5)
+    bound = tolerance(spread, want, reach, int(lens.max()), dim, dt) + 448 * unit * 2.0 ** -24 * int(lens.max())
+    assert (np.abs(got - want) <= bound).all(), (np.abs(got - want) / bound).max()
+    some = ~np.isneginf(wlse)
+    assert (np.isneginf(lse) == ~some).all()
+    step = 2.0 ** -11 + 2.0 ** -23 * (dim + 8) * (reach + abs(s) + 16) + 2.0 ** -22 * (np.abs(np.where(some, wlse, 0)) + 16)
+    assert (off(lse, wlse) <= step)[some].all()
