@@ -44,6 +44,11 @@ constexpr float ATT_RAISE = 8.0f, ATT_LIFT = 6.0f;  // powers of two
 // was, and m is taken from them before LIFT comes to it: the largest is 2^LIFT exactly.
 constexpr float ATT_FAR = 1048576.0f;
 
+// Scores are the products' sums t times f = 2^k scale log2(e), k their keys' exponent.  Where
+// f itself is no normal number, 2^k and the rest come one after the other: the scores may
+// be ordinary for all that, and a factor of 0 is no mask (0 times -infinity).
+__device__ __forceinline__ bool att_normal(float f) { return f >= 1.17549435e-38f && f < INFINITY; }
+
 // Weighted values are summed in units of 2^E, E whole, of each row.  What a block adds is
 // of the size of its value scale 2^e times its largest weight, and E follows the largest
 // size of what the row has seen (where m rises, all before get smaller), and not the
@@ -338,8 +343,7 @@ __global__ __launch_bounds__(64 * STREAM_WAVES) void attend_stream_kernel(Attend
 
             const int mine = g & 2 ? s1 : s0, token = (pair0 + u) * STREAM_PAIR + (g & 2 ? 32 : 0) + (g & 1) * 4;
             const bool have = (g & 2 ? b1 : b0) >= 0;
-            // the score's factor; never 0, for -infinity times 0 is no mask
-            const float f = fmaxf(ldexpf(a.scale_log2, (mine & 255) - 127), 1.17549435e-38f);
+            float f = ldexpf(a.scale_log2, (mine & 255) - 127);
 
             // subtile x = 2 i + q holds tokens 16 i + 8 q + 4 h + r
             v4f st[NR][4];
@@ -359,7 +363,8 @@ __global__ __launch_bounds__(64 * STREAM_WAVES) void attend_stream_kernel(Attend
             }
             const int tokens0 = (pair0 + u) * STREAM_PAIR;
             const bool whole = b0 >= 0 && b1 >= 0 && tokens0 + STREAM_PAIR <= s.len;
-            if (!whole || tokens0 < every_lo || tokens0 + STREAM_PAIR > every_hi) {
+            if (!whole || tokens0 < every_lo || tokens0 + STREAM_PAIR > every_hi || __ballot(!att_normal(f)) != 0) {
+                const bool apart = !att_normal(f);
 #pragma unroll
                 for (int n = 0; n < NR; n++)
 #pragma unroll
@@ -367,8 +372,10 @@ __global__ __launch_bounds__(64 * STREAM_WAVES) void attend_stream_kernel(Attend
 #pragma unroll
                         for (int r = 0; r < 4; r++) {
                             const int t = token + 8 * x + r;
+                            if (apart) st[n][x][r] = ldexpf(st[n][x][r], (mine & 255) - 127) * a.scale_log2;
                             if (!have || t < row_lo[n] || t >= row_hi[n]) st[n][x][r] = -INFINITY;
                         }
+                f = apart ? 1.0f : f;
             }
             if (!whole) {  // nothing but zeros where there is no token
                 const int t0 = tokens0 + (g & 2 ? 32 : 0), in = have ? min(max(s.len - t0, 0), KV_BLOCK) : 0;
@@ -682,7 +689,7 @@ __global__ __launch_bounds__(C::THREADS, C::EU_WAVES) void attend_tile_kernel(At
     const int every_hi = wrows ? span_of(a, s, wrow0, wrow0 + 1).hi : 0;
 
     // lane i, for block i of 64 of this workgroup's: where it lies, and its scales (16
-    // bits, and EDGE where not every row sees all of it), or -1 where this wave has
+    // bits, and EDGE where not every row sees all of it or its factor is not normal), or -1 where this wave has
     // nothing to do.  One read of a lane a block then, not a dozen scalar operations.
     constexpr int EDGE = 1 << 16;
     int held_block = -1, held_info = -1, held_chunk = 0;
@@ -698,7 +705,7 @@ __global__ __launch_bounds__(C::THREADS, C::EU_WAVES) void attend_tile_kernel(At
         const int token = (block0 + held_chunk * 64 + lane) * KV_BLOCK;
         const bool some = held_block >= 0 && token + KV_BLOCK > wspan.lo && token < wspan.hi;
         held_info = some ? reinterpret_cast<const uint16_t *>(a.pool.scales)[held_block] : -1;
-        if (some && (token < every_lo || token + KV_BLOCK > every_hi)) held_info |= EDGE;
+        if (some && (token < every_lo || token + KV_BLOCK > every_hi || !att_normal(ldexpf(a.scale_log2, (held_info & 255) - 127)))) held_info |= EDGE;
     };
     fetch_block(0);  // first: all that follows waits for the pages
 
@@ -808,8 +815,13 @@ __global__ __launch_bounds__(C::THREADS, C::EU_WAVES) void attend_tile_kernel(At
             att_interleave<N>();
             __builtin_amdgcn_sched_barrier(0);
             ask(std::integral_constant<int, 1>{});
-            const float f = fmaxf(ldexpf(a.scale_log2, (scale & 255) - 127), 1.17549435e-38f);  // never 0: -infinity stays
+            float f = ldexpf(a.scale_log2, (scale & 255) - 127);
             if (scale & EDGE) {
+                if (!att_normal(f)) {
+#pragma unroll
+                    for (int v = 0; v < 16; v++) t[v] = ldexpf(t[v], (scale & 255) - 127) * a.scale_log2;
+                    f = 1.0f;
+                }
                 const int token = (block0 + first + j) * KV_BLOCK;
 #pragma unroll
                 for (int v = 0; v < 16; v++) {

@@ -142,3 +142,27 @@ def test_blocks_of_other_value_scales(first, power, plan, sizes, dim):
     assert (np.isneginf(lse) == ~some).all()
     step = 2.0 ** -11 + 2.0 ** -23 * (dim + 8) * (reach + abs(s) + 16) + 2.0 ** -22 * (np.abs(np.where(some, wlse, 0)) + 16)
     assert (off(lse, wlse) <= step)[some].all()
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("plan,sizes", PLANS)
+def test_factors_past_fp32s_normal_range(plan, sizes, dim):
+    """A block's key scale times the call's scale below 2^-126, under bf16 queries of 2^122
+    (scores of about 0.1, 2^-127 a key); past 2^128, where queries of zeros still see every
+    token alike; and a scale that fp32 has only zero for."""
+    q_heads, heads, _ = sizes
+    rng, pages, codes, scales, starts, lens = plan_case(plan, sizes, dim, 4)
+    keys = rng.choice(np.arange(256)[np.arange(256) & 127 < 60], (*codes.shape[:3], 32, dim)).astype(np.uint8)
+    put(codes, 0, keys, dim)
+    rows, length = int(starts[-1]), int(lens.max())
+    ordinary = rng.standard_normal((rows, q_heads, dim))
+    for queries, key_scales, scale in ((ordinary * 2.0 ** 122, (0, 3), dim ** -0.5), (0 * ordinary, (240, 247), 1e5), (ordinary, (100, 127), 1e-60)):
+        scales[..., 0] = rng.integers(*key_scales, scales[..., 0].shape)
+        q = torch.from_numpy(queries).to(DEV, torch.bfloat16)
+        want, wlse, spread, reach = twin.attention(q.float().cpu().numpy(), codes, scales, pages, starts, lens, scale)
+        got, lse = run(q, codes, scales, pages, starts, lens, scale=scale)
+        bound = tolerance(spread, want, reach, length, dim, torch.bfloat16) + 448 * 2.0 ** -5 * 2.0 ** -24 * length
+        assert (np.abs(got - want) <= bound).all(), (scale, (np.abs(got - want) / bound).max())
+        some = ~np.isneginf(wlse)
+        assert (np.isneginf(lse) == ~some).all()
+        assert (off(lse, wlse) <= 2.0 ** -11 + 2.0 ** -23 * (dim + 8) * (reach + 16) + 2.0 ** -22 * (np.abs(np.where(some, wlse, 0)) + 16))[some].all()
