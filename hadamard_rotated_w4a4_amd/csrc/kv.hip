@@ -148,7 +148,7 @@ size_t workspace_of(const Plan &p, int64_t heads, int64_t dim) {
 // With a window a tile's rows see fewer tokens; the workspace is as the sizes alone have it.
 Plan plan_of(int64_t rows, int64_t seqs, int64_t q_heads, int64_t heads, int64_t dim, int64_t tokens, int64_t window) {
     const Plan all = plan_of(rows, seqs, q_heads, heads, dim, tokens);
-    if (!window) return all;
+    if (!window || window >= tokens) return all;
     const Plan less = plan_of(rows, seqs, q_heads, heads, dim, std::min(tokens, window + 3 * KV_BLOCK));
     return workspace_of(less, heads, dim) <= workspace_of(all, heads, dim) ? less : all;
 }
