@@ -773,7 +773,7 @@ def new_kv_cache(pages: int, page: int, heads: int, dim: int, device) -> tuple[t
     """An empty pool of `pages` pages of `page` tokens for `heads` key/value heads
     of width `dim`: codes uint8 [pages, heads, page/32, 2, 32 dim], scales uint8
     [pages, heads, page/32, 2] (include/w4a4.h has the layout)."""
-    if pages and not lib().w4a4_kv_cache_code_bytes(pages, page, heads, dim):
+    if not lib().w4a4_kv_cache_code_bytes(pages or 1, page, heads, dim):  # of no pages: 0 bytes, whatever their size
         raise W4A4Error(f"no cache of {pages} pages of {page} tokens, {heads} heads of {dim}")
     return (torch.zeros((pages, heads, page // 32, 2, 32 * dim), dtype=torch.uint8, device=device),
             torch.zeros((pages, heads, page // 32, 2), dtype=torch.uint8, device=device))
