@@ -824,6 +824,7 @@ def attention_kv(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, pag
     """Attention of q (fp16 or bf16 [rows, q_heads, dim]) over the cache, the rows
     being each sequence's last tokens (starts, lens as in append_kv); scale 1 /
     sqrt(dim) unless given.  Returns [rows, q_heads, dim] of `dtype` (fp16 or bf16;
-    out's type, or q's); lse (fp32 [rows, q_heads]) is written where given."""
+    out's type, or q's); lse (fp32 [rows, q_heads]) is written where given.  A call is
+    planned for all of pages: pages[:, :n] is faster where n are enough."""
     return (_native_module or _native()).attention_kv(q, codes, scales, pages, starts, lens, scale, causal, window, out, lse,
                                                       workspace, dtype)

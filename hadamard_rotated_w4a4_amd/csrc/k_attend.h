@@ -12,12 +12,15 @@
 // exact but below 2^-14.  (Applied by the values' conversion it would be one E for all
 // rows of a wave, and one that not all of them may see.)
 //
-// One row of 131072 tokens (24 heads over 4 of 256, 268 MB) takes 59 us, 4.5 TB/s; 32
+// One row of 131072 tokens (24 heads over 4 of 256, 268 MB) takes 58 us, 4.6 TB/s; 32
 // sequences of up to 16384 (48 over 8 of 128, 683 MB) 133, 5.1 TB/s: memory, where a
-// copy reaches 4.9.  512 rows of 32768 tokens take 400 to 408 us, 1010 TFLOP/s at D = 256,
-// and of 8192 148, 680, at D = 128, where a large product reaches 1200: a block's 32 x 32
-// scores cost a wave the same 85 vector instructions and 16 exponentials whatever D,
-// and its keys and values D / 2 conversions, beside D / 8 products.
+// copy reaches 4.9.  512 rows of 32768 tokens take 375 to 411 us (with the card's clock),
+// 1.0 to 1.1 PFLOP/s, at D = 256, and of 8192 151, 660 TFLOP/s, at D = 128, where a large
+// product reaches 1200.  A block's 32 x 32 scores cost a wave the same 90 vector instructions
+// and 16 exponentials whatever D, and its keys and values D / 2 conversions, beside D / 8
+// products, and these hardly overlap: at D = 128 the vector units are 40 % and the matrix
+// cores 24 % busy (192 workgroups; 53 and 32 % on the CUs that have one), at D = 64 71 and
+// 28 %, at D = 256 50 and 42 %.
 //
 // m is raised only where a tile's maximum passes it by over RAISE: accumulators are
 // rescaled seldom.  Weights carry a factor 2^LIFT: at most 2^(LIFT + RAISE) < 65504,
@@ -212,8 +215,9 @@ constexpr int STREAM_WORKERS = 256;                          // at most: a threa
 __device__ __forceinline__ int steps_over(const Span &x) { return x.hi <= x.lo ? 0 : (x.hi + STREAM_PAIR - 1) / STREAM_PAIR - x.lo / STREAM_PAIR; }
 // Steps that count for a tile of a sequence of n > 0 rows: one number for all of them,
 // at least what each takes, so that any can be found without the others (a prompt of 512
-// rows beside 255 single ones, 8 x 8 heads of 128: 700 us, and 2130 where every workgroup
-// and row summed the tiles before its own).
+// rows beside 255 single ones, 8 x 8 heads of 128, shared: 700 us, and 2130 where every
+// workgroup and row summed the tiles before its own; its 4000 tasks are not shared
+// any more, 452).
 template <int R>
 __device__ __forceinline__ int steps_each(const AttendArgs &a, const KvSeq &s) {
     int steps = steps_over(span_of(a, s, 0, s.n * a.group));
@@ -241,7 +245,7 @@ __device__ __forceinline__ int64_t workers_used(int64_t steps, int workers) {
 // g holds the tokens of block g / 2 and half g % 2 as the value pieces have them.
 // A wave asks for a step's 128 D bytes at once, 16 contiguous bytes a lane: with 4 waves
 // a CU 128 KB in flight at D = 256, and no faster with 8 or 16.  Short sequences are a
-// chain of latencies (lengths, page, codes, two steps, the waves' sums): 300 tokens 8.9 us.
+// chain of latencies (lengths, page, codes, two steps, the waves' sums): 300 tokens 8.6 us.
 template <int D, bool BF16, int NR>
 __global__ __launch_bounds__(64 * STREAM_WAVES) void attend_stream_kernel(AttendArgs a) {
     constexpr int R = 16 * NR, J = D / 64, C = D / 32, PITCH = D + 4;

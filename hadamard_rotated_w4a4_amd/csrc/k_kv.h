@@ -20,11 +20,13 @@
 // rounded again on the coarser grid, which is exact but for values below
 // 2^-6 of a code.  (A grid of 8-bit integers would lose half a step every time.)
 //
-// What bounds these kernels: memory for many tokens (8 prompts of up to 1023 tokens,
-// 32 + 2 x 4 heads of 128, three axes, 94 MB: 31 us, 3.0 TB/s; the vector issue of
-// norm and rotation keeps it from a copy's 4.9: the queries copied alone take 19), and for a decode
-// step the chain of dependent loads: lengths, page, scale (one token 5.8 us, 64
-// sequences' 6.0; the norm's sum and the table's row cost 1 us each of it).
+// What bounds these kernels.  Many tokens (8 prompts of up to 1023 tokens, 32 + 2 x 4 heads of
+// 128, three axes, 94 MB): 31 us, 3.0 TB/s, where a copy reaches 4.9 and the queries copied
+// alone take 19; vector instructions (norm, rotation, codes) issue for half of the time, and
+// waves wait for their loads for half of theirs: neither alone.  A prompt of 512 (10 us) has
+// a fifth of its time in vector instructions: the chain below, in 68 workgroups for its
+// blocks.  A decode step is the chain of dependent loads: lengths, page, scale (one token
+// 5.8 us, 64 sequences' 6.0; the norm's sum and the table's row cost 1 us each of it).
 #pragma once
 
 #include "common.h"

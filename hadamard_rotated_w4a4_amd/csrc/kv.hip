@@ -106,8 +106,8 @@ Plan plan_of(int64_t rows, int64_t seqs, int64_t q_heads, int64_t heads, int64_t
         // lengths than the longest cost the first kind more than this knows: 14 us or less is
         // taken as it is, and a quarter more than the second, up to 512 tasks.  With those the
         // CUs have more than one each and even out by themselves: 66 sequences of up to 8192
-        // tokens (8 heads of 256) 217 us, shared 243; 160 (8 of 64) 141 and 211; 50 of up to
-        // 16384 (8 of 128), 400 tasks, 173 shared.
+        // tokens (8 heads of 256) 218 us, shared 243; 160 (8 of 64) 144 and 211; 50 of up to
+        // 16384 (8 of 128), 400 tasks, 177 shared.
         const double bytes_us = (double)(std::min(rows, seqs) * tokens * heads * 2 * dim) / 5e6;
         const double step_us = (dim == 256 ? 1.3 : dim == 128 ? 0.9 : 0.6) * (p.rows == 32 ? 1.6 : 1.0);
         const double rounds = (double)((tasks + 256 * (512 / dim) - 1) / (256 * (512 / dim)));

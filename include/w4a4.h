@@ -741,7 +741,8 @@ size_t w4a4_kv_cache_scale_bytes(int64_t pages, int64_t page, int64_t heads, int
  *   q_weight, k_weight  [dim] fp32 or NULL; 4-byte aligned.
  *   eps       > 0, finite (read only where there is a weight).
  *   rope      NULL: no rotation.
- * Two sequences of a call may not write one block.
+ * No two blocks that a call writes may be one (of two sequences, or of one that names a
+ * page twice).
  * Errors: an unknown type, or odt fp32 -> W4A4_ERR_UNSUPPORTED_DTYPE; sizes past
  * the bounds, a dim or page as above, a bad stride, width, eps or table, null
  * pointers with work to do -> W4A4_ERR_INVALID_VALUE; misalignment ->
@@ -780,6 +781,11 @@ w4a4_status w4a4_read_kv(const w4a4_kv_cache *cache, const w4a4_kv_batch *batch,
  *         pages_per_seq * page) bytes, 256-byte aligned (may be NULL when that is 0);
  *         contents on entry are ignored, calls that share one must not overlap,
  *         replays of captured calls among them.
+ * A call is planned for pages_per_seq * page tokens a sequence, since lens is on the
+ * device: for longer ones than there are it takes more workspace and launches (512 rows
+ * of 512 tokens, 24 heads over 4 of 256: 21 us with as many pages as tokens, 36 with
+ * pages for 8192 and 61 for 131072; one row of 300 9 and 19).  Where the longest length is known,
+ * pages_per_seq may say it, with ld as it is.
  * The result of a row does not depend on the other sequences of the call but for
  * the order of its fp32 sums, which is fixed for a call's sizes and lens.
  *
