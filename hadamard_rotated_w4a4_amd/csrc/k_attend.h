@@ -60,7 +60,8 @@ __device__ __forceinline__ bool att_normal(float f) { return f >= 1.17549435e-38
 // below it; further ones get it in the exponent, and are summed for themselves.  E stays
 // where it is up to SPARE over what it could be, so that blocks of nearly one scale raise
 // it seldom.  A weight times its scale is off by 2^-24 of the largest size at most:
-// fp16's half step, 2^-25, times 2^ABOVE, 2^(SPARE + 1), over 2^LIFT.
+// fp16's half step, 2^-25, times 2^ABOVE, 2^(SPARE + 1), over 2^LIFT.  (Sums are joined by
+// fp32 factors, which end at 2^-126: weights below 2^(RAISE - 126) may be lost with them.)
 constexpr float ATT_ABOVE = 4.0f, ATT_SPARE = 2.0f, ATT_NEVER = -2000.0f;
 constexpr float ATT_UNSEEN = 1000.0f;  // E of a row that has seen nothing
 // x <= 0, an exponent, up to the next whole number; NaN (neither has seen anything) as NEVER.

@@ -770,6 +770,7 @@ w4a4_status w4a4_read_kv(const w4a4_kv_cache *cache, const w4a4_kv_batch *batch,
  * its range have no value.  Weights are rounded to fp16, the largest between 2^6 and 2^14;
  * times its block's value scale a weight is off by 2^-24 more at most of the largest of
  * the products, of a block's value scale and its largest weight, that the row has seen.
+ * Weights below 2^-118 of a row's largest may count as zeros, whatever their values.
  * Tokens that a row does not see do not reach it, whatever they hold
  * (value codes are taken to hold no NaN, and w4a4_append_kv writes none).
  *   q     [rows][q_heads][dim] of type dt, fp16 or bf16.
